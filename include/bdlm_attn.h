@@ -364,6 +364,101 @@ bdlm_status bdlm_attn_bwd_varlen(const void* Qc, const void* Kc, const void* Vc,
                                  bdlm_dtype g_dtype, void* workspace, size_t ws_bytes,
                                  bdlm_stream stream);
 
+/* ---- Serving from an 8-bit cache of the clean stream ----------------------
+ * A trained block diffusion model answers block by block: the clean prefix of
+ * a sequence is fixed, and the rows of its next block (a corrupted block at a
+ * denoising step, the finished block, or a single token) attend to that prefix
+ * and, bidirectionally, to their own block: the corrupted stream's mask
+ * above, with the clean blocks before it read from a cache.
+ *
+ * The cache.  Tokens lie in pages of `page` (16, 32, 64 or 128) consecutive
+ * tokens of one sequence; token i of sequence s is slot i % page of page
+ * page_table[s, i / page].  k8 / v8 hold e4m3 codes [n_pages, Hkv, page, d],
+ * and every (page, KV head) block has one fp32 scale in k_scale / v_scale
+ * [n_pages, Hkv]: value = code * scale (finite codes; scale > 0).
+ * lens [n_seqs] are the cached tokens of the sequences.  page_table and lens
+ * are device arrays, read when the kernels run, so that a captured step
+ * replays on lengths and pages that move.  Pages may be shared by sequences
+ * that only read them (a common prefix).
+ *
+ * New rows are packed [rows, H, d]: sequence s owns rows [row_offsets[s],
+ * row_offsets[s+1]) (a device array of n_seqs + 1 int32; rows from
+ * row_offsets[n_seqs] on are not touched), at most max_rows each; or, with
+ * row_offsets null, max_rows rows each (rows = n_seqs * max_rows).
+ *
+ * Workspace: bdlm_workspace_size_cache bytes, whose first 256 the caller
+ * zeroes ONCE (these calls do not clear the status word: an error stays until
+ * bdlm_sync_status reads it).  Contents that only the device can check -- a
+ * page id outside the pool, a length that is negative or outside the page
+ * table, row offsets that leave the rows or exceed max_rows -- are left out of
+ * the result (those keys unseen, that length cut, those rows skipped) and
+ * reported by bdlm_sync_status as BDLM_ERR_INVALID_ARG. */
+typedef struct {
+  void* k8;                  /* [n_pages, Hkv, page, d] e4m3 */
+  void* v8;
+  float* k_scale;            /* [n_pages, Hkv] */
+  float* v_scale;
+  const int32_t* page_table; /* [n_seqs, max_pages] */
+  const int32_t* lens;       /* [n_seqs] */
+  int64_t n_pages;
+  int n_seqs, max_pages, page, Hkv, d;
+} bdlm_cache;
+
+/* Bytes of workspace for every call on a cache of these sizes; keep is the
+ * largest `keep` of a bdlm_cache_evict that is given no `kept` (else 0).
+ * Returns 0 for an invalid shape. */
+size_t bdlm_workspace_size_cache(int n_seqs, int Hkv, int d, int64_t keep);
+
+/* Quantises the rows' K and V [rows, Hkv, d] (bf16) into the sequences' pages
+ * behind their lens tokens.  A block's scale is the smallest power of two, at
+ * least 2^-64, that holds the largest magnitude of its new tokens within 448;
+ * codes are the nearest e4m3 value, ties to even.  A block that already holds
+ * tokens keeps its scale if that is larger; else its old codes are rounded
+ * to the new scale.  A block that takes in a NaN or an infinity gets a NaN
+ * scale: every row that sees it reads NaN.  lens_out [n_seqs] (may be null)
+ * gets lens + rows; it must not overlap lens, which is left as it is.  Pages
+ * written by the call must belong to one sequence only. */
+bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* cache, const int32_t* row_offsets,
+                              int64_t rows, int64_t max_rows, int32_t* lens_out, void* workspace, size_t ws_bytes,
+                              bdlm_stream stream);
+
+/* Attention of the rows to their sequence's lens cached tokens and, unless Kn
+ * and Vn are null, to the rows of their own sequence:
+ *   O_i = sum_j exp(s_ij - LSE_i) v_j,  s_ij = scale q_i . k_j,  LSE natural log.
+ * Qn [rows, Hq, d], Kn, Vn [rows, Hkv, d] bf16; O [rows, Hq, d] in o_dtype;
+ * LSE [Hq, rows] fp32.  A row without a key gets O = 0, LSE = -inf.  For a
+ * bf16 output the probabilities are rounded to 16 bits; for an fp32 one they
+ * enter the product with V in several 16-bit parts (off by 2^-22 at most).
+ * Deterministic: the keys are split over the GPU by their number, and the
+ * parts are joined in a fixed order. */
+bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, const bdlm_cache* cache,
+                             const int32_t* row_offsets, int64_t rows, int64_t max_rows, int Hq, float scale, void* O,
+                             bdlm_dtype o_dtype, float* LSE, void* workspace, size_t ws_bytes, bdlm_stream stream);
+
+/* Adds to weights [n_seqs, Hkv, max_pages * page] (fp32) the attention weight
+ * that each cached token received from the rows of its sequence,
+ *   weights[s, h, j] += sum_{i in rows of s} sum_{heads of h's group} exp(s_ij - LSE_i),
+ * with the LSE of bdlm_attn_cached on the same rows.  Rows whose LSE is -inf
+ * add nothing.  Deterministic. */
+bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cache* cache, const int32_t* row_offsets,
+                               int64_t rows, int64_t max_rows, int Hq, float scale, float* weights, void* workspace,
+                               size_t ws_bytes, bdlm_stream stream);
+
+/* Cuts every sequence back to at most `keep` tokens, for each KV head on its
+ * own: the first `sinks` and the last `recent` tokens stay, and of the others
+ * those of largest weight (equal weights: the lower position; NaN counts as
+ * the largest).  The kept tokens move, in order, to slots 0, 1, ... of the
+ * pages of dst_table [n_seqs, max_pages] (pages of the same pool that no
+ * sequence reads; entries behind the last page needed are not used), in
+ * blocks that get the scale of bdlm_cache_append for what they hold.
+ * lens_out [n_seqs] = min(lens, keep); weights_out gets the kept tokens'
+ * weights and zero behind them; kept [n_seqs, Hkv, keep] (may be null) their
+ * old positions and -1 behind them.  The old pages, page_table, lens and
+ * weights are left as they are.  sinks + recent <= keep. */
+bdlm_status bdlm_cache_evict(const bdlm_cache* cache, const float* weights, const int32_t* dst_table, int64_t keep,
+                             int64_t sinks, int64_t recent, int32_t* lens_out, float* weights_out, int32_t* kept,
+                             void* workspace, size_t ws_bytes, bdlm_stream stream);
+
 /* Host-only: the forward work list in the order the persistent CTAs claim
  * its items, for inspection and tests.
  * One item per (query tile of tile_q rows, query head, stream), longest
@@ -387,8 +482,9 @@ int64_t bdlm_worklist(int64_t L, int64_t B, int Hq, int Hkv, int tile_q, int til
                       int32_t* out, int64_t cap);
 
 /* Waits for `stream`, then reads and clears the workspace's status word.
- * Returns BDLM_ERR_TIMEOUT if a kernel's bounded wait expired, BDLM_ERR_CUDA
- * if the stream reported an error, else BDLM_OK. */
+ * Returns BDLM_ERR_TIMEOUT if a kernel's bounded wait expired,
+ * BDLM_ERR_INVALID_ARG if a cache call met contents out of range,
+ * BDLM_ERR_CUDA if the stream reported an error, else BDLM_OK. */
 bdlm_status bdlm_sync_status(void* workspace, bdlm_stream stream);
 
 /* Exercises the device watchdog: launches a one-warp kernel that waits on an

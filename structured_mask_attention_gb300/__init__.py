@@ -23,6 +23,8 @@ __all__ = [
     "bdlm_lse_merge", "bdlm_bwd_preprocess", "bdlm_attn_bwd", "bdlm_attn_bwd_noalloc", "bdlm_attn_bwd_shard",
     "bdlm_worklist", "bdlm_workspace_size_varlen", "bdlm_attn_fwd_varlen", "bdlm_attn_bwd_varlen",
     "bdlm_sync_status", "bdlm_watchdog_selftest", "bdlm_sync_status_noalloc", "bdlm_watchdog_selftest_noalloc",
+    "BdlmCache", "bdlm_cache_workspace", "bdlm_workspace_size_cache", "bdlm_cache_append", "bdlm_attn_cached",
+    "bdlm_cache_weights", "bdlm_cache_evict",
     "bdlm_kernel_launches", "bdlm_last_error",
     "bdlm_version", "bdlm_timing_enable", "bdlm_timing_report", "header_functions", "LIB_PATH",
     "HEADER_PATH",
@@ -77,6 +79,11 @@ _SIGS = {
     "bdlm_workspace_size_varlen": (_SZ, [_I, _P, _I, _I, _I, _I]),
     "bdlm_attn_fwd_varlen": (_I, [_P] * 6 + [_P, _I, _I64, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P, _SZ, _P]),
     "bdlm_attn_bwd_varlen": (_I, [_P] * 12 + [_P, _I, _I64, _I, _I, _I, _F] + [_P] * 6 + [_I, _P, _SZ, _P]),
+    "bdlm_workspace_size_cache": (_SZ, [_I, _I, _I, _I64]),
+    "bdlm_cache_append": (_I, [_P, _P, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "bdlm_attn_cached": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _P, _I, _P, _P, _SZ, _P]),
+    "bdlm_cache_weights": (_I, [_P, _P, _P, _P, _I64, _I64, _I, _F, _P, _P, _SZ, _P]),
+    "bdlm_cache_evict": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
     "bdlm_sync_status": (_I, [_P, _P]),
     "bdlm_sync_status_noalloc": (_I, [_P]),
     "bdlm_watchdog_selftest_noalloc": (_I, [ctypes.c_uint32, _P]),
@@ -557,9 +564,224 @@ def bdlm_attn_bwd_varlen(Qc, Kc, Vc, Qn, Kn, Vn, Oc, On, dOc, dOn, LSEc, LSEn, s
     return out
 
 
+# ------------------------------------------------------------ 8-bit cache
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k8", _P), ("v8", _P), ("k_scale", _P), ("v_scale", _P), ("page_table", _P), ("lens", _P),
+                ("n_pages", _I64), ("n_seqs", _I), ("max_pages", _I), ("page", _I), ("Hkv", _I), ("d", _I)]
+
+
+class BdlmCache:
+    """A paged 8-bit cache over the caller's tensors, checked once here:
+
+    ``k8``, ``v8`` [n_pages, Hkv, page, d] torch.float8_e4m3fn (codes);
+    ``k_scale``, ``v_scale`` [n_pages, Hkv] float32 (value = code * scale);
+    ``page_table`` [n_seqs, max_pages] int32; ``lens`` [n_seqs] int32.
+
+    The handle keeps the tensors; update ``page_table`` and ``lens`` in place
+    (``copy_``), or make a new handle for other tensors."""
+    __slots__ = ("k8", "v8", "k_scale", "v_scale", "page_table", "lens", "device", "n_pages", "n_seqs", "max_pages",
+                 "page", "Hkv", "d", "_struct", "_ref")
+
+    def __init__(self, k8, v8, k_scale, v_scale, page_table, lens):
+        torch = _torch()
+        if k8.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("k8 must be [n_pages, Hkv, page, d], page_table [n_seqs, max_pages]")
+        n_pages, Hkv, page, d = k8.shape
+        n_seqs, max_pages = page_table.shape
+        for name, t, dtype, shape in (("k8", k8, torch.float8_e4m3fn, (n_pages, Hkv, page, d)),
+                                      ("v8", v8, torch.float8_e4m3fn, (n_pages, Hkv, page, d)),
+                                      ("k_scale", k_scale, torch.float32, (n_pages, Hkv)),
+                                      ("v_scale", v_scale, torch.float32, (n_pages, Hkv)),
+                                      ("page_table", page_table, torch.int32, (n_seqs, max_pages)),
+                                      ("lens", lens, torch.int32, (n_seqs,))):
+            _check_tensor(name, t, dtype, shape, k8.device)
+            object.__setattr__(self, name, t)
+        set_ = lambda name, v: object.__setattr__(self, name, v)
+        for name, v in (("device", k8.device), ("n_pages", n_pages), ("n_seqs", n_seqs), ("max_pages", max_pages),
+                        ("page", page), ("Hkv", Hkv), ("d", d)):
+            set_(name, v)
+        set_("_struct", _CacheStruct(*(t.data_ptr() for t in (k8, v8, k_scale, v_scale, page_table, lens)),
+                                     n_pages, n_seqs, max_pages, page, Hkv, d))
+        set_("_ref", ctypes.cast(ctypes.pointer(self._struct), _P))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a BdlmCache is fixed: update its tensors in place or make a new handle")
+
+
+def _check_tensor(name, t, dtype, shape, device):
+    if t.device != device or not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device} (a CUDA "
+                         f"device), not {t.dtype} {list(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _cache_rows(cache, row_offsets, max_rows, T):
+    """(row_offsets pointer, max_rows) of a call on T packed rows."""
+    if row_offsets is None:
+        if max_rows is None:
+            if T % cache.n_seqs:
+                raise ValueError(f"{T} rows are not a multiple of n_seqs = {cache.n_seqs}: give row_offsets")
+            max_rows = T // cache.n_seqs
+        return None, max_rows
+    _check_tensor("row_offsets", row_offsets, _torch().int32, (cache.n_seqs + 1,), cache.device)
+    return row_offsets.data_ptr(), T if max_rows is None else max_rows
+
+
+def _cache_call(name, cache, stream, args, tensors=()):
+    """Calls entry point `name` with the current (or given) stream of the cache's device appended; `tensors` made by
+    this call are marked as used on a given stream."""
+    cuda = _torch().cuda
+    if stream is None:
+        stream = cuda.current_stream(cache.device)
+    else:
+        if stream.device != cache.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
+        for t in tensors:
+            t.record_stream(stream)
+    fn = getattr(load_library(), name)
+    if cuda.current_device() == cache.device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with cuda.device(cache.device):
+            status = fn(*args, stream.cuda_stream)
+    if status:
+        _check(status)
+
+
+def bdlm_workspace_size_cache(n_seqs: int, Hkv: int, d: int, keep: int = 0) -> int:
+    return int(load_library().bdlm_workspace_size_cache(n_seqs, Hkv, d, keep))
+
+
+def bdlm_cache_workspace(cache, Hq: int = 0, max_rows: int = 0, keep: int = 0):
+    """A zeroed workspace for every call on ``cache`` (evictions to at most
+    ``keep`` tokens).  One call at a time uses it; make one per stream and one
+    per captured graph that may run beside others.  ``Hq`` and ``max_rows``
+    are accepted for callers that size by them; no call needs more for them."""
+    torch = _torch()
+    n = bdlm_workspace_size_cache(cache.n_seqs, cache.Hkv, cache.d, keep)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.device)
+
+
+def _cache_workspace(cache, ws, made, need):
+    if ws is None:
+        # the kernels' part is written before it is read; only the header has to be zero
+        ws = _torch().empty(need, dtype=_torch().uint8, device=cache.device)
+        ws[:256].zero_()
+        made.append(ws)
+    elif ws.device != cache.device:
+        raise ValueError(f"the workspace is on {ws.device}, the cache on {cache.device}")
+    return ws
+
+
+def bdlm_cache_append(cache, K, V, row_offsets=None, max_rows: int | None = None, lens_out=None, workspace=None,
+                      stream=None):
+    """Quantises the new tokens' K, V [rows, Hkv, d] (bf16) into the pages of
+    their sequences, behind ``cache.lens`` tokens (which stays as it is).
+    Returns ``lens_out`` [n_seqs] int32 = lens + rows; copy it into
+    ``cache.lens`` once the sequences have grown."""
+    torch = _torch()
+    T = K.shape[0]
+    _check_tensor("K", K, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
+    _check_tensor("V", V, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
+    off, max_rows = _cache_rows(cache, row_offsets, max_rows, T)
+    made = []
+    if lens_out is None:
+        lens_out = torch.empty(cache.n_seqs, dtype=torch.int32, device=cache.device)
+        made.append(lens_out)
+    else:
+        _check_tensor("lens_out", lens_out, torch.int32, (cache.n_seqs,), cache.device)
+    ws = _cache_workspace(cache, workspace, made, 256)
+    _cache_call("bdlm_cache_append", cache, stream,
+                (K.data_ptr(), V.data_ptr(), cache._ref, off, T, max_rows, lens_out.data_ptr(), ws.data_ptr(),
+                 ws.numel()), made)
+    return lens_out
+
+
+def bdlm_attn_cached(Qn, Kn, Vn, cache, row_offsets=None, max_rows: int | None = None, scale: float | None = None,
+                     o_dtype=None, out=None, workspace=None, stream=None):
+    """Attention of packed new rows (Qn [rows, Hq, d]; Kn, Vn [rows, Hkv, d],
+    or both None for the cached tokens alone) to their sequence's cached
+    tokens and their own block.  Returns (O [rows, Hq, d], LSE [Hq, rows])."""
+    torch = _torch()
+    T, Hq, d = Qn.shape
+    _check_tensor("Qn", Qn, torch.bfloat16, (T, Hq, cache.d), cache.device)
+    if (Kn is None) != (Vn is None):
+        raise ValueError("Kn and Vn: give both or neither")
+    if Kn is not None:
+        _check_tensor("Kn", Kn, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
+        _check_tensor("Vn", Vn, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
+    off, max_rows = _cache_rows(cache, row_offsets, max_rows, T)
+    made = []
+    if out is None:
+        O = torch.empty((T, Hq, d), dtype=torch.bfloat16 if o_dtype is None else o_dtype, device=cache.device)
+        LSE = torch.empty((Hq, T), dtype=torch.float32, device=cache.device)
+        made += [O, LSE]
+    else:
+        O, LSE = out
+        _check_tensor("O", O, O.dtype if o_dtype is None else o_dtype, (T, Hq, d), cache.device)
+        _check_tensor("LSE", LSE, torch.float32, (Hq, T), cache.device)
+    if O.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"O must be bfloat16 or float32, not {O.dtype}")
+    ws = _cache_workspace(cache, workspace, made,
+                          bdlm_workspace_size_cache(cache.n_seqs, cache.Hkv, cache.d) if workspace is None else 0)
+    _cache_call("bdlm_attn_cached", cache, stream,
+                (Qn.data_ptr(), None if Kn is None else Kn.data_ptr(), None if Vn is None else Vn.data_ptr(), cache._ref,
+                 off, T, max_rows, Hq, 1.0 / math.sqrt(d) if scale is None else scale, O.data_ptr(),
+                 F32 if O.dtype == torch.float32 else BF16, LSE.data_ptr(), ws.data_ptr(), ws.numel()), made)
+    return O, LSE
+
+
+def bdlm_cache_weights(Qn, LSE, cache, weights, row_offsets=None, max_rows: int | None = None,
+                       scale: float | None = None, workspace=None, stream=None):
+    """Adds to ``weights`` [n_seqs, Hkv, max_pages * page] float32 the attention
+    weight that every cached token receives from the rows (their LSE [Hq,
+    rows] from ``bdlm_attn_cached``).  Returns ``weights``."""
+    torch = _torch()
+    T, Hq, d = Qn.shape
+    _check_tensor("Qn", Qn, torch.bfloat16, (T, Hq, cache.d), cache.device)
+    _check_tensor("LSE", LSE, torch.float32, (Hq, T), cache.device)
+    _check_tensor("weights", weights, torch.float32, (cache.n_seqs, cache.Hkv, cache.max_pages * cache.page),
+                  cache.device)
+    off, max_rows = _cache_rows(cache, row_offsets, max_rows, T)
+    made = []
+    ws = _cache_workspace(cache, workspace, made, 256)
+    _cache_call("bdlm_cache_weights", cache, stream,
+                (Qn.data_ptr(), LSE.data_ptr(), cache._ref, off, T, max_rows, Hq,
+                 1.0 / math.sqrt(d) if scale is None else scale, weights.data_ptr(), ws.data_ptr(), ws.numel()), made)
+    return weights
+
+
+def bdlm_cache_evict(cache, weights, dst_table, keep: int, sinks: int = 0, recent: int = 0, lens_out=None,
+                     weights_out=None, kept=None, workspace=None, stream=None):
+    """Cuts every sequence back to at most ``keep`` tokens per KV head (the
+    first ``sinks``, the last ``recent``, and those of largest weight), moved
+    to the pages of ``dst_table`` [n_seqs, max_pages].  Returns (lens_out,
+    weights_out, kept); kept [n_seqs, Hkv, keep] int32 holds the old
+    positions, -1 behind the last."""
+    torch = _torch()
+    shape = (cache.n_seqs, cache.Hkv, cache.max_pages * cache.page)
+    _check_tensor("weights", weights, torch.float32, shape, cache.device)
+    _check_tensor("dst_table", dst_table, torch.int32, (cache.n_seqs, cache.max_pages), cache.device)
+    made = []
+    new = lambda s, dt: made.append(torch.empty(s, dtype=dt, device=cache.device)) or made[-1]
+    lens_out = new((cache.n_seqs,), torch.int32) if lens_out is None else lens_out
+    weights_out = new(shape, torch.float32) if weights_out is None else weights_out
+    if kept is None:
+        kept = new((cache.n_seqs, cache.Hkv, max(int(keep), 0)), torch.int32)
+    _check_tensor("lens_out", lens_out, torch.int32, (cache.n_seqs,), cache.device)
+    _check_tensor("weights_out", weights_out, torch.float32, shape, cache.device)
+    _check_tensor("kept", kept, torch.int32, (cache.n_seqs, cache.Hkv, max(int(keep), 0)), cache.device)
+    ws = _cache_workspace(cache, workspace, made, 256)
+    _cache_call("bdlm_cache_evict", cache, stream,
+                (cache._ref, weights.data_ptr(), dst_table.data_ptr(), keep, sinks, recent, lens_out.data_ptr(),
+                 weights_out.data_ptr(), kept.data_ptr() or None, ws.data_ptr(), ws.numel()), made)
+    return lens_out, weights_out, kept
+
+
 def bdlm_sync_status(workspace, stream=None):
     """Synchronises and raises BdlmError(BDLM_ERR_TIMEOUT) if a kernel's
-    bounded wait expired since the last call on this workspace."""
+    bounded wait expired since the last call on this workspace, or
+    BdlmError(BDLM_ERR_INVALID_ARG) if a cache call met contents out of range."""
     _check(load_library().bdlm_sync_status(_ptr(workspace), _stream(stream)))
 
 

@@ -20,6 +20,8 @@
 #include <vector>
 
 #include "../../include/bdlm_attn.h"
+#include "abi_internal.h"
+#include "cache.cuh"
 #include "geometry.cuh"
 #include "kernels.h"
 
@@ -31,9 +33,12 @@ thread_local std::string g_last_error;
 std::atomic<uint64_t> g_launches{0};
 
 // ---------------------------------------------------------------- timing
-enum KernelKind { K_FWD = 0, K_DKV, K_DQ, K_PREP, K_MERGE, K_WATCHDOG, K_COUNT };
+enum KernelKind { K_FWD = 0, K_DKV, K_DQ, K_PREP, K_MERGE, K_WATCHDOG, K_CACHE0, K_COUNT = K_CACHE0 + 5 };
 const char* const kKindNames[K_COUNT] = {"bdlm_fwd_tc", "bdlm_bwd_dkv", "bdlm_bwd_dq",
-                                         "bdlm_preprocess", "bdlm_merge", "bdlm_watchdog"};
+                                         "bdlm_preprocess", "bdlm_merge", "bdlm_watchdog",
+                                         // in the order of AbiTimer
+                                         "bdlm_cache_append", "bdlm_attn_cached", "bdlm_cached_merge",
+                                         "bdlm_cache_weights", "bdlm_cache_evict"};
 
 struct Timing {
   std::mutex mu;
@@ -174,10 +179,6 @@ bdlm_status device_info(DeviceInfo& info) {
     return fail(BDLM_ERR_UNSUPPORTED, "device is sm_%d%d; this library is built for sm_103a", info.major, info.minor);
   return BDLM_OK;
 }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 bdlm_status get_encoder(EncodeTiledFn& fn) {
   static std::once_flag once;
@@ -569,6 +570,36 @@ bdlm_status varlen_tables(const Geom& all, const int64_t* off, int n, int tq, bo
 
 void bdlm::set_last_error(const std::string& msg) { g_last_error = msg; }
 
+// ------------------------------------------------ shared with the cache calls
+bdlm_status bdlm::abi_fail(bdlm_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return s;
+}
+
+bdlm_status bdlm::abi_device(int* sms) {
+  DeviceInfo info;
+  BDLM_CHECK(device_info(info));
+  *sms = info.sms;
+  return BDLM_OK;
+}
+
+bdlm_status bdlm::abi_encoder(EncodeTiledFn* fn) { return get_encoder(*fn); }
+
+uint64_t bdlm::abi_wait_limit_ns() { return wait_limit_ns(); }
+
+void* bdlm::abi_timer_begin(AbiTimer kind, cudaStream_t st) {
+  return timing().on.load() ? new ScopedKernelTimer(K_CACHE0 + (int)kind, st) : nullptr;
+}
+
+void bdlm::abi_timer_end(void* timer) { delete static_cast<ScopedKernelTimer*>(timer); }
+
+bdlm_status bdlm::abi_finish(cudaError_t e, int launches, const char* what) { return finish(e, launches, what); }
+
 extern "C" {
 
 size_t bdlm_workspace_size(int op, int64_t L, int64_t B, int Hq, int Hkv, int d, int P) {
@@ -938,6 +969,11 @@ bdlm_status bdlm_sync_status(void* workspace, bdlm_stream stream) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(status)");
     e = cudaMemset(workspace, 0, 4);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(status)");
+    if ((word >> 8) == (kStatusCacheMask >> 8))
+      return fail(BDLM_ERR_INVALID_ARG, "cache contents out of range (status 0x%x):%s%s%s", word,
+                  (word & 0xff & kStatusBadPage) ? " a page id outside the pool;" : "",
+                  (word & 0xff & kStatusBadLen) ? " a length outside its page table;" : "",
+                  (word & 0xff & kStatusBadRows) ? " row offsets outside the rows;" : "");
     if (word != 0)
       return fail(BDLM_ERR_TIMEOUT, "device wait limit expired (status 0x%x, wait site %u)", word, word & 0xffu);
     return BDLM_OK;

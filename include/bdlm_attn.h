@@ -404,10 +404,11 @@ typedef struct {
   int n_seqs, max_pages, page, Hkv, d;
 } bdlm_cache;
 
-/* Bytes of workspace for every call on a cache of these sizes; keep is the
- * largest `keep` of a bdlm_cache_evict that is given no `kept` (else 0).
- * Returns 0 for an invalid shape. */
-size_t bdlm_workspace_size_cache(int n_seqs, int Hkv, int d, int64_t keep);
+/* Bytes of workspace for every call on a cache of these sizes with at most
+ * max_rows new rows per sequence (0: no bdlm_attn_cached); keep is the largest
+ * `keep` of a bdlm_cache_evict that is given no `kept` (else 0).  Returns 0 for
+ * an invalid shape. */
+size_t bdlm_workspace_size_cache(int n_seqs, int Hq, int Hkv, int d, int64_t max_rows, int64_t keep);
 
 /* Quantises the rows' K and V [rows, Hkv, d] (bf16) into the sequences' pages
  * behind their lens tokens.  A block's scale is the smallest power of two, at

@@ -79,7 +79,7 @@ _SIGS = {
     "bdlm_workspace_size_varlen": (_SZ, [_I, _P, _I, _I, _I, _I]),
     "bdlm_attn_fwd_varlen": (_I, [_P] * 6 + [_P, _I, _I64, _I, _I, _I, _F, _P, _P, _I, _P, _P, _P, _SZ, _P]),
     "bdlm_attn_bwd_varlen": (_I, [_P] * 12 + [_P, _I, _I64, _I, _I, _I, _F] + [_P] * 6 + [_I, _P, _SZ, _P]),
-    "bdlm_workspace_size_cache": (_SZ, [_I, _I, _I, _I64]),
+    "bdlm_workspace_size_cache": (_SZ, [_I, _I, _I, _I, _I64, _I64]),
     "bdlm_cache_append": (_I, [_P, _P, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "bdlm_attn_cached": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _P, _I, _P, _P, _SZ, _P]),
     "bdlm_cache_weights": (_I, [_P, _P, _P, _P, _I64, _I64, _I, _F, _P, _P, _SZ, _P]),
@@ -648,17 +648,19 @@ def _cache_call(name, cache, stream, args, tensors=()):
         _check(status)
 
 
-def bdlm_workspace_size_cache(n_seqs: int, Hkv: int, d: int, keep: int = 0) -> int:
-    return int(load_library().bdlm_workspace_size_cache(n_seqs, Hkv, d, keep))
+def bdlm_workspace_size_cache(n_seqs: int, Hq: int, Hkv: int, d: int, max_rows: int, keep: int = 0) -> int:
+    return int(load_library().bdlm_workspace_size_cache(n_seqs, Hq, Hkv, d, max_rows, keep))
 
 
 def bdlm_cache_workspace(cache, Hq: int = 0, max_rows: int = 0, keep: int = 0):
-    """A zeroed workspace for every call on ``cache`` (evictions to at most
-    ``keep`` tokens).  One call at a time uses it; make one per stream and one
-    per captured graph that may run beside others.  ``Hq`` and ``max_rows``
-    are accepted for callers that size by them; no call needs more for them."""
+    """A zeroed workspace for every call on ``cache``: attention of at most
+    ``max_rows`` new rows per sequence with ``Hq`` query heads, evictions to at
+    most ``keep`` tokens.  One call at a time uses it; make one per stream and
+    one per captured graph that may run beside others."""
     torch = _torch()
-    n = bdlm_workspace_size_cache(cache.n_seqs, cache.Hkv, cache.d, keep)
+    n = bdlm_workspace_size_cache(cache.n_seqs, Hq, cache.Hkv, cache.d, max_rows, keep)
+    if not n:
+        raise ValueError(f"no workspace for Hq={Hq}, max_rows={max_rows}, keep={keep} on this cache")
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.device)
 
 
@@ -723,7 +725,8 @@ def bdlm_attn_cached(Qn, Kn, Vn, cache, row_offsets=None, max_rows: int | None =
     if O.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"O must be bfloat16 or float32, not {O.dtype}")
     ws = _cache_workspace(cache, workspace, made,
-                          bdlm_workspace_size_cache(cache.n_seqs, cache.Hkv, cache.d) if workspace is None else 0)
+                          max(bdlm_workspace_size_cache(cache.n_seqs, Hq, cache.Hkv, d, max_rows), 256)
+                          if workspace is None else 0)
     _cache_call("bdlm_attn_cached", cache, stream,
                 (Qn.data_ptr(), None if Kn is None else Kn.data_ptr(), None if Vn is None else Vn.data_ptr(), cache._ref,
                  off, T, max_rows, Hq, 1.0 / math.sqrt(d) if scale is None else scale, O.data_ptr(),

@@ -98,8 +98,35 @@ bdlm_status check_space(void* ws, size_t bytes, size_t need) {
   return BDLM_OK;
 }
 
-size_t attn_space(int d) {
-  return (size_t)kSmsMax * kSmallCtasPerSm * 2 * part_floats(kSmallRows, d) * sizeof(float);
+size_t attn_space(int64_t flat, int d) {
+  const int tile = cached_tile_rows(flat);
+  return (size_t)cached_ctas(tile, kSmsMax) * 2 * part_floats(tile, d) * sizeof(float);
+}
+
+// K's codes: boxes of one (page, KV head) block, swizzled by the row's bytes.
+bdlm_status encode_codes(EncodeTiledFn fn, CUtensorMap* m, const CacheDesc& c) {
+  cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)(c.n_pages * c.Hkv)};
+  cuuint64_t strides[2] = {(cuuint64_t)c.d, (cuuint64_t)c.d * c.page};
+  cuuint32_t box[3] = {(cuuint32_t)c.d, (cuuint32_t)c.page, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k8, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return abi_fail(BDLM_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return BDLM_OK;
+}
+
+// [T, H, d] bf16: boxes of 64 columns, one head, 128 rows.
+bdlm_status encode_rows(EncodeTiledFn fn, CUtensorMap* m, const void* p, int64_t T, int H, int d) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return abi_fail(BDLM_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return BDLM_OK;
 }
 size_t kept_space(int n_seqs, int Hkv, int64_t keep) { return (size_t)n_seqs * Hkv * keep * sizeof(int32_t); }
 
@@ -107,11 +134,12 @@ size_t kept_space(int n_seqs, int Hkv, int64_t keep) { return (size_t)n_seqs * H
 
 extern "C" {
 
-size_t bdlm_workspace_size_cache(int n_seqs, int Hkv, int d, int64_t keep) {
-  if (n_seqs <= 0 || n_seqs > 65535 || Hkv <= 0 || Hkv > 4096 || (d != 64 && d != 128) || keep < 0 ||
-      keep > (int64_t)1 << 30)
+size_t bdlm_workspace_size_cache(int n_seqs, int Hq, int Hkv, int d, int64_t max_rows, int64_t keep) {
+  if (n_seqs <= 0 || n_seqs > 65535 || Hkv <= 0 || Hkv > 4096 || Hq < 0 || Hq > 4096 || Hq % Hkv ||
+      (d != 64 && d != 128) || max_rows < 0 || max_rows > (int64_t)1 << 24 || keep < 0 || keep > (int64_t)1 << 30)
     return 0;
-  return kHeader + std::max(attn_space(d), kept_space(n_seqs, Hkv, keep));
+  const int64_t flat = max_rows * (Hq / Hkv);
+  return kHeader + std::max(flat > 0 ? attn_space(flat, d) : 0, kept_space(n_seqs, Hkv, keep));
 }
 
 bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* cache, const int32_t* row_offsets,
@@ -162,7 +190,8 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     }
     CACHE_CHECK(check_ptr("O", O, 16));
     CACHE_CHECK(check_ptr("LSE", LSE, 4));
-    CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(p.c.d)));
+    const int64_t flat = max_rows * (Hq / p.c.Hkv);
+    CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(flat, p.c.d)));
     int sms;
     CACHE_CHECK(abi_device(&sms));
     p.sp.group = Hq / p.c.Hkv;
@@ -178,12 +207,22 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     p.status = static_cast<uint32_t*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
     p.limit_ns = abi_wait_limit_ns();
-    p.sp.tile_rows = kSmallRows;
-    p.G = std::min(sms, kSmsMax) * kSmallCtasPerSm;
+    p.sp.tile_rows = cached_tile_rows(flat);
+    p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
+    CachedMaps maps;
+    if (p.sp.tile_rows != kSmallRows) {
+      EncodeTiledFn enc;
+      CACHE_CHECK(abi_encoder(&enc));
+      CACHE_CHECK(encode_codes(enc, &maps.k8, p.c));
+      // without own keys these maps are not used: any valid tensor encodes
+      CACHE_CHECK(encode_rows(enc, &maps.k, Kn ? Kn : Qn, rows, Kn ? p.c.Hkv : Hq, p.c.d));
+      CACHE_CHECK(encode_rows(enc, &maps.v, Vn ? Vn : Qn, rows, Vn ? p.c.Hkv : Hq, p.c.d));
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int launches = 0;
     void* tm = abi_timer_begin(ABI_T_ATTN_CACHED, st);
-    cudaError_t e = launch_cached_small(p, st, &launches);
+    cudaError_t e = p.sp.tile_rows == kSmallRows ? launch_cached_small(p, st, &launches)
+                                                 : launch_cached_tc(maps, p, st, &launches);
     abi_timer_end(tm);
     if (e == cudaSuccess) {
       tm = abi_timer_begin(ABI_T_CACHED_MERGE, st);

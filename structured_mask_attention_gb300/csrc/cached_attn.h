@@ -28,8 +28,20 @@ struct CachedParams {
 // then their running maxima (log2 units) and sums, all fp32.
 __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (int64_t)tile_rows * (d + 2); }
 
-constexpr int kSmallRows = 16;       // row tile of the mma.sync kernel
-constexpr int kSmallCtasPerSm = 2;   // its resident CTAs
+constexpr int kSmallRows = 16;      // row tile of the mma.sync kernel
+constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
+
+// Row tile of a call whose sequences have at most `flat` rows times heads of
+// a group: 16 (mma.sync), 128 or 256 (tcgen05, split and pairs).
+inline int cached_tile_rows(int64_t flat) { return flat <= kSmallRows ? kSmallRows : flat <= 128 ? 128 : 256; }
+inline int cached_ctas(int tile_rows, int sms) { return tile_rows == kSmallRows ? sms * kSmallCtasPerSm : sms; }
+
+// Tensor maps of the tcgen05 kernel: K's codes as [n_pages * Hkv, page, d],
+// the new rows' K and V as [T, Hkv, d] bf16.
+struct CachedMaps {
+  CUtensorMap k8, k, v;
+};
+cudaError_t launch_cached_tc(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 
 cudaError_t launch_cached_small(const CachedParams& p, cudaStream_t st, int* launches);
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches);

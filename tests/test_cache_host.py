@@ -102,9 +102,11 @@ def test_evict_is_checked(lib, kw, status):
 
 
 def test_workspace_size(lib):
-    assert m.bdlm_workspace_size_cache(4, 2, 96) == 0 and m.bdlm_workspace_size_cache(0, 2, 64) == 0
-    small = m.bdlm_workspace_size_cache(4, 2, 64)
-    assert small > 256 and m.bdlm_workspace_size_cache(4, 2, 64, keep=1 << 24) >= 256 + 4 * 2 * (1 << 24) * 4
+    size = m.bdlm_workspace_size_cache
+    assert size(4, 4, 2, 96, 1) == 0 and size(0, 4, 2, 64, 1) == 0 and size(4, 3, 2, 64, 1) == 0
+    assert size(4, 4, 2, 64, 0) == 256 and size(4, 4, 2, 64, -1) == 0
+    assert 256 < size(4, 4, 2, 64, 1) < size(4, 4, 2, 64, 200)
+    assert size(4, 4, 2, 64, 1, keep=1 << 24) >= 256 + 4 * 2 * (1 << 24) * 4
 
 
 def test_handle_refuses_host_tensors_and_reassignment(lib):

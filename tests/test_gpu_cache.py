@@ -315,7 +315,7 @@ def test_contents_out_of_range_are_left_out_and_reported(lib, rows):
     for name, call in calls.items():
         for what, msg in (("page", "page id"), ("len", "length"), ("rows", "row offsets")):
             c, dst, cache = fresh()
-            ws, o = m.bdlm_cache_workspace(cache, keep=16), torch.from_numpy(off).cuda()
+            ws, o = m.bdlm_cache_workspace(cache, 2, rows, 16), torch.from_numpy(off).cuda()
             if what == "page":
                 cache.page_table[0, 3] = [1 << 30, -5][rows > 1]
             elif what == "len":
@@ -405,7 +405,7 @@ def test_captured_step_follows_lengths_and_pages(lib, B):
                     torch.empty((Hq, 2 * B), device="cuda"))
     ca, Wa = make()
     cb, Wb = make()
-    wa, wb, oa, ob, x = m.bdlm_cache_workspace(ca), m.bdlm_cache_workspace(cb), outs(), outs(), rows(0)
+    wa, wb, oa, ob, x = (*(m.bdlm_cache_workspace(k, Hq, B) for k in (ca, cb)), outs(), outs(), rows(0))
     lens0 = cb.lens.clone()
     saved = [t.clone() for t in (cb.k8.view(torch.uint8), cb.v8.view(torch.uint8), cb.k_scale, cb.v_scale)]
     graph = torch.cuda.CUDAGraph()

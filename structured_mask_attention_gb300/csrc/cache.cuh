@@ -124,46 +124,48 @@ struct AttnSplit {
   int group;      // query heads per KV head
   int tile_rows;  // rows of a row tile
   int local;      // the rows also read their own block
+  int extra;      // empty positions that open a segment
 };
 
 struct SegInfo {
   SeqView v;
   int rtiles, ktiles, ltiles;  // row tiles, cached units, own-block units that are not folded
   int units;                   // per segment
+  int span;                    // its positions in the list
 };
 
 __device__ __forceinline__ SegInfo seg_info(const CacheDesc& c, const RowsDesc& r, const AttnSplit& a, int s,
                                             uint32_t& bad) {
   SegInfo g;
   g.v = seq_view(c, r, s, bad);
-  const int64_t fr = (int64_t)g.v.rows * a.group;
-  g.rtiles = (int)((fr + a.tile_rows - 1) / a.tile_rows);
+  g.rtiles = (g.v.rows * a.group + a.tile_rows - 1) / a.tile_rows;
   g.ktiles = (g.v.len + kUnit - 1) / kUnit;
   g.ltiles = a.local && g.v.rows > kFoldRows ? (g.v.rows + kUnit - 1) / kUnit : 0;
   const int n = g.ktiles + g.ltiles;
   g.units = n > 0 ? n : 1;
+  g.span = g.units + a.extra;
   return g;
 }
 
 struct UnitPos {
-  int s, h, rt, j;
+  int s, h, rt, j;  // j: position in the segment; unit j - extra
 };
 
-// Units of all segments (every lane of the calling warp gets the sum).
+// Positions of all segments (every lane of the calling warp gets the sum).
 __device__ __forceinline__ int64_t total_units(const CacheDesc& c, const RowsDesc& r, const AttnSplit& a,
                                                uint32_t& bad) {
   const int lane = threadIdx.x & 31;
   int64_t sum = 0;
   for (int s = lane; s < c.n_seqs; s += 32) {
     const SegInfo g = seg_info(c, r, a, s, bad);
-    sum += (int64_t)g.rtiles * c.Hkv * g.units;
+    sum += (int64_t)g.rtiles * c.Hkv * g.span;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
 }
 
-// The segment and unit of list position u (0 <= u < total), by the whole warp.
+// The segment of list position u (0 <= u < total), by the whole warp.
 __device__ __forceinline__ UnitPos locate_unit(const CacheDesc& c, const RowsDesc& r, const AttnSplit& a, int64_t u,
                                                uint32_t& bad) {
   const int lane = threadIdx.x & 31;
@@ -171,12 +173,12 @@ __device__ __forceinline__ UnitPos locate_unit(const CacheDesc& c, const RowsDes
   for (int s0 = 0; s0 < c.n_seqs; s0 += 32) {
     const int s = s0 + lane;
     int64_t n = 0;
-    int units = 1, rt = 1;
+    int span = 1, rt = 1;
     if (s < c.n_seqs) {
       const SegInfo g = seg_info(c, r, a, s, bad);
-      units = g.units;
+      span = g.span;
       rt = g.rtiles;
-      n = (int64_t)g.rtiles * c.Hkv * g.units;
+      n = (int64_t)g.rtiles * c.Hkv * g.span;
     }
     int64_t cum = n;
 #pragma unroll
@@ -188,14 +190,14 @@ __device__ __forceinline__ UnitPos locate_unit(const CacheDesc& c, const RowsDes
     if (hit) {
       const int l = __ffs(hit) - 1;
       const int64_t left = u - (before + __shfl_sync(0xffffffffu, cum - n, l));
-      units = __shfl_sync(0xffffffffu, units, l);
+      span = __shfl_sync(0xffffffffu, span, l);
       rt = __shfl_sync(0xffffffffu, rt, l);
-      const int64_t seg = left / units;
+      const int64_t seg = left / span;
       UnitPos p;
       p.s = s0 + l;
       p.h = (int)(seg / rt);
       p.rt = (int)(seg % rt);
-      p.j = (int)(left % units);
+      p.j = (int)(left % span);
       return p;
     }
     before += __shfl_sync(0xffffffffu, cum, 31);
@@ -206,6 +208,14 @@ __device__ __forceinline__ UnitPos locate_unit(const CacheDesc& c, const RowsDes
 // CTAs that take part: no more than there are units, so that none is empty.
 __device__ __forceinline__ int split_ctas(int64_t U, int G) { return U < G ? (int)U : G; }
 __device__ __forceinline__ int64_t split_begin(int64_t U, int G, int c) { return U * c / G; }
+// The units [b, e) of the segment at pos (whose info is g) that lie below list position u1, pos being at u.
+__device__ __forceinline__ void split_units(const SegInfo& g, const AttnSplit& a, const UnitPos& pos, int64_t u, int64_t u1,
+                                            int& b, int& e) {
+  const int64_t n = u1 - u;
+  const int end = n < g.span - pos.j ? pos.j + (int)n : g.span;
+  b = pos.j > a.extra ? pos.j - a.extra : 0;
+  e = end > a.extra ? end - a.extra : 0;
+}
 // The CTA whose range holds unit u.
 __device__ __forceinline__ int split_owner(int64_t U, int G, int64_t u) { return (int)(((u + 1) * G - 1) / U); }
 

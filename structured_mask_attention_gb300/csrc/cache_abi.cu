@@ -194,6 +194,8 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(flat, p.c.d)));
     int sms;
     CACHE_CHECK(abi_device(&sms));
+    if (flat > (int64_t)1 << 30)
+      return abi_fail(BDLM_ERR_SHAPE, "max_rows * Hq / Hkv = %lld exceeds 2^30", (long long)flat);
     p.sp.group = Hq / p.c.Hkv;
     p.sp.local = Kn != nullptr;
     p.Q = Qn;
@@ -208,6 +210,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
     p.limit_ns = abi_wait_limit_ns();
     p.sp.tile_rows = cached_tile_rows(flat);
+    p.sp.extra = p.sp.tile_rows == kSmallRows ? kSmallExtra : kTcExtra;
     p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
     CachedMaps maps;
     if (p.sp.tile_rows != kSmallRows) {

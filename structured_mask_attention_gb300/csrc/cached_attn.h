@@ -24,12 +24,14 @@ struct CachedParams {
   uint64_t limit_ns;
 };
 
-// A partial result: O (not yet divided by the row sum) of tile_rows rows,
-// then their running maxima (log2 units) and sums, all fp32.
+// A partial result, fp32: O (not yet divided by the row sum), four columns of
+// all tile_rows rows together (so that threads that hold a row each write
+// side by side), then the rows' reference maxima (log2 units) and sums.
 __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (int64_t)tile_rows * (d + 2); }
 
 constexpr int kSmallRows = 16;      // row tile of the mma.sync kernel
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
+constexpr int kSmallExtra = 1, kTcExtra = 3;  // AttnSplit::extra: what a segment costs beside its units
 
 // Row tile of a call whose sequences have at most `flat` rows times heads of
 // a group: 16 (mma.sync), 128 or 256 (tcgen05, split and pairs).

@@ -71,8 +71,14 @@ struct State {
 
 // Scores of one group of N8 * 8 keys -> probabilities in place; the running
 // maximum moves, O and l are rescaled when it does.
+//
+// Value scales.  A cached key's score comes with log2 of its value block's
+// scale added: p' = exp2(s + log2 vs - m) is then the weight of the codes
+// themselves (O = sum p' code, at the fp16 precision of the largest weight
+// whatever the scales), and the row sum takes p' / vs (iv).  In units of
+// exp2(m), O / l is the attention's output and m + log2 l its LSE.
 template <int HD, int N8>
-__device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4]) {
+__device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], const float (&iv)[N8 / 2]) {
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     float mx = -INFINITY;
@@ -92,14 +98,15 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4]) {
       st.l[r] *= alpha;
     }
     st.m[r] = mn;
-    float sum = 0.f;
+    float sum[N8 / 2] = {};
 #pragma unroll
     for (int i = 0; i < N8; ++i) {
       s[i][2 * r] = ex2_approx(s[i][2 * r] - base);
       s[i][2 * r + 1] = ex2_approx(s[i][2 * r + 1] - base);
-      sum += s[i][2 * r] + s[i][2 * r + 1];
+      sum[i / 2] += s[i][2 * r] + s[i][2 * r + 1];
     }
-    st.l[r] += sum;
+#pragma unroll
+    for (int i = 0; i < N8 / 2; ++i) st.l[r] = fmaf(sum[i], iv[i], st.l[r]);
   }
 }
 
@@ -136,8 +143,10 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
     UnitPos pos = locate_unit(c, p.r, p.sp, u0, bad);
     SegInfo seg = seg_info(c, p.r, p.sp, pos.s, bad);
     for (int64_t u = u0; u < u1;) {
-      const int jb = pos.j;
-      const int je = (int)imin64(seg.units, jb + (u1 - u));
+      int jb, je;
+      split_units(seg, p.sp, pos, u, u1, jb, je);
+      u += seg.span - pos.j;
+      if (je == 0) break;  // only the segment's opening lies here: the next CTA begins it
       // ---- the tile's rows: fp16, each scaled by a power of two that puts
       // its largest magnitude in [2^14, 2^15): exact down to 2^-28 of it
       uint32_t q[KH * 4][4];
@@ -146,10 +155,9 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
       bool live[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int64_t fr = (int64_t)pos.rt * kSmallRows + g + 8 * r;
-        const int64_t tok = fr / p.sp.group;
+        const int fr = pos.rt * kSmallRows + g + 8 * r, tok = fr / p.sp.group;
         live[r] = tok < seg.v.rows;
-        const int head = pos.h * p.sp.group + (int)(fr - tok * p.sp.group);
+        const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
         qoff[r] = ((seg.v.row0 + (live[r] ? tok : 0)) * p.Hq + head) * HD;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) + qoff[r];
         uint32_t w[KH][8];
@@ -249,24 +257,24 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
           }
         }
         load_k(j + 1, npid);  // (ids of -1 past the end: nothing is read)
-        float vs[2];
+        float iv[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int64_t b = (int64_t)max(pid[x], 0) * c.Hkv + pos.h;
           const float ks = pid[x] >= 0 ? __ldg(c.ks + b) : 0.f;
-          vs[x] = pid[x] >= 0 ? __ldg(c.vs + b) : 0.f;  // (no key there: nothing is added)
+          const float vs = pid[x] >= 0 ? __ldg(c.vs + b) : 1.f;
+          const float lv = log2f(vs);
+          iv[x] = 1.f / vs;
           const int key = j * kUnit + warp * 32 + 16 * x + 2 * t;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const bool ok = pid[x] >= 0 && key + 8 * i + (e & 1) < seg.v.len;
-              s[2 * x + i][e] = ok ? s[2 * x + i][e] * (cq[e >> 1] * ks) : -INFINITY;
+              s[2 * x + i][e] = ok ? fmaf(s[2 * x + i][e], cq[e >> 1] * ks, lv) : -INFINITY;
             }
         }
-        softmax_step<HD, 4>(st, s);
-        // O += vs P V, the two halves apart where their pages' scales differ
-        const bool one = vs[0] == vs[1];
+        softmax_step<HD, 4>(st, s, iv);
         uint32_t pa[2][4], pr[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -280,7 +288,6 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
         for (int w = 0; w < VW; ++w)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {  // bytes 2 hf, 2 hf + 1 of word w: column tiles 4 w + 2 hf, + 1
-            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const uint32_t lo = __byte_perm(vw[x][0][w], vw[x][1][w], hf ? 0x7362 : 0x5140);
@@ -288,27 +295,10 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const uint32_t b0 = e4m3x2_to_half2(lo >> (16 * y)), b1 = e4m3x2_to_half2(hi >> (16 * y));
-                mma_f16(acc[y], pa[x][0], pa[x][1], pa[x][2], pa[x][3], b0, b1);
-                if (FINE) mma_f16(acc[y], pr[x][0], pr[x][1], pr[x][2], pr[x][3], b0, b1);
-              }
-              if (x == 0 && !one) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    float& o = st.o[4 * w + 2 * hf + y][e];
-                    o = fmaf(vs[0], acc[y][e], o);
-                    acc[y][e] = 0.f;
-                  }
+                mma_f16(st.o[4 * w + 2 * hf + y], pa[x][0], pa[x][1], pa[x][2], pa[x][3], b0, b1);
+                if (FINE) mma_f16(st.o[4 * w + 2 * hf + y], pr[x][0], pr[x][1], pr[x][2], pr[x][3], b0, b1);
               }
             }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float& o = st.o[4 * w + 2 * hf + y][e];
-                o = fmaf(vs[1], acc[y][e], o);
-              }
           }
         load_v(j + 1, npid);
         pid[0] = npid[0];
@@ -351,7 +341,8 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               s[i][e] = key0 + 8 * i + 2 * t + (e & 1) < seg.v.rows ? s[i][e] * p.sl2 : -INFINITY;
-          softmax_step<HD, 2>(st, s);
+          const float one[1] = {1.f};
+          softmax_step<HD, 2>(st, s, one);
           uint32_t pa[4], pr[4], pq[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -422,12 +413,11 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
           w[x] = M == -INFINITY ? 0.f : ex2_approx(red_ml[x][row][0] - M);
           L = fmaf(w[x], red_ml[x][row][1], L);
         }
-        const int64_t fr = (int64_t)pos.rt * kSmallRows + row;
-        const int64_t tok = fr / p.sp.group;
+        const int fr = pos.rt * kSmallRows + row, tok = fr / p.sp.group;
         const bool whole = jb == 0 && je == seg.units;
         float* slot = p.part + (2 * (int64_t)cta + (jb == 0 ? 1 : 0)) * part_floats(kSmallRows, HD);
         if (tok < seg.v.rows) {
-          const int head = pos.h * p.sp.group + (int)(fr - tok * p.sp.group);
+          const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
           const int64_t o0 = ((seg.v.row0 + tok) * p.Hq + head) * HD;
           const float inv = whole ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
 #pragma unroll
@@ -441,7 +431,7 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
               a.z = fmaf(w[x], b.z, a.z); a.w = fmaf(w[x], b.w, a.w);
             }
             a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
-            if (!whole) *reinterpret_cast<float4*>(slot + row * HD + col) = a;
+            if (!whole) reinterpret_cast<float4*>(slot)[(col >> 2) * kSmallRows + row] = a;
             else if (p.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o0 + col) = a;
             else
               *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + o0 + col) =
@@ -457,7 +447,6 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
         }
       }
       __syncthreads();
-      u += je - jb;
       if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
     }
   }
@@ -467,12 +456,14 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
 // Joins the partial results of the segments that span CTAs.  Block c takes
 // the segment that CTA c of the attention kernel began and did not finish (a
 // CTA has one such at most): its partials lie in slot 2 c + 1 and in slot
-// 2 c' of the CTAs c' that continue it, and are joined in that order.  A block
-// row takes kMergeRows rows; a row's HD columns go to HD / 4 threads.
-constexpr int kMergeThreads = 128;
+// 2 c' of the CTAs c' that continue it, and are joined in that order.  A
+// block takes 16 of the tile's rows; neighbouring threads read neighbouring
+// rows (the partials' layout), and the rows leave through shared memory.
+constexpr int kMergeThreads = 128, kMergeRows = 16;
 template <int HD>
 __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const CachedParams p) {
-  constexpr int kRows = kMergeThreads / (HD / 4);
+  constexpr int N = HD / 4 * kMergeRows / kMergeThreads;  // float4 per thread
+  __shared__ __align__(16) float out[kMergeRows][HD + 4];
   uint32_t bad = 0;
   const CacheDesc& c = p.c;
   const int cta = blockIdx.x;
@@ -482,36 +473,66 @@ __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const 
   const int64_t u0 = split_begin(U, G, cta), u1 = split_begin(U, G, cta + 1);
   const UnitPos pos = locate_unit(c, p.r, p.sp, u1 - 1, bad);
   const SegInfo seg = seg_info(c, p.r, p.sp, pos.s, bad);
-  const int64_t first = u1 - 1 - pos.j, last = first + seg.units - 1;
-  if (first < u0 || last < u1) return;  // begun by another CTA, or finished here
+  const int64_t begin = u1 - 1 - pos.j, last = begin + seg.span - 1;
+  // begun by another CTA (its first unit lies before or behind this CTA's range), or finished here
+  if (begin + p.sp.extra < u0 || begin + p.sp.extra >= u1 || last < u1) return;
   const int c1 = split_owner(U, G, last);
-  const int row = blockIdx.y * kRows + threadIdx.x / (HD / 4), col = (threadIdx.x % (HD / 4)) * 4;
-  const int64_t fr = (int64_t)pos.rt * p.sp.tile_rows + row, tok = fr / p.sp.group;
-  if (row >= p.sp.tile_rows || tok >= seg.v.rows) return;
-  const int64_t pf = part_floats(p.sp.tile_rows, HD);
-  float M = -INFINITY, L = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int R = p.sp.tile_rows, row0 = blockIdx.y * kMergeRows;
+  const int r = threadIdx.x % kMergeRows, row = row0 + r, c4 = threadIdx.x / kMergeRows;
+  const int rows = seg.v.rows * p.sp.group - pos.rt * R;  // of this tile
+  if (row0 >= rows) return;
+  const int64_t pf = part_floats(R, HD);
+  const float* parts = p.part + 2 * (int64_t)cta * pf;
+  auto slot = [&](int x) { return parts + (2 * (int64_t)(x - cta) + (x == cta ? 1 : 0)) * pf; };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int x = cta; x <= c1; ++x) M = fmaxf(M, slot(x)[R * HD + row]);
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  float4 a[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
   for (int x = cta; x <= c1; ++x) {
-    const float* slot = p.part + (2 * (int64_t)x + (x == cta ? 1 : 0)) * pf;
-    const float m = slot[p.sp.tile_rows * HD + row], l = slot[p.sp.tile_rows * (HD + 1) + row];
-    const float4 o = *reinterpret_cast<const float4*>(slot + row * HD + col);
-    const float mn = fmaxf(M, m), base = mn == -INFINITY ? 0.f : mn;
-    const float wa = ex2_approx(M - base), wb = ex2_approx(m - base);
-    M = mn;
-    L = L * wa + l * wb;
-    a.x = a.x * wa + o.x * wb; a.y = a.y * wa + o.y * wb;
-    a.z = a.z * wa + o.z * wb; a.w = a.w * wa + o.w * wb;
+    const float* q = slot(x);
+    const float w = ex2_approx(q[R * HD + row] - base);
+    L = fmaf(w, q[R * (HD + 1) + row], L);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 o = reinterpret_cast<const float4*>(q)[(c4 + i * (kMergeThreads / kMergeRows)) * R + row];
+      a[i].x = fmaf(w, o.x, a[i].x); a[i].y = fmaf(w, o.y, a[i].y);
+      a[i].z = fmaf(w, o.z, a[i].z); a[i].w = fmaf(w, o.w, a[i].w);
+    }
   }
   const float inv = L != 0.f ? 1.f / L : 0.f;
-  a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
-  const int head = pos.h * p.sp.group + (int)(fr - tok * p.sp.group);
-  const int64_t o0 = ((seg.v.row0 + tok) * p.Hq + head) * HD + col;
-  if (p.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o0) = a;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + o0) =
-        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-  if (col == 0)
-    p.LSE[(int64_t)head * p.r.T + seg.v.row0 + tok] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    *reinterpret_cast<float4*>(&out[r][4 * (c4 + i * (kMergeThreads / kMergeRows))]) =
+        make_float4(a[i].x * inv, a[i].y * inv, a[i].z * inv, a[i].w * inv);
+  auto place = [&](int rr, int64_t& at, int& head) {  // packed row and query head of tile row row0 + rr
+    const int fr = pos.rt * R + row0 + rr, tok = fr / p.sp.group;
+    head = pos.h * p.sp.group + fr - tok * p.sp.group;
+    at = seg.v.row0 + tok;
+  };
+  int64_t at;
+  int head;
+  if (c4 == 0 && row < rows) {
+    place(r, at, head);
+    p.LSE[(int64_t)head * p.r.T + at] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int k = threadIdx.x + i * kMergeThreads, rr = k / (HD / 4), col = (k % (HD / 4)) * 4;
+    if (row0 + rr >= rows) continue;
+    place(rr, at, head);
+    const float4 o = *reinterpret_cast<const float4*>(&out[rr][col]);
+    const int64_t o0 = (at * p.Hq + head) * HD + col;
+    if (p.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o0) = o;
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + o0) =
+          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  }
 }
 
 }  // namespace
@@ -528,8 +549,7 @@ cudaError_t launch_cached_small(const CachedParams& p, cudaStream_t st, int* lau
 }
 
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches) {
-  const int rows = kMergeThreads / (p.c.d / 4);
-  const dim3 grid(p.G, (p.sp.tile_rows + rows - 1) / rows);
+  const dim3 grid(p.G, p.sp.tile_rows / kMergeRows);
   if (p.c.d == 128) bdlm_cached_merge_kernel<128><<<grid, kMergeThreads, 0, st>>>(p);
   else bdlm_cached_merge_kernel<64><<<grid, kMergeThreads, 0, st>>>(p);
   ++*launches;

@@ -10,11 +10,16 @@
 // 2^-10 of it, off by at most 2^-18 of it below.)  Scores meet the key
 // blocks' scales in the softmax, one multiplication per block that the
 // exponent's fma absorbs.
-// P V runs in bf16: P needs 8 bits, and the values code * scale (a power of two)
-// are exact in bf16, so a warpgroup turns V's codes into a bf16 tile in shared
-// memory while the tensor cores work on the tile before (16384 values against
-// 32768 exponentials per 128 keys; splitting P in two e4m3 parts instead
-// would triple the exponentials' cost).
+// P V runs in fp16: an e4m3 code is exact in fp16 and one instruction turns
+// two, so a warpgroup converts V's codes, without their scales, while the tensor
+// cores work on the tile before.  The scales join the scores: with log2 of its
+// value block's scale added to a key's score, p' = exp2(s + log2 vs - m) is the
+// weight of the codes themselves, at fp16's precision of the largest weight
+// whatever the scales, and the row sum takes p' / vs: a few operations per
+// block of keys and row.  (In bf16, V's values code * scale cost five
+// instructions for two, as much issue as the softmax; P in two e4m3 parts
+// would triple the exponentials' cost.)  For an fp32 output P goes in two
+// parts, the second what the first's rounding left (own keys: bf16, three).
 //
 // A CTA per SM takes its share of the units of 128 keys (cache.cuh).  Two
 // arrangements of the same roles:
@@ -33,6 +38,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "cached_attn.h"
 #include "ptx.cuh"
 
@@ -40,26 +47,28 @@ namespace bdlm {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRegsControl = 56, kRegsConvert = 72, kRegsSoftmax = 192;
+constexpr int kRegsControl = 72, kRegsConvert = 40, kRegsSoftmax = 200;
 constexpr int kLaunchRegs = 128;
 static_assert(128 * (kRegsControl + kRegsConvert) + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
               "register split exceeds the block");
 constexpr float kRescale = 8.0f;  // log2 units: the reference maximum moves in steps of at least this
+// (fp32 outputs) weights are kept 2^7 larger, up to 2^15: the second part's smallest step, 2^-24, is so much finer
+constexpr float kFineShift = 7.0f;
 constexpr int NK = 3;             // K slots: 128 keys of codes, or one 64-column panel of own keys
 constexpr int NI = 8;             // tile-info slots (more than any two roles are apart)
 constexpr int kSlot = 128 * 128;  // bytes of a K slot, of a V slot and of a bf16 panel
 
 enum { B_QF = 0, B_KF = 2, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + 2, B_WF = B_VE + 2, B_WE = B_WF + 2,
        B_SF = B_WE + 2, B_PF = B_SF + 2, B_OD = B_PF + 2, B_OE = B_OD + 2, B_FD = B_OE + 2, B_P2 = B_FD + 2,
-       B_ML = B_P2 + 2, B_KI = B_ML + 1, B_VI = B_KI + NI, B_COUNT = B_VI + NI };
+       B_ML = B_P2 + 2, B_KI = B_ML + 1, B_PCF = B_KI + NI, B_PCE = B_PCF + 4, B_COUNT = B_PCE + 4 };
 
-struct KInfo {   // what the softmax needs of a tile
-  float s[8];    // scale of each 16 keys
-  int fine;      // scales differ inside 32 keys, or some keys are missing pages
-  int gone;      // bit x: keys 16 x .. 16 x + 15 have no page
-};
-struct VInfo {
-  float s[8];    // 0 where there is no page
+// What the softmax and the conversion need of a tile.  s, lv, iv: K's scale, log2
+// and inverse of V's (1, 0, 1 where there is no page), [0][x] of keys 32 x ..
+// 32 x + 15 and [1][x] of the 16 behind them.
+struct alignas(16) KInfo {
+  float s[2][4], lv[2][4], iv[2][4];
+  int fine;  // scales differ inside 32 keys, or some keys' page is missing
+  int gone;  // bit x: the page of keys 16 x .. 16 x + 15 is missing
 };
 
 template <int HD>
@@ -68,80 +77,67 @@ struct Lay {
   static constexpr int kQBytes = 128 * HD * 2;
   static constexpr int kK = 2 * kQBytes;
   static constexpr int kV = kK + NK * kSlot;      // codes of V, 2 slots
-  static constexpr int kW = kV + 2 * kSlot;       // bf16 V, 2 slots of HD / 64 panels
+  static constexpr int kW = kV + 2 * kSlot;       // fp16 (own keys: bf16) V, 2 slots of HD / 64 panels
   static constexpr int kWBytes = kSlot * (HD / 64);
   static constexpr int kBar = kW + 2 * kWBytes;
-  static constexpr int kKI = kBar + ((8 * B_COUNT + 16 + 15) & ~15);
-  static constexpr int kVI = kKI + NI * (int)sizeof(KInfo);
-  static constexpr int kML = kVI + NI * (int)sizeof(VInfo);
+  static constexpr int kKI = kBar + ((8 * B_COUNT + 8 + 15) & ~15);
+  static constexpr int kML = kKI + NI * (int)sizeof(KInfo);
   static constexpr int kCQ = kML + 2 * 128 * 8;
-  static constexpr int kBytes = kCQ + 128 * 4;
+  static constexpr int kPC = kCQ + 128 * 4;
+  static constexpr int kBytes = kPC + 4 * 64;
   // 1024 bytes to align; at least 120 KB so that no second CTA shares the SM (each holds all of TMEM)
   static constexpr int kAlloc = kBytes + 1024 > 120 * 1024 ? kBytes + 1024 : 120 * 1024;
 };
 static_assert(Lay<128>::kAlloc <= 232448, "shared memory");
 
-// One CTA's share of a segment.
+// One CTA's share of a segment, as the roles read it from a ring in shared
+// memory (warp 3 fills it, so that no other role carries the walk over the
+// segments in its registers).
 struct Piece {
-  UnitPos pos;
-  SegInfo seg;
-  int nk, k0;   // cached tiles, the first
-  int nl, l0;   // own tiles, the first
-  bool whole, first;
+  int64_t row0;        // the sequence's first row
+  int s, h, rt;        // sequence, KV head, row tile
+  int len, rows;       // cached tokens and new rows of the sequence
+  int nk, k0;          // cached tiles, the first; nk = -1: no more pieces
+  int nl, l0;          // own tiles, the first
+  int whole, first;    // the whole segment; its beginning
 };
+constexpr int NP = 4;  // ring slots
 
-struct PieceIter {
-  int64_t u, u1;
-  UnitPos pos;
-  SegInfo seg;
-};
-
-// By a whole warp.
-__device__ __forceinline__ PieceIter piece_begin(const CachedParams& p, uint32_t& bad) {
-  PieceIter it;
-  const int64_t U = total_units(p.c, p.r, p.sp, bad);
-  const int G = split_ctas(U, p.G), cta = blockIdx.x;
-  it.u = it.u1 = 0;
-  if (cta < G) {
-    it.u = split_begin(U, G, cta);
-    it.u1 = split_begin(U, G, cta + 1);
-    it.pos = locate_unit(p.c, p.r, p.sp, it.u, bad);
-    it.seg = seg_info(p.c, p.r, p.sp, it.pos.s, bad);
-  }
-  return it;
+// Shared-memory descriptors (see sdesc_sw128) as their two words: the upper
+// one is a constant of the layout, the lower one the start address (and, for an
+// MN-major operand, the panel stride), so that the issuing thread holds one
+// register per operand.  128-byte (SW = 2) or 64-byte (SW = 4) swizzle.
+__host__ __device__ constexpr uint32_t desc_hi(int sw, int sbo) {
+  return (uint32_t)(sbo >> 4) | (1u << 14) | ((uint32_t)sw << 29);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, int lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(lbo >> 4) << 16);
 }
 
-// By any thread.
-__device__ __forceinline__ bool piece_next(const CachedParams& p, PieceIter& it, Piece& pc, uint32_t& bad) {
-  if (it.u >= it.u1) return false;
-  const int jb = it.pos.j, je = (int)imin64(it.seg.units, jb + (it.u1 - it.u));
-  pc.pos = it.pos;
-  pc.seg = it.seg;
-  const int kt = it.seg.ktiles;
-  pc.k0 = jb;
-  pc.nk = max(min(je, kt) - jb, 0);
-  pc.l0 = max(jb - kt, 0);
-  pc.nl = it.seg.ltiles > 0 ? max(je - kt, 0) - pc.l0 : (p.sp.local && je == it.seg.units ? 1 : 0);
-  pc.first = jb == 0;
-  pc.whole = jb == 0 && je == it.seg.units;
-  it.u += je - jb;
-  if (it.u < it.u1) next_segment(p.c, p.r, p.sp, it.pos, it.seg, bad);
-  return true;
+// D[tmem] (+)= A[smem] B[smem]: e4m3, K = 32 (F8), or bf16, K = 16.
+template <bool F8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
+                                       uint32_t idesc, uint32_t acc) {
+  if (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
+        : "memory");
 }
-
-// 128-byte (SW = 2) or 64-byte (SW = 4) swizzled operand; see sdesc_sw128.
-template <int SW>
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | ((uint64_t)SW << 61);
-}
-
-// D[tmem] (+)= A[smem] B[smem], e4m3 in, fp32 accumulator, K = 32.
-__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A[tmem] B[smem], 16-bit types, K = 16.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // fp32 accumulator, e4m3 A and B (format 0), both K-major.
@@ -155,12 +151,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-
 __device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
   float u[10];
 #pragma unroll
@@ -176,36 +166,58 @@ __device__ __forceinline__ void mask32(uint32_t (&a)[32], int hi) {
     if (c >= hi) a[c] = __float_as_uint(-INFINITY);
 }
 
-// p = exp2(s f - m) of 32 scores in place; returns their sum.
-__device__ __forceinline__ float exp32(uint32_t (&a)[32], float f, float nm) {
-  const uint64_t f2x = f2(f, f), n2 = f2(nm, nm);
-  float r0 = 0.f, r1 = 0.f;
+// 32 scores of two key blocks of unlike scales: times their factors, plus
+// their shifts, or -inf where a block's page is missing.
+__device__ __forceinline__ void scores16(uint32_t (&a)[32], float f, float lf, float g, float lg, int gone) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    const float x = fmaf(__uint_as_float(a[c]), c < 16 ? f : g, c < 16 ? lf : lg);
+    a[c] = (gone >> (c >> 4)) & 1 ? __float_as_uint(-INFINITY) : __float_as_uint(x);
+  }
+}
+
+// p = exp2(s f + n) of 32 scores in place, and the sums of the first and the last 16.
+__device__ __forceinline__ void exp32(uint32_t (&a)[32], float f, float n, float& s0, float& s1) {
+  const uint64_t f2x = f2(f, f), n2 = f2(n, n);
+  uint64_t r[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     float x0, x1;
     f2_split(f2_fma(f2(__uint_as_float(a[c]), __uint_as_float(a[c + 1])), f2x, n2), x0, x1);
     x0 = ex2_approx(x0);
     x1 = ex2_approx(x1);
-    r0 += x0;
-    r1 += x1;
+    r[c >> 4] = f2_add(r[c >> 4], f2(x0, x1));
     a[c] = __float_as_uint(x0);
     a[c + 1] = __float_as_uint(x1);
   }
-  return r0 + r1;
+  float x, y;
+  f2_split(r[0], x, y);
+  s0 = x + y;
+  f2_split(r[1], x, y);
+  s1 = x + y;
 }
 
-// Packs 32 values to bf16 at 16 columns of TMEM; REST: the values become what the rounding left.
-template <bool REST>
+// P lies over the S columns that it replaces, 32 keys by 32 keys: 16 packed
+// columns, then 16 of the second part (FINE).  Column of the 16 keys of PV
+// k-step kk:
+__device__ __forceinline__ uint32_t p_col(int kk) { return (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8); }
+
+// Packs 32 values to fp16 (bf16) at 16 columns of TMEM; REST: the values become what the rounding left.
+template <bool BF, bool REST>
 __device__ __forceinline__ void store_p(uint32_t (&a)[32], uint32_t taddr) {
   uint32_t pk[16];
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     const float x = __uint_as_float(a[c]), y = __uint_as_float(a[c + 1]);
-    const uint32_t w = pack_bf16x2(x, y);
+    uint32_t w;
+    if (BF) w = pack_bf16x2(x, y);
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
     pk[c / 2] = w;
     if (REST) {
-      a[c] = __float_as_uint(x - __uint_as_float(w << 16));
-      a[c + 1] = __float_as_uint(y - __uint_as_float(w & 0xffff0000u));
+      const float2 z = BF ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                          : __half22float2(*reinterpret_cast<const __half2*>(&w));
+      a[c] = __float_as_uint(x - z.x);
+      a[c + 1] = __float_as_uint(y - z.y);
     }
   }
   tmem_st16(taddr, pk);
@@ -228,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bp + LY::kBar + 8 * B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bp + LY::kBar + 8 * B_COUNT + 4);
   KInfo* kinfo = reinterpret_cast<KInfo*>(bp + LY::kKI);
-  VInfo* vinfo = reinterpret_cast<VInfo*>(bp + LY::kVI);
   // split only: both sub-tiles' states of the rows, and the rows' score factors
   float2* ml = reinterpret_cast<float2*>(bp + LY::kML);  // [2][128]
   float* row_cq = reinterpret_cast<float*>(bp + LY::kCQ);
+  Piece* pieces = reinterpret_cast<Piece*>(bp + LY::kPC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -253,10 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(B_P2 + i), 128);
     }
     mbar_init(BAR(B_ML), 256);
-    for (int i = 0; i < NI; ++i) {
-      mbar_init(BAR(B_KI + i), 1);
-      mbar_init(BAR(B_VI + i), 1);
+    for (int i = 0; i < NP; ++i) {
+      mbar_init(BAR(B_PCF + i), 1);
+      mbar_init(BAR(B_PCE + i), 32 + 32 + 1 + 256 + 128);  // K and V loader, MMA thread, softmax, conversion
     }
+    for (int i = 0; i < NI; ++i) mbar_init(BAR(B_KI + i), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -270,58 +283,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{p.status, p.limit_ns, abort_flag};
   const CacheDesc& c = p.c;
-  uint32_t bad = 0;
+  // the n-th piece (null: none left, or gave up); its slot stays this thread's until done(n)
+  auto piece = [&](uint32_t n) -> const Piece* {
+    if (!mbar_wait(BAR(B_PCF + (n % NP)), (n / NP) & 1, wd, 10)) return nullptr;
+    const Piece* q = pieces + n % NP;
+    return q->nk < 0 ? nullptr : q;
+  };
+  auto done = [&](uint32_t n) { mbar_arrive(BAR(B_PCE + (n % NP))); };
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsControl>();
-    if (warp == 0 || warp == 2) {
+    auto load = [&](auto is_v) {
       // ---------------------------------------------- loaders: K (warp 0), V (warp 2)
-      // Lane 8 a + x looks up the page and scale of keys 16 x of tile a of a
-      // batch of 4 tiles; the lookups of the next batch are in flight while
-      // this one is loaded.
-      const bool isV = warp == 2;
-      const float* scales = isV ? c.vs : c.ks;
-      PieceIter it = piece_begin(p, bad);
-      Piece pc;
+      // Lane 8 a + x looks up the page (K's loader: and the scales) of keys
+      // 16 x of tile a of a batch of 4 tiles; the lookups of the next batch are
+      // in flight while this one is loaded.
+      constexpr bool isV = decltype(is_v)::value;
+      uint32_t bad = 0;
       uint32_t slot = 0, sph = 1, tc = 0;  // slot and its phase parity to wait for, tiles so far
-      const int nslots = isV ? 2 : NK;
+      constexpr int nslots = isV ? 2 : NK;
       bool ok = true;
-      while (ok && piece_next(p, it, pc, bad)) {
-        const int len = pc.seg.v.len;
+      for (uint32_t np = 0; ok; ++np) {
+        const Piece* pp = piece(np);
+        if (__any_sync(0xffffffffu, pp == nullptr)) break;
+        const int len = pp->len, nk = pp->nk, k0 = pp->k0, h = pp->h;
+        const int32_t* table = c.table + (int64_t)pp->s * c.max_pages;
         auto lookup = [&](int b) {  // page of this lane's 16 keys of batch b, -1: none
-          const int tile = 4 * b + (lane >> 3), key = (pc.k0 + tile) * kUnit + 16 * (lane & 7);
-          return tile < pc.nk && key < len ? page_id(c, pc.pos.s, key >> c.lp, bad) : -1;
+          const int tile = 4 * b + (lane >> 3), key = (k0 + tile) * kUnit + 16 * (lane & 7);
+          if (tile >= nk || key >= len) return -1;
+          const int id = __ldg(table + (key >> c.lp));
+          if (id >= 0 && id < c.n_pages) return id;
+          bad |= kStatusBadPage;
+          return -1;
         };
-        auto scale_of = [&](int id) { return id >= 0 ? __ldg(scales + (int64_t)id * c.Hkv + pc.pos.h) : 0.f; };
+        auto scale_of = [&](const float* sc, int id) { return id >= 0 ? __ldg(sc + (int64_t)id * c.Hkv + h) : 1.f; };
         int id = lookup(0), id1 = lookup(1);
-        float sc = scale_of(id);
-        for (int b = 0; ok && 4 * b < pc.nk; ++b) {
-          const float sc1 = scale_of(id1);
+        float sk = 1.f, sv = 1.f, sk1 = 1.f, sv1 = 1.f;
+        if (!isV) sk = scale_of(c.ks, id), sv = scale_of(c.vs, id);
+        for (int b = 0; ok && 4 * b < nk; ++b) {
+          if (!isV) sk1 = scale_of(c.ks, id1), sv1 = scale_of(c.vs, id1);
           const int id2 = lookup(b + 2);
-          for (int a = 0; a < 4 && 4 * b + a < pc.nk; ++a, ++tc) {
-            const int key0 = (pc.k0 + 4 * b + a) * kUnit;
+          for (int a = 0; a < 4 && 4 * b + a < nk; ++a, ++tc) {
+            const int key0 = (k0 + 4 * b + a) * kUnit;
             ok = mbar_wait(BAR((isV ? B_VE : B_KE) + slot), sph, wd, 20 + warp);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const int x = lane & 7;
             const int cid = __shfl_sync(0xffffffffu, id, 8 * a + x);
-            const float csc = __shfl_sync(0xffffffffu, sc, 8 * a + x);
             const unsigned none = __ballot_sync(0xffffffffu, cid < 0) & 0xffu;
             const uint32_t fb = BAR((isV ? B_VF : B_KF) + slot);
-            if (isV) {
-              if (lane < 8) vinfo[tc % NI].s[x] = csc;
-            } else {
-              const float peer = __shfl_xor_sync(0xffffffffu, csc, 1);
+            if (!isV) {
+              const float ck = __shfl_sync(0xffffffffu, sk, 8 * a + x), cv = __shfl_sync(0xffffffffu, sv, 8 * a + x);
+              const float pk = __shfl_xor_sync(0xffffffffu, ck, 1), pv = __shfl_xor_sync(0xffffffffu, cv, 1);
               const unsigned gone = __ballot_sync(0xffffffffu, cid < 0 && key0 + 16 * x < len) & 0xffu;
-              const unsigned odd = __ballot_sync(0xffffffffu, cid >= 0 && key0 + 16 * (x | 1) < len && csc != peer) & 0xffu;
-              if (lane < 8) kinfo[tc % NI].s[x] = csc;
-              if (lane == 0) {
-                kinfo[tc % NI].fine = (gone | odd) != 0;
-                kinfo[tc % NI].gone = (int)gone;
+              const unsigned odd = __ballot_sync(0xffffffffu, key0 + 16 * (x | 1) < len && (ck != pk || cv != pv)) & 0xffu;
+              KInfo& ki = kinfo[tc % NI];
+              if (lane < 8) {
+                ki.s[x & 1][x >> 1] = ck;
+                ki.lv[x & 1][x >> 1] = log2f(cv);
+                ki.iv[x & 1][x >> 1] = 1.f / cv;
               }
+              if (lane == 0) {
+                ki.fine = (gone | odd) != 0;
+                ki.gone = (int)gone;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(BAR(B_KI + tc % NI));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR((isV ? B_VI : B_KI) + tc % NI));
             // pages of the tile that hold keys: lane q loads page q
             const int per = kUnit >> c.lp, step = c.page >> 4;  // pages per tile, 16-key groups per page
             int n = 0;
@@ -334,22 +362,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pid = __shfl_sync(0xffffffffu, cid, (lane * step) & 7);
             if (lane < per && pid >= 0) {
               const uint32_t dst = base + (isV ? LY::kV : LY::kK) + slot * kSlot + lane * c.page * HD;
-              const int64_t blk = (int64_t)pid * c.Hkv + pc.pos.h;
+              const int64_t blk = (int64_t)pid * c.Hkv + h;
               if (isV) bulk_load(dst, c.v8 + blk * c.page * HD, (uint32_t)(c.page * HD), fb);
               else tma_load_3d(dst, &tK8, fb, 0, 0, (int)blk);
             }
             if (++slot == (uint32_t)nslots) slot = 0, sph ^= 1;
           }
-          id = id1; id1 = id2; sc = sc1;
+          id = id1; id1 = id2; sk = sk1; sv = sv1;
         }
         // own tiles: K by panels through the K slots; V straight into the bf16 slot that its tile has
-        for (int l = 0; ok && l < pc.nl; ++l, ++tc) {
-          const int row = (int)(pc.seg.v.row0 + (int64_t)(pc.l0 + l) * kUnit);
-          if (lane == 0) {
-            if (!isV)
-              for (int x = 0; x < 8; ++x) kinfo[tc % NI].s[x] = 1.f;
-            if (!isV) kinfo[tc % NI].fine = kinfo[tc % NI].gone = 0;
-            mbar_arrive(BAR((isV ? B_VI : B_KI) + tc % NI));
+        const int nl = pp->nl;
+        for (int l = 0; ok && l < nl; ++l, ++tc) {
+          const int row = (int)(pp->row0 + (int64_t)(pp->l0 + l) * kUnit);
+          if (!isV) {
+            KInfo& ki = kinfo[tc % NI];
+            if (lane < 4) ki.s[0][lane] = ki.iv[0][lane] = 1.f, ki.lv[0][lane] = 0.f;
+            if (lane == 0) ki.fine = ki.gone = 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(B_KI + tc % NI));
           }
           if (isV) {
             ok = mbar_wait(BAR(B_VE + slot), sph, wd, 24);
@@ -359,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               mbar_arrive_expect_tx(BAR(B_VF + slot), LY::kWBytes);
               for (int pn = 0; pn < KP; ++pn)
-                tma_load_3d(base + LY::kW + slot * LY::kWBytes + pn * kSlot, &tV, BAR(B_VF + slot), 64 * pn, pc.pos.h, row);
+                tma_load_3d(base + LY::kW + slot * LY::kWBytes + pn * kSlot, &tV, BAR(B_VF + slot), 64 * pn, h, row);
             }
             slot ^= 1;
             if (slot == 0) sph ^= 1;
@@ -370,120 +400,185 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               if (lane == 0) {
                 mbar_arrive_expect_tx(BAR(B_KF + slot), kSlot);
-                tma_load_3d(base + LY::kK + slot * kSlot, &tK, BAR(B_KF + slot), 64 * pn, pc.pos.h, row);
+                tma_load_3d(base + LY::kK + slot * kSlot, &tK, BAR(B_KF + slot), 64 * pn, h, row);
               }
               if (++slot == NK) slot = 0, sph ^= 1;
             }
           }
         }
+        done(np);
       }
       if (bad) atomicOr(p.status, bad);
+    };
+    if (warp == 0) {
+      load(std::false_type{});
+    } else if (warp == 2) {
+      load(std::true_type{});
+    } else if (warp == 3) {
+      // ---------------------------------------------- walk over the CTA's pieces
+      uint32_t bad = 0;
+      const int64_t U = total_units(c, p.r, p.sp, bad);
+      const int G = split_ctas(U, p.G), cta = blockIdx.x;
+      int64_t u = 0, u1 = 0;
+      UnitPos pos{0, 0, 0, 0};
+      SegInfo seg;
+      if (cta < G) {
+        u = split_begin(U, G, cta);
+        u1 = split_begin(U, G, cta + 1);
+        pos = locate_unit(c, p.r, p.sp, u, bad);
+        seg = seg_info(c, p.r, p.sp, pos.s, bad);
+      }
+      if (lane == 0) {
+        for (uint32_t n = 0;; ++n) {
+          if (n >= NP && !mbar_wait(BAR(B_PCE + n % NP), (n / NP - 1) & 1, wd, 11)) break;
+          Piece& q = pieces[n % NP];
+          if (u >= u1) {
+            q.nk = -1;
+            mbar_arrive(BAR(B_PCF + n % NP));
+            break;
+          }
+          int jb, je;
+          split_units(seg, p.sp, pos, u, u1, jb, je);
+          u += seg.span - pos.j;
+          if (je == 0) {  // only the segment's opening lies here: the next CTA begins it
+            q.nk = -1;
+            mbar_arrive(BAR(B_PCF + n % NP));
+            break;
+          }
+          const int kt = seg.ktiles;
+          q.row0 = seg.v.row0;
+          q.s = pos.s; q.h = pos.h; q.rt = pos.rt;
+          q.len = seg.v.len; q.rows = seg.v.rows;
+          q.k0 = jb;
+          q.nk = max(min(je, kt) - jb, 0);
+          q.l0 = max(jb - kt, 0);
+          q.nl = seg.ltiles > 0 ? max(je - kt, 0) - q.l0 : (p.sp.local && je == seg.units ? 1 : 0);
+          q.first = jb == 0;
+          q.whole = jb == 0 && je == seg.units;
+          mbar_arrive(BAR(B_PCF + n % NP));
+          if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
+        }
+        if (bad) atomicOr(p.status, bad);
+      }
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issue
-      PieceIter it = piece_begin(p, bad);
       if (lane == 0) {
         constexpr uint32_t kId8 = idesc_e4m3(128, 128);
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
-        constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true);
-        Piece pc;
+        constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true);    // own keys
+        constexpr uint32_t kIdO16 = kIdO & ~((1u << 7) | (1u << 10));  // cached keys: fp16 P and V
         uint32_t ks = 0, kph = 0;            // next K slot and its full parity
-        uint32_t qph[2] = {0, 0};            // parity of Q's next full phase (split: of Q8, of bf16 Q)
+        // bit t of a mask: the parity of sub-tile t's next phase (in pairs both bits are equal, bit 0 alone is kept)
+        uint32_t qph = 0;                    // Q (split: bit 0 of Q8, bit 1 of bf16 Q)
+        uint32_t pph = 0;                    // P
+        uint32_t oph = 3;                    // O left by the last piece (first wait passes)
+        uint32_t p2 = 0;                     // third part of P
         uint32_t wc = 0;                     // V tiles multiplied so far
-        uint32_t st[2] = {0, 0};             // tiles of each sub-tile so far
-        uint32_t itn[2] = {0, 0};            // pieces of each sub-tile so far
+        auto bit = [](uint32_t m, int t) { return (m >> (KS ? t : 0)) & 1; };
+        auto flip = [](uint32_t& m, int t) {
+          if (KS || t == 1) m ^= 1u << (KS ? t : 0);  // pairs: sub-tile 1 comes last
+        };
         bool ok = true;
-        // slots of the tile whose S is being issued; waits for its keys
-        uint32_t cur[2], ncur = 0;
+        uint32_t k0 = 0, k1 = 0;             // slots of the tile whose S is being issued
+        // the tile's keys are there
         auto take_k = [&](bool own) {
-          ncur = own ? KP : 1;
-          for (uint32_t i = 0; i < ncur; ++i) {
-            cur[i] = ks;
+          k0 = ks;
+          if (!mbar_wait(BAR(B_KF + ks), kph, wd, 30)) return false;
+          if (++ks == NK) ks = 0, kph ^= 1;
+          if (KP == 2 && own) {
+            k1 = ks;
             if (!mbar_wait(BAR(B_KF + ks), kph, wd, 30)) return false;
             if (++ks == NK) ks = 0, kph ^= 1;
           }
           tc_fence_after();
           return true;
         };
-        auto free_k = [&]() {
-          for (uint32_t i = 0; i < ncur; ++i) tc_commit(BAR(B_KE + cur[i]));
+        auto free_k = [&](bool own) {
+          tc_commit(BAR(B_KE + k0));
+          if (KP == 2 && own) tc_commit(BAR(B_KE + k1));
         };
         auto issue_s = [&](int t, bool own) {
+          const uint32_t d = tmem + t * 128;
           if (!own) {
-            const uint32_t q = base + LY::kQ + (KS ? 0 : t) * LY::kQBytes;
-            const uint64_t hi = sdesc<SWQ>(q, 16, SBO8), lo = sdesc<SWQ>(q + 128 * HD, 16, SBO8);
-            const uint64_t k = sdesc<SWQ>(base + LY::kK + cur[0] * kSlot, 16, SBO8);
+            constexpr uint32_t H = desc_hi(SWQ, SBO8);
+            const uint32_t q = desc_lo(base + LY::kQ + (KS ? 0 : t) * LY::kQBytes, 16);
+            const uint32_t k = desc_lo(base + LY::kK + k0 * kSlot, 16);
 #pragma unroll
-            for (int kk = 0; kk < HD / 32; ++kk) tc_mma_f8(tmem + t * 128, desc_add(hi, kk * 32), desc_add(k, kk * 32), kId8, kk > 0);
+            for (int kk = 0; kk < HD / 32; ++kk) mma_ss<true>(d, q + kk * 2, H, k + kk * 2, H, kId8, kk > 0);
 #pragma unroll
-            for (int kk = 0; kk < HD / 32; ++kk) tc_mma_f8(tmem + t * 128, desc_add(lo, kk * 32), desc_add(k, kk * 32), kId8, 1);
+            for (int kk = 0; kk < HD / 32; ++kk) mma_ss<true>(d, q + 8 * HD + kk * 2, H, k + kk * 2, H, kId8, 1);
           } else {
-            const uint32_t q = base + LY::kQ + (KS ? 1 : t) * LY::kQBytes;
+            constexpr uint32_t H = desc_hi(2, 1024);
 #pragma unroll
             for (int pn = 0; pn < KP; ++pn) {
-              const uint64_t a = sdesc_sw128(q + pn * kSlot, 16, 1024);
-              const uint64_t k = sdesc_sw128(base + LY::kK + cur[pn] * kSlot, 16, 1024);
+              const uint32_t q = desc_lo(base + LY::kQ + (KS ? 1 : t) * LY::kQBytes + pn * kSlot, 16);
+              const uint32_t k = desc_lo(base + LY::kK + (pn ? k1 : k0) * kSlot, 16);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ss(tmem + t * 128, desc_add(a, kk * 32), desc_add(k, kk * 32), kIdS, (pn | kk) > 0);
+              for (int kk = 0; kk < 4; ++kk) mma_ss<false>(d, q + kk * 2, H, k + kk * 2, H, kIdS, (pn | kk) > 0);
             }
           }
           tc_commit(BAR(B_SF + t));
         };
         // O_t += P_t V of V tile w
-        auto pv = [&](int t, uint32_t w, uint32_t col, bool first) {
-          const uint64_t v = sdesc_sw128(base + LY::kW + (w & 1) * LY::kWBytes, kSlot, 1024);
+        // (col: 0 the first part of P, 16 the second)
+        auto pv = [&](int t, uint32_t w, uint32_t col, bool own, bool first) {
+          const uint32_t v = desc_lo(base + LY::kW + (w & 1) * LY::kWBytes, kSlot);
+          const uint32_t id = own ? kIdO : kIdO16;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + col + kk * 8, desc_add(v, kk * 2048), kIdO,
-                      (kk > 0 || !first) ? 1u : 0u);
+            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + col + p_col(kk), v + kk * 128, desc_hi(2, 1024), id,
+                   (kk > 0 || !first) ? 1u : 0u);
         };
-        auto issue_pv = [&](int t, uint32_t w, bool first) {
-          if (!mbar_wait(BAR(B_PF + t), st[t] & 1, wd, 31)) return false;
-          if (first && itn[t] > 0 && !mbar_wait(BAR(B_OE + t), (itn[t] - 1) & 1, wd, 32)) return false;
+        auto issue_pv = [&](int t, uint32_t w, bool own, bool first) {
+          if (!mbar_wait(BAR(B_PF + t), bit(pph, t), wd, 31)) return false;
+          flip(pph, t);
+          if (first) {
+            if (!mbar_wait(BAR(B_OE + t), bit(oph, t), wd, 32)) return false;
+            flip(oph, t);
+          }
           if (!mbar_wait(BAR(B_WF + (w & 1)), (w >> 1) & 1, wd, 33)) return false;
           tc_fence_after();
-          pv(t, w, 0, first);
-          if (FINE) {
-            pv(t, w, 64, false);
+          pv(t, w, 0, own, first);
+          if (FINE) pv(t, w, 16, own, false);
+          if (FINE && own) {
             tc_commit(BAR(B_FD + t));
-            if (!mbar_wait(BAR(B_P2 + t), st[t] & 1, wd, 34)) return false;
+            if (!mbar_wait(BAR(B_P2 + t), bit(p2, t), wd, 34)) return false;
+            flip(p2, t);
             tc_fence_after();
-            pv(t, w, 0, false);
+            pv(t, w, 0, true, false);
           }
-          ++st[t];
           return true;
         };
-        while (ok && piece_next(p, it, pc, bad)) {
-          const int n = pc.nk + pc.nl;
+        for (uint32_t np = 0; ok; ++np) {
+          const Piece* pp = piece(np);
+          if (!pp) break;
+          const int nk = pp->nk, n = nk + pp->nl;
+          done(np);
           if (n == 0) continue;
-          auto own = [&](int j) { return j >= pc.nk; };
+          auto own = [&](int j) { return j >= nk; };
           // Q of sub-tile t (split: of kind t) has to be there before the first tile of each kind
           auto wait_q = [&](int t) {
-            const bool r = mbar_wait(BAR(B_QF + t), qph[t], wd, 35);
-            qph[t] ^= 1;
+            const bool r = mbar_wait(BAR(B_QF + t), bit(qph, t), wd, 35);
+            flip(qph, t);
             if (r) tc_fence_after();
             return r;
           };
           if (KS) {
             auto start_s = [&](int j) {
-              if ((j == 0 || j == pc.nk) && !wait_q(own(j) ? 1 : 0)) return false;
+              if ((j == 0 || j == nk) && !wait_q(own(j) ? 1 : 0)) return false;
               if (!take_k(own(j))) return false;
               issue_s(j & 1, own(j));
-              free_k();
+              free_k(own(j));
               return true;
             };
             ok = start_s(0) && (n < 2 || start_s(1));
             for (int j = 0; ok && j < n; ++j, ++wc) {
               const int t = j & 1;
-              ok = issue_pv(t, wc, j < 2);
+              ok = issue_pv(t, wc, own(j), j < 2);
               if (!ok) break;
               tc_commit(BAR(B_WE + (wc & 1)));
-              if (j + 2 >= n) {
-                tc_commit(BAR(B_OD + t));
-                ++itn[t];
-              } else {
-                ok = start_s(j + 2);
-              }
+              if (j + 2 >= n) tc_commit(BAR(B_OD + t));
+              else ok = start_s(j + 2);
             }
           } else {
             ok = wait_q(0) && take_k(own(0));
@@ -491,11 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && wait_q(1);
             if (ok) {
               issue_s(1, own(0));
-              free_k();
+              free_k(own(0));
             }
             for (int j = 0; ok && j < n; ++j, ++wc) {
-              const bool last = j == n - 1, swap = j + 1 == pc.nk && pc.nk > 0 && !last;
-              ok = issue_pv(0, wc, j == 0);
+              const bool last = j == n - 1, swap = j + 1 == nk && !last;
+              ok = issue_pv(0, wc, own(j), j == 0);
               if (!ok) break;
               if (last) tc_commit(BAR(B_OD + 0));
               if (!last) {
@@ -503,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 issue_s(0, own(j + 1));
               }
-              ok = issue_pv(1, wc, j == 0);
+              ok = issue_pv(1, wc, own(j), j == 0);
               if (!ok) break;
               tc_commit(BAR(B_WE + (wc & 1)));
               if (last) {
@@ -512,11 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = !swap || wait_q(1);
                 if (!ok) break;
                 issue_s(1, own(j + 1));
-                free_k();
+                free_k(own(j + 1));
               }
             }
-            ++itn[0];
-            ++itn[1];
           }
         }
       }
@@ -528,55 +621,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + tl + t * 128, tO = tmem + tl + 256;
-    PieceIter it = piece_begin(p, bad);
-    Piece pc;
-    uint32_t sc = 0, tcount = 0, itn[2] = {0, 0}, mlc = 0, q8c = 0;
+    uint32_t sc = 0, tcount = 0, itn[2] = {0, 0}, mlc = 0, q8c = 0, p2 = 0;
     bool ok = true;
-    while (ok && piece_next(p, it, pc, bad)) {
-      const int n = pc.nk + pc.nl;
-      const int64_t fr = (int64_t)pc.pos.rt * kTileRows + (KS ? 0 : t * 128) + row;
-      const int64_t tok = fr / p.sp.group;
-      const bool live = tok < pc.seg.v.rows;
-      const int head = pc.pos.h * p.sp.group + (int)(fr - tok * p.sp.group);
-      const int64_t grow = pc.seg.v.row0 + (live ? tok : 0);
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q) + (grow * p.Hq + head) * HD;
+    for (uint32_t np = 0; ok; ++np) {
+      const Piece* pp = piece(np);
+      if (__any_sync(0xffffffffu, pp == nullptr)) break;
+      const int nk = pp->nk, nl = pp->nl, n = nk + nl;
+      // this thread's row: its token and query head (worked out again where it is needed)
+      struct Row {
+        int64_t at;  // row of the packed tensors
+        int head;
+        bool live;
+      };
+      auto my_row = [&]() {
+        const int fr = pp->rt * kTileRows + (KS ? 0 : t * 128) + row, tok = fr / p.sp.group;
+        Row r;
+        r.live = tok < pp->rows;
+        r.head = pp->h * p.sp.group + fr - tok * p.sp.group;
+        r.at = pp->row0 + (r.live ? tok : 0);
+        return r;
+      };
       float cq = p.sl2;
 
       // Q's row to shared memory: e4m3 in two parts, or bf16
       auto put_q8 = [&]() {
+        const Row r = my_row();
+        const bool live = r.live;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q) + (r.at * p.Hq + r.head) * HD;
         const uint32_t dst = base + LY::kQ + (KS ? 0 : t) * LY::kQBytes;
-        uint32_t amax = 0;
+        uint32_t w[HD / 2], amax = 0;
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i) {
           const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
         }
+#pragma unroll
+        for (int i = 0; i < HD / 2; ++i) amax = max(amax, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
         int e = 7 + 127 - (int)(amax >> 7);
         if (amax >= 0x7f80u || amax == 0) e = 0;
-        const bool nan = amax >= 0x7f80u;  // e4m3 has no infinity: a row that is not finite reads NaN
         e = min(e, 126);
-        const float f = nan ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e + 127) << 23);
+        // e4m3 has no infinity: a row that is not finite reads NaN
+        const float f = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e + 127) << 23);
         cq = p.sl2 * __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 2
+#pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q) + 2 * i + y) : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(w[k] << 16) * f, b = __uint_as_float(w[k] & 0xffff0000u) * f;
-              h[k] = to_e4m3x2(a, b);
-              const uint32_t hh = e4m3x2_to_half2(h[k]);
-              const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-              l[k] = to_e4m3x2(a - r.x, b - r.y);
-            }
-            hi[2 * y] = h[0] | h[1] << 16; hi[2 * y + 1] = h[2] | h[3] << 16;
-            lo[2 * y] = l[0] | l[1] << 16; lo[2 * y + 1] = l[2] | l[3] << 16;
+          for (int k = 0; k < 8; ++k) {
+            // (in fp16 the scaled values are exact down to 2^-24, below e4m3's smallest step)
+            const __half2 v = __floats2half2_rn(__uint_as_float(w[8 * i + k] << 16) * f,
+                                                __uint_as_float(w[8 * i + k] & 0xffff0000u) * f);
+            const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t back = e4m3x2_to_half2(h);
+            const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
+            const uint32_t l = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(d), __NV_SATFINITE, __NV_E4M3);
+            hi[k >> 1] = k & 1 ? hi[k >> 1] | h << 16 : h;
+            lo[k >> 1] = k & 1 ? lo[k >> 1] | l << 16 : l;
           }
           const uint32_t at = HD == 128 ? (uint32_t)(row * 128 + ((i ^ (row & 7)) << 4))
                                         : (uint32_t)(row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
@@ -585,6 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto put_q16 = [&]() {
+        const Row r = my_row();
+        const bool live = r.live;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q) + (r.at * p.Hq + r.head) * HD;
         const uint32_t dst = base + LY::kQ + (KS ? 1 : t) * LY::kQBytes;
 #pragma unroll 4
         for (int i = 0; i < HD / 8; ++i) {
@@ -595,19 +698,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0) {
         if (KS) {
           // sub-tile 0's threads write the codes, sub-tile 1's the bf16 rows
-          if (t == 0 && pc.nk > 0) {
+          if (t == 0 && nk > 0) {
             put_q8();
             row_cq[row] = cq;
             fence_proxy_async_smem();
             mbar_arrive(BAR(B_QF + 0));
           }
-          if (t == 1 && pc.nl > 0) {
+          if (t == 1 && nl > 0) {
             put_q16();
             fence_proxy_async_smem();
             mbar_arrive(BAR(B_QF + 1));
           }
         } else {
-          if (pc.nk > 0) put_q8();
+          if (nk > 0) put_q8();
           else put_q16();
           fence_proxy_async_smem();
           mbar_arrive(BAR(B_QF + t));
@@ -615,11 +718,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m_ref = -INFINITY, l = 0.f;
       bool have_cq = !KS || t == 0;
+      // keys left from the piece's first cached (own) tile on
+      const int left_k = pp->len - pp->k0 * kUnit, left_l = pp->rows - pp->l0 * kUnit;
       for (int j = KS ? t : 0; j < n; j += KS ? 2 : 1, ++sc) {
-        const bool own = j >= pc.nk;
+        const bool own = j >= nk;
         const uint32_t ti = tcount + (uint32_t)j;
-        ok = mbar_wait(BAR(B_SF + t), sc & 1, wd, 40);
-        if (ok) ok = mbar_wait(BAR(B_KI + ti % NI), (ti / NI) & 1, wd, 41);
+        ok = mbar_wait(BAR(B_KI + ti % NI), (ti / NI) & 1, wd, 41);
+        // (read before the wait for S: shared memory is slow to answer beside the MMAs)
+        const KInfo& ki = kinfo[ti % NI];
+        const float4 ks4 = *reinterpret_cast<const float4*>(ki.s[0]);
+        const float4 lv4 = *reinterpret_cast<const float4*>(ki.lv[0]);
+        const float4 iv4 = *reinterpret_cast<const float4*>(ki.iv[0]);
+        const int fine = ki.fine;
+        if (ok) ok = mbar_wait(BAR(B_SF + t), sc & 1, wd, 40);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -632,35 +743,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           cq = row_cq[row];
           have_cq = true;
         }
-        const KInfo& ki = kinfo[ti % NI];
-        uint32_t a0[32], a1[32], a2[32], a3[32];
-        tmem_ld32x4(tS, tS + 32, tS + 64, tS + 96, a0, a1, a2, a3);
-        const int key0 = own ? (pc.l0 + j - pc.nk) * kUnit : (pc.k0 + j) * kUnit;
-        const int hi = (own ? pc.seg.v.rows : pc.seg.v.len) - key0;
+        const int hi = own ? left_l - (j - nk) * kUnit : left_k - j * kUnit;
         const float rf = own ? p.sl2 : cq;
-        float f0 = rf * ki.s[0], f1 = rf * ki.s[2], f2_ = rf * ki.s[4], f3 = rf * ki.s[6];
-        if (ki.fine) {  // a scale for each 16 keys, keys without a page
+        float f[4] = {rf * ks4.x, rf * ks4.y, rf * ks4.z, rf * ks4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
+        const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+        uint32_t a[4][32];  // the row's 128 scores
+        tmem_ld32x4(tS, tS + 32, tS + 64, tS + 96, a[0], a[1], a[2], a[3]);
+        if (fine) {
           const int gone = ki.gone;
 #pragma unroll
-          for (int c8 = 0; c8 < 32; ++c8) {
-            const int x = c8 >> 4;
-            a0[c8] = (gone >> x) & 1 ? __float_as_uint(-INFINITY) : __float_as_uint(__uint_as_float(a0[c8]) * (rf * ki.s[x]));
-            a1[c8] = (gone >> (2 + x)) & 1 ? __float_as_uint(-INFINITY) : __float_as_uint(__uint_as_float(a1[c8]) * (rf * ki.s[2 + x]));
-            a2[c8] = (gone >> (4 + x)) & 1 ? __float_as_uint(-INFINITY) : __float_as_uint(__uint_as_float(a2[c8]) * (rf * ki.s[4 + x]));
-            a3[c8] = (gone >> (6 + x)) & 1 ? __float_as_uint(-INFINITY) : __float_as_uint(__uint_as_float(a3[c8]) * (rf * ki.s[6 + x]));
+          for (int x = 0; x < 4; ++x) {
+            scores16(a[x], f[x], lv[x], rf * ki.s[1][x], ki.lv[1][x], gone >> (2 * x));
+            f[x] = 1.f;
+            lv[x] = 0.f;
           }
-          f0 = f1 = f2_ = f3 = 1.f;
         }
         if (hi < kUnit) {
-          mask32(a0, hi);
-          mask32(a1, hi - 32);
-          mask32(a2, hi - 64);
-          mask32(a3, hi - 96);
-          if (hi <= 32) f1 = f0;  // (blocks behind the end have no scale: any finite factor keeps -inf)
-          if (hi <= 64) f2_ = f0;
-          if (hi <= 96) f3 = f0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mask32(a[x], hi - 32 * x);
         }
-        const float mx = fmaxf(fmaxf(max32(a0) * f0, max32(a1) * f1), fmaxf(max32(a2) * f2_, max32(a3) * f3));
+        const float mx = fmaxf(fmaxf(fmaf(max32(a[0]), f[0], lv[0]), fmaf(max32(a[1]), f[1], lv[1])),
+                               fmaxf(fmaf(max32(a[2]), f[2], lv[2]), fmaf(max32(a[3]), f[3], lv[3])));
         bool rescale = false;
         float alpha = 1.f;
         if (m_ref == -INFINITY) {
@@ -670,21 +773,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_ref = mx;
           rescale = true;
         }
-        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-        float sum = exp32(a0, f0, nm);
-        sum += exp32(a1, f1, nm);
-        sum += exp32(a2, f2_, nm);
-        sum += exp32(a3, f3, nm);
-        l = fmaf(l, alpha, sum);
-        store_p<FINE>(a0, tS);
-        store_p<FINE>(a1, tS + 16);
-        store_p<FINE>(a2, tS + 32);
-        store_p<FINE>(a3, tS + 48);
-        if (FINE) {
-          store_p<true>(a0, tS + 64);
-          store_p<true>(a1, tS + 80);
-          store_p<true>(a2, tS + 96);
-          store_p<true>(a3, tS + 112);
+        const float nm = m_ref == -INFINITY ? 0.f : (FINE ? kFineShift : 0.f) - m_ref;
+        l *= alpha;
+        uint32_t rest[FINE ? 64 : 1];  // own keys, FINE: the third parts, packed
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float s0, s1;
+          exp32(a[x], f[x], nm + lv[x], s0, s1);
+          l = fine ? fmaf(s0, iv[x], fmaf(s1, ki.iv[1][x], l)) : fmaf(s0 + s1, iv[x], l);
+          if (own) {
+            store_p<true, FINE>(a[x], tS + 32 * x);
+            if (FINE) {
+              store_p<true, true>(a[x], tS + 32 * x + 16);
+#pragma unroll
+              for (int y = 0; y < 16; ++y)
+                rest[(FINE ? 16 * x + y : 0)] =
+                    pack_bf16x2(__uint_as_float(a[x][2 * y]), __uint_as_float(a[x][2 * y + 1]));
+            }
+          } else {
+            store_p<false, FINE>(a[x], tS + 32 * x);
+            if (FINE) store_p<false, false>(a[x], tS + 32 * x + 16);
+          }
         }
         // O is complete up to the tile before (S of this one was issued behind its product)
         if (__any_sync(0xffffffffu, rescale)) {
@@ -699,19 +808,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(BAR(B_PF + t));
-        if (FINE) {  // the third part, once the first two are multiplied
-          ok = mbar_wait(BAR(B_FD + t), sc & 1, wd, 43);
+        if (FINE && own) {  // the third part, once the first two are multiplied
+          ok = mbar_wait(BAR(B_FD + t), p2 & 1, wd, 43);
+          ++p2;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          store_p<false>(a0, tS);
-          store_p<false>(a1, tS + 16);
-          store_p<false>(a2, tS + 32);
-          store_p<false>(a3, tS + 48);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) pk[y] = rest[FINE ? 16 * x + y : 0];
+            tmem_st16(tS + 32 * x, pk);
+          }
           tc_fence_before();
           mbar_arrive(BAR(B_P2 + t));
         }
-        if (!KS && j == pc.nk - 1 && pc.nl > 0) {  // the cached keys are through with Q's codes
+        if (!KS && j == nk - 1 && nl > 0) {  // the cached keys are through with Q's codes
           put_q16();
           fence_proxy_async_smem();
           mbar_arrive(BAR(B_QF + t));
@@ -719,9 +832,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       tcount += (uint32_t)n;
-      if (pc.nk > 0) ++q8c;
+      if (nk > 0) ++q8c;
 
       // ---- the piece's result
+      if (FINE) m_ref -= kFineShift;  // the reference of the weights as they were kept
       float w0 = 1.f, w1 = 0.f, M = m_ref, L = l;
       const int n0 = KS ? (n + 1) / 2 : n, n1 = KS ? n / 2 : n;
       if (KS && n > 0) {
@@ -753,10 +867,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const float inv = L != 0.f ? 1.f / L : 0.f;
-      const float s0 = pc.whole ? w0 * inv : w0, s1 = pc.whole ? w1 * inv : w1;
-      float* slot = p.part + (2 * (int64_t)blockIdx.x + (pc.first ? 1 : 0)) * part_floats(kTileRows, HD);
+      const bool whole = pp->whole;
+      const Row r = my_row();
+      const bool live = r.live;
+      const float s0 = whole ? w0 * inv : w0, s1 = whole ? w1 * inv : w1;
+      float* slot = p.part + (2 * (int64_t)blockIdx.x + (pp->first ? 1 : 0)) * part_floats(kTileRows, HD);
       const int prow = (KS ? 0 : t * 128) + row;
-      const int64_t oofs = (grow * p.Hq + head) * HD;
+      const int64_t oofs = (r.at * p.Hq + r.head) * HD;
+      done(np);  // (the rest is in registers)
       // split: sub-tile t's threads write columns HD / 2 t ..; both read both accumulators
       constexpr int kCols = KS ? HD / 2 : HD;
       const int col0 = KS ? t * (HD / 2) : 0;
@@ -774,10 +892,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 32; ++x)
             o[x] = __float_as_uint(fmaf(__uint_as_float(o1[x]), s1, __uint_as_float(o[x])));
         }
-        if (live) {
-          if (!pc.whole || p.o_f32) {
-            float4* d = reinterpret_cast<float4*>(pc.whole ? static_cast<float*>(p.O) + oofs + col
-                                                           : slot + (int64_t)prow * HD + col);
+        if (!whole) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            reinterpret_cast<float4*>(slot)[(col / 4 + x) * kTileRows + prow] =
+                make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
+                            __uint_as_float(o[4 * x + 3]));
+        } else if (live) {
+          if (p.o_f32) {
+            float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.O) + oofs + col);
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               d[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
@@ -802,9 +925,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(BAR(B_OE + t));
         }
       }
-      if (live && (!KS || t == 0)) {
-        if (pc.whole) {
-          p.LSE[(int64_t)head * p.r.T + grow] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      if (!KS || t == 0) {
+        if (whole) {
+          if (live) p.LSE[(int64_t)r.head * p.r.T + r.at] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
         } else {
           slot[(int64_t)kTileRows * HD + prow] = M;
           slot[(int64_t)kTileRows * (HD + 1) + prow] = L;
@@ -812,58 +935,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------ V's codes -> bf16
+    // ------------------------------------------------ V's codes -> fp16
     setmaxnreg_dec<kRegsConvert>();
     const int i = threadIdx.x - 384;
     constexpr int CH = HD / 16;             // 16-code chunks of a key
-    PieceIter it = piece_begin(p, bad);
-    Piece pc;
     uint32_t w = 0;
     bool ok = true;
-    while (ok && piece_next(p, it, pc, bad)) {
-      for (int j = 0; j < pc.nk + pc.nl; ++j, ++w) {
+    for (uint32_t np = 0; ok; ++np) {
+      const Piece* pp = piece(np);
+      if (!pp) break;
+      const int nk = pp->nk, n = nk + pp->nl;
+      const int left_k = pp->len - pp->k0 * kUnit, left_l = pp->rows - pp->l0 * kUnit;
+      done(np);
+      for (int j = 0; j < n; ++j, ++w) {
         const uint32_t slot = w & 1, ph = (w >> 1) & 1;
         ok = mbar_wait(BAR(B_VF + slot), ph, wd, 50) && mbar_wait(BAR(B_WE + slot), ph ^ 1, wd, 51) &&
-             mbar_wait(BAR(B_VI + w % NI), (w / NI) & 1, wd, 52);
+             mbar_wait(BAR(B_KI + w % NI), (w / NI) & 1, wd, 52);
         if (!ok) break;
         const uint32_t dst = base + LY::kW + slot * LY::kWBytes;
-        if (j < pc.nk) {
-          const uint32_t src = base + LY::kV + slot * kSlot;
-          const int left = pc.seg.v.len - (pc.k0 + j) * kUnit;
-          const VInfo& vi = vinfo[w % NI];
-#pragma unroll 4
-          for (int x = 0; x < CH; ++x) {
-            const int id = x * 128 + i, key = id / CH, c16 = id % CH;
-            uint4 v = ld_shared_v4(src + id * 16);
-            float s = vi.s[key >> 4];
-            if (key >= left || s == 0.f) {  // stale codes (or none) may be anything
-              v = make_uint4(0, 0, 0, 0);
-              s = 0.f;
+        if (j < nk) {
+          const uint4* src = reinterpret_cast<const uint4*>(bp + LY::kV + slot * kSlot) + i;
+          const int left = left_k - j * kUnit;
+          const int gone = kinfo[w % NI].gone;
+          const bool full = left >= kUnit && gone == 0;
+          const int c16 = i % CH, key0 = i / CH;
+          // 8-value chunks 2 c16, 2 c16 + 1 of a key; the second panel's threads write them in the other order,
+          // so that the 8 lanes of a store phase cover all banks
+          const uint32_t at0 = dst + (c16 >> 2) * kSlot, ch = (uint32_t)(c16 & 3) * 2;
+          const bool odd = c16 >= 4;
+          constexpr int XB = 4;  // loads in flight
+#pragma unroll
+          for (int x0 = 0; x0 < CH; x0 += XB) {
+            uint4 v[XB];
+#pragma unroll
+            for (int x = 0; x < XB; ++x) v[x] = src[(x0 + x) * 128];
+#pragma unroll
+            for (int x = 0; x < XB; ++x) {
+              const int key = key0 + (x0 + x) * (128 / CH);
+              if (!full && (key >= left || ((gone >> (key >> 4)) & 1))) v[x] = make_uint4(0, 0, 0, 0);  // stale codes
+              const uint32_t a[2] = {odd ? v[x].z : v[x].x, odd ? v[x].w : v[x].y};
+              const uint32_t b[2] = {odd ? v[x].x : v[x].z, odd ? v[x].y : v[x].w};
+              const uint32_t at = at0 + key * 128, sw = (uint32_t)key & 7u;
+              st_shared_v4(at + (((ch + (odd ? 1 : 0)) ^ sw) << 4), e4m3x2_to_half2(a[0]), e4m3x2_to_half2(a[0] >> 16),
+                           e4m3x2_to_half2(a[1]), e4m3x2_to_half2(a[1] >> 16));
+              st_shared_v4(at + (((ch + (odd ? 0 : 1)) ^ sw) << 4), e4m3x2_to_half2(b[0]), e4m3x2_to_half2(b[0] >> 16),
+                           e4m3x2_to_half2(b[1]), e4m3x2_to_half2(b[1] >> 16));
             }
-            const uint32_t wd4[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[8];
-            const uint64_t s2 = f2(s, s);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t h = e4m3x2_to_half2(wd4[k] >> (16 * y));
-                const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                float z0, z1;
-                f2_split(f2_mul(f2(z.x, z.y), s2), z0, z1);
-                o[2 * k + y] = pack_bf16x2(z0, z1);
-              }
-            // 8-value chunks 2 c16, 2 c16 + 1 of the key; the second panel's threads write them in the other
-            // order, so that the 8 lanes of a store phase cover all banks
-            const uint32_t at = dst + (c16 >> 2) * kSlot + key * 128;
-            const uint32_t ch = (uint32_t)(c16 & 3) * 2, sw = (uint32_t)key & 7u;
-            const bool odd = c16 >= 4;
-            st_shared_v4(at + (((ch + (odd ? 1 : 0)) ^ sw) << 4), odd ? o[4] : o[0], odd ? o[5] : o[1], odd ? o[6] : o[2], odd ? o[7] : o[3]);
-            st_shared_v4(at + (((ch + (odd ? 0 : 1)) ^ sw) << 4), odd ? o[0] : o[4], odd ? o[1] : o[5], odd ? o[2] : o[6], odd ? o[3] : o[7]);
           }
         } else {
           // own tile, loaded as bf16: rows behind the sequence's belong to others
-          const int left = pc.seg.v.rows - (pc.l0 + j - pc.nk) * kUnit;
+          const int left = left_l - (j - nk) * kUnit;
           if (i >= left)
             for (int x = 0; x < HD / 8; ++x) st_shared_v4(dst + (x >> 3) * kSlot + i * 128 + (x & 7) * 16, 0, 0, 0, 0);
         }

@@ -125,6 +125,8 @@ struct AttnSplit {
   int tile_rows;  // rows of a row tile
   int local;      // the rows also read their own block
   int extra;      // empty positions that open a segment
+  int keyed;      // weights: one segment per (sequence, KV head) that holds all
+                  // rows; a unit of keys counts once for each row tile
 };
 
 struct SegInfo {
@@ -143,6 +145,11 @@ __device__ __forceinline__ SegInfo seg_info(const CacheDesc& c, const RowsDesc& 
   g.ltiles = a.local && g.v.rows > kFoldRows ? (g.v.rows + kUnit - 1) / kUnit : 0;
   const int n = g.ktiles + g.ltiles;
   g.units = n > 0 ? n : 1;
+  if (a.keyed) {
+    g.units = g.ktiles * g.rtiles;
+    g.ltiles = g.rtiles;  // (positions of one unit of keys)
+    g.rtiles = g.units > 0 ? 1 : 0;
+  }
   g.span = g.units + a.extra;
   return g;
 }

@@ -83,9 +83,11 @@ bdlm_status check_rows(const CacheDesc& c, const int32_t* off, int64_t T, int64_
   return BDLM_OK;
 }
 
-bdlm_status check_heads(const CacheDesc& c, int Hq, float scale) {
+bdlm_status check_heads(const CacheDesc& c, const RowsDesc& r, int Hq, float scale) {
   if (Hq <= 0 || Hq > 4096 || Hq % c.Hkv)
     return abi_fail(BDLM_ERR_SHAPE, "Hq=%d must be a positive multiple of Hkv=%d, at most 4096", Hq, c.Hkv);
+  if ((int64_t)r.max_rows * (Hq / c.Hkv) > (int64_t)1 << 29)
+    return abi_fail(BDLM_ERR_SHAPE, "max_rows * Hq / Hkv exceeds 2^29");
   if (!(scale > 0.f) || !std::isfinite(scale))
     return abi_fail(BDLM_ERR_INVALID_ARG, "scale=%g must be finite and > 0", scale);
   return BDLM_OK;
@@ -179,7 +181,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     CachedParams p;
     CACHE_CHECK(check_cache(cache, &p.c));
     CACHE_CHECK(check_rows(p.c, row_offsets, rows, max_rows, &p.r));
-    CACHE_CHECK(check_heads(p.c, Hq, scale));
+    CACHE_CHECK(check_heads(p.c, p.r, Hq, scale));
     if (o_dtype != BDLM_BF16 && o_dtype != BDLM_F32) return abi_fail(BDLM_ERR_INVALID_ARG, "bad o_dtype %d", (int)o_dtype);
     if (!Kn != !Vn) return abi_fail(BDLM_ERR_INVALID_ARG, "Kn and Vn: give both or neither");
     if (rows == 0) return BDLM_OK;
@@ -194,8 +196,6 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(flat, p.c.d)));
     int sms;
     CACHE_CHECK(abi_device(&sms));
-    if (flat > (int64_t)1 << 30)
-      return abi_fail(BDLM_ERR_SHAPE, "max_rows * Hq / Hkv = %lld exceeds 2^30", (long long)flat);
     p.sp.group = Hq / p.c.Hkv;
     p.sp.local = Kn != nullptr;
     p.Q = Qn;
@@ -211,6 +211,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     p.limit_ns = abi_wait_limit_ns();
     p.sp.tile_rows = cached_tile_rows(flat);
     p.sp.extra = p.sp.tile_rows == kSmallRows ? kSmallExtra : kTcExtra;
+    p.sp.keyed = 0;
     p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
     CachedMaps maps;
     if (p.sp.tile_rows != kSmallRows) {
@@ -243,7 +244,7 @@ bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cach
     WeightsParams p;
     CACHE_CHECK(check_cache(cache, &p.c));
     CACHE_CHECK(check_rows(p.c, row_offsets, rows, max_rows, &p.r));
-    CACHE_CHECK(check_heads(p.c, Hq, scale));
+    CACHE_CHECK(check_heads(p.c, p.r, Hq, scale));
     if (rows == 0) return BDLM_OK;
     CACHE_CHECK(check_ptr("Qn", Qn, 16));
     CACHE_CHECK(check_ptr("LSE", LSE, 4));
@@ -256,11 +257,18 @@ bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cach
     p.Hq = Hq;
     p.sl2 = scale * 1.4426950408889634f;
     p.W = weights;
+    p.sp = AttnSplit{Hq / p.c.Hkv, 128, 0, kTcExtra, 1};
+    p.G = std::min(sms, kSmsMax);
     p.status = static_cast<uint32_t*>(workspace);
+    p.limit_ns = abi_wait_limit_ns();
+    EncodeTiledFn enc;
+    CUtensorMap k8;
+    CACHE_CHECK(abi_encoder(&enc));
+    CACHE_CHECK(encode_codes(enc, &k8, p.c));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int launches = 0;
     void* tm = abi_timer_begin(ABI_T_WEIGHTS, st);
-    cudaError_t e = launch_cache_weights(p, st, &launches);
+    cudaError_t e = launch_cache_weights(k8, p, st, &launches);
     abi_timer_end(tm);
     return abi_finish(e, launches, "cache weights launch");
   });

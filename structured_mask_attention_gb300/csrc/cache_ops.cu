@@ -1,6 +1,6 @@
 // cache_ops.cu -- the 8-bit cache's memory-bound calls: append (quantise new
-// tokens into their pages), weights (attention weight per cached token) and
-// evict (keep the most attended tokens, in other pages).
+// tokens into their pages) and evict (keep the most attended tokens, in other
+// pages).
 #include <cuda_bf16.h>
 
 #include "cache_ops.h"
@@ -133,75 +133,6 @@ __global__ void __launch_bounds__(kAppendThreads) bdlm_cache_append_kernel(const
     *sp = sc;
     if (bad) atomicOr(p.status, bad);
   }
-}
-
-// ----------------------------------------------------------------- weights
-// One thread per cached key: its codes stay in registers while the rows'
-// queries pass through shared memory, kQ rows at a time.
-constexpr int kWThreads = 128, kQ = 8;
-template <int HD>
-__global__ void __launch_bounds__(kWThreads) bdlm_cache_weights_kernel(const WeightsParams p) {
-  __shared__ float4 q[kQ][HD / 4];
-  __shared__ float lse[kQ];
-  const CacheDesc& c = p.c;
-  uint32_t bad = 0;
-  const int s = blockIdx.z, h = blockIdx.y;
-  const SeqView v = seq_view(c, p.r, s, bad);
-  const int group = p.Hq / c.Hkv;
-  const int64_t fr_end = (int64_t)v.rows * group;
-  for (int64_t k0 = (int64_t)blockIdx.x * kWThreads; k0 < v.len && fr_end > 0; k0 += (int64_t)gridDim.x * kWThreads) {
-    const int64_t key = k0 + threadIdx.x;
-    const int pid = key < v.len ? page_id(c, s, (int)(key >> c.lp), bad) : -1;
-    const int64_t b = (int64_t)max(pid, 0) * c.Hkv + h;
-    uint32_t w[HD / 4];
-    const uint4* src = reinterpret_cast<const uint4*>(c.k8 + (b * c.page + (key & (c.page - 1))) * HD);
-#pragma unroll
-    for (int i = 0; i < HD / 16; ++i) {
-      const uint4 x = pid >= 0 ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-      w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-    }
-    const float ks = p.sl2 * (pid >= 0 ? c.ks[b] : 0.f);
-    float sum = 0.f;
-    for (int64_t f0 = 0; f0 < fr_end; f0 += kQ) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kQ * HD / 4; i += kWThreads) {
-        const int r = i / (HD / 4), x = i % (HD / 4);
-        const int64_t fr = f0 + r, tok = fr / group;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (fr < fr_end) {
-          const int head = h * group + (int)(fr - tok * group);
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.Q) +
-                                                               ((v.row0 + tok) * p.Hq + head) * HD) + x);
-          y = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                          __uint_as_float(u.y & 0xffff0000u));
-          if (x == 0) lse[r] = p.LSE[(int64_t)head * p.r.T + v.row0 + tok] * 1.4426950408889634f;
-        } else if (x == 0) {
-          lse[r] = INFINITY;
-        }
-        q[r][x] = y;
-      }
-      __syncthreads();
-      float acc[kQ];
-#pragma unroll
-      for (int r = 0; r < kQ; ++r) acc[r] = 0.f;
-#pragma unroll
-      for (int i = 0; i < HD / 4; ++i) {
-        float k[4];
-        e4m3x4_to_float(w[i], k);
-#pragma unroll
-        for (int r = 0; r < kQ; ++r) {
-          const float4 y = q[r][i];
-          acc[r] = fmaf(k[0], y.x, fmaf(k[1], y.y, fmaf(k[2], y.z, fmaf(k[3], y.w, acc[r]))));
-        }
-      }
-      // a row with no visible key has LSE = -inf: it gives no weight
-#pragma unroll
-      for (int r = 0; r < kQ; ++r)
-        sum += lse[r] == -INFINITY ? 0.f : ex2_approx(fmaf(acc[r], ks, -lse[r]));
-    }
-    if (pid >= 0) p.W[((int64_t)s * c.Hkv + h) * ((int64_t)c.max_pages << c.lp) + key] += sum;
-  }
-  if (bad) atomicOr(p.status, bad);
 }
 
 // ------------------------------------------------------------------- evict
@@ -410,16 +341,6 @@ cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* lau
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (p.c.d == 128) bdlm_cache_append_kernel<128><<<(unsigned)blocks, kAppendThreads, 0, st>>>(p, per);
   else bdlm_cache_append_kernel<64><<<(unsigned)blocks, kAppendThreads, 0, st>>>(p, per);
-  ++*launches;
-  return cudaGetLastError();
-}
-
-cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t st, int* launches) {
-  const int64_t cap = (int64_t)p.c.max_pages << p.c.lp;
-  const int64_t tiles = (cap + kWThreads - 1) / kWThreads;
-  const dim3 grid((unsigned)(tiles < 4096 ? tiles : 4096), p.c.Hkv, p.c.n_seqs);
-  if (p.c.d == 128) bdlm_cache_weights_kernel<128><<<grid, kWThreads, 0, st>>>(p);
-  else bdlm_cache_weights_kernel<64><<<grid, kWThreads, 0, st>>>(p);
   ++*launches;
   return cudaGetLastError();
 }

@@ -21,14 +21,18 @@ cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* lau
 struct WeightsParams {
   CacheDesc c;
   RowsDesc r;
+  AttnSplit sp;  // keyed
   const void* Q;     // bf16 [T, Hq, d]
   const float* LSE;  // [Hq, T]
   int Hq;
   float sl2;
   float* W;  // [n_seqs, Hkv, max_pages * page]
+  int G;     // CTAs
   uint32_t* status;
+  uint64_t limit_ns;
 };
-cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t st, int* launches);
+// k8: K's codes as [n_pages * Hkv, page, d].
+cudaError_t launch_cache_weights(const CUtensorMap& k8, const WeightsParams& p, cudaStream_t st, int* launches);
 
 struct EvictParams {
   CacheDesc c;

@@ -41,7 +41,7 @@
 #include <type_traits>
 
 #include "cached_attn.h"
-#include "ptx.cuh"
+#include "cached_tc.cuh"
 
 namespace bdlm {
 namespace {
@@ -103,54 +103,6 @@ struct Piece {
 };
 constexpr int NP = 4;  // ring slots
 
-// Shared-memory descriptors (see sdesc_sw128) as their two words: the upper
-// one is a constant of the layout, the lower one the start address (and, for an
-// MN-major operand, the panel stride), so that the issuing thread holds one
-// register per operand.  128-byte (SW = 2) or 64-byte (SW = 4) swizzle.
-__host__ __device__ constexpr uint32_t desc_hi(int sw, int sbo) {
-  return (uint32_t)(sbo >> 4) | (1u << 14) | ((uint32_t)sw << 29);
-}
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, int lbo) {
-  return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(lbo >> 4) << 16);
-}
-
-// D[tmem] (+)= A[smem] B[smem]: e4m3, K = 32 (F8), or bf16, K = 16.
-template <bool F8>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
-                                       uint32_t idesc, uint32_t acc) {
-  if (F8)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\t"
-        "mov.b64 b, {%3, %4};\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\t"
-        "mov.b64 b, {%3, %4};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// D[tmem] (+)= A[tmem] B[smem], 16-bit types, K = 16.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc,
-                                       uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// fp32 accumulator, e4m3 A and B (format 0), both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// Contiguous copy into shared memory (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
   float u[10];
 #pragma unroll
@@ -657,29 +609,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < HD / 2; ++i) amax = max(amax, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        int e = 7 + 127 - (int)(amax >> 7);
-        if (amax >= 0x7f80u || amax == 0) e = 0;
-        e = min(e, 126);
-        // e4m3 has no infinity: a row that is not finite reads NaN
-        const float f = amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e + 127) << 23);
-        cq = p.sl2 * __uint_as_float((uint32_t)(127 - e) << 23);
+        float inv;
+        const float f = row_factor(amax, inv);
+        cq = p.sl2 * inv;
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
           uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            // (in fp16 the scaled values are exact down to 2^-24, below e4m3's smallest step)
-            const __half2 v = __floats2half2_rn(__uint_as_float(w[8 * i + k] << 16) * f,
-                                                __uint_as_float(w[8 * i + k] & 0xffff0000u) * f);
-            const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t back = e4m3x2_to_half2(h);
-            const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
-            const uint32_t l = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(d), __NV_SATFINITE, __NV_E4M3);
-            hi[k >> 1] = k & 1 ? hi[k >> 1] | h << 16 : h;
-            lo[k >> 1] = k & 1 ? lo[k >> 1] | l << 16 : l;
-          }
-          const uint32_t at = HD == 128 ? (uint32_t)(row * 128 + ((i ^ (row & 7)) << 4))
-                                        : (uint32_t)(row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
+          split_e4m3(w + 8 * i, f, hi, lo);
+          const uint32_t at = e4m3_chunk<HD>(row, i);
           st_shared_v4(dst + at, hi[0], hi[1], hi[2], hi[3]);
           st_shared_v4(dst + 128 * HD + at, lo[0], lo[1], lo[2], lo[3]);
         }

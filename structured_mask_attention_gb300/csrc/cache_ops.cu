@@ -1,10 +1,13 @@
 // cache_ops.cu -- the 8-bit cache's memory-bound calls: append (quantise new
 // tokens into their pages) and evict (keep the most attended tokens, in other
 // pages).
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "cache_ops.h"
 #include "ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace bdlm {
 namespace {
@@ -14,8 +17,13 @@ __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return a > b
 // Eight e4m3 codes of eight values times inv (pow2 scale) or divided by s.
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, float inv, bool pow2) {
   float y[8];
+  if (pow2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = pow2 ? x[i] * inv : __fdiv_rn(x[i], s);
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  }
   return make_uint2(to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16,
                     to_e4m3x2(y[4], y[5]) | to_e4m3x2(y[6], y[7]) << 16);
 }
@@ -27,45 +35,24 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float* f) {
   f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
 }
 
-// Largest of `v` over the `n` threads (a power of two, 8 .. 256) of an aligned
-// group of the block; every thread of the block calls it.  What the group's
-// threads read before it, they may write after it.
-__device__ __forceinline__ uint32_t group_max(uint32_t v, int n, uint32_t* red) {
-  const int lim = n < 32 ? n : 32;
-  __syncwarp();
-  for (int o = lim >> 1; o > 0; o >>= 1) v = umax2(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (n <= 32) return v;
-  const int w = threadIdx.x >> 5, nw = n >> 5;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[w] = v;
-  __syncthreads();
-  const int w0 = w & ~(nw - 1);
-  for (int i = 0; i < nw; ++i) v = umax2(v, red[w0 + i]);
-  return v;
-}
-
 // ------------------------------------------------------------------ append
-// A slab is one (sequence, touched page, KV head) of K or of V; page * HD / 64
-// threads of a 256-thread block take it, 64 values each (eight 16-byte loads
-// in flight), so the new tokens are read once and stay in registers between
-// the block maximum and the codes.
+// A CTA takes TT = max(page, 64) slots of one (sequence, KV head), K and V: 16
+// values per thread and step (two 16-byte loads, HD / 16 lanes to a token),
+// all in flight at once and held between the blocks' maxima and their codes,
+// so the new tokens are read once.  Bound by HBM: 2 bytes read and 1 written per
+// value.
 constexpr int kAppendThreads = 256;
-template <int HD>
-__global__ void __launch_bounds__(kAppendThreads) bdlm_cache_append_kernel(const AppendParams p, int pages_per_seq) {
-  __shared__ uint32_t red[kAppendThreads / 32];
-  constexpr int CH = HD / 8;  // 8-value chunks of a token
+template <int HD, int TT>
+__global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_kernel(const AppendParams p) {
+  constexpr int CH = HD / 16;                     // 16-value chunks of a token
+  constexpr int kThreads = kAppendThreads * TT / 64;
+  constexpr int NT = 2 * TT * CH / kThreads;      // chunks per thread, the first half K's
+  __shared__ uint32_t s_amax[2][TT / 16];
+  __shared__ float s_was[2][TT / 16];             // the blocks' scales before
+  __shared__ int s_page[TT / 16];
   const CacheDesc& c = p.c;
-  const int tps = c.page * HD / 64;  // threads per slab
-  const int64_t slab = (int64_t)blockIdx.x * (kAppendThreads / tps) + threadIdx.x / tps;
-  const int tl = threadIdx.x % tps;
-  const int64_t n_slabs = (int64_t)c.n_seqs * pages_per_seq * c.Hkv * 2;
+  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
   uint32_t bad = 0;
-  const bool in = slab < n_slabs;
-  const int64_t id = in ? slab : 0;
-  const int kv = (int)(id & 1);
-  const int h = (int)((id >> 1) % c.Hkv);
-  const int64_t sj = (id >> 1) / c.Hkv;
-  const int j = (int)(sj % pages_per_seq), s = (int)(sj / pages_per_seq);
   const SeqView v = seq_view(c, p.r, s, bad);
   const int64_t cap = (int64_t)c.max_pages << c.lp;
   int rows = v.rows;
@@ -73,80 +60,119 @@ __global__ void __launch_bounds__(kAppendThreads) bdlm_cache_append_kernel(const
     bad |= kStatusBadLen;
     rows = (int)(cap - v.len);
   }
-  const int lpage = (v.len >> c.lp) + j;             // logical page
-  const int first = (lpage << c.lp) - v.len;         // new-token index of its slot 0 (negative: old tokens before)
-  const bool hit = in && rows > 0 && first < rows;
-  const int pid = hit ? page_id(c, s, lpage, bad) : -1;
-  if (in && tl == 0 && j == 0 && h == 0 && kv == 0 && p.lens_out) p.lens_out[s] = v.len + rows;
-  const __nv_bfloat16* X = static_cast<const __nv_bfloat16*>(kv ? p.V : p.K);
-  uint4 x[8];
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ch = i * tps + tl, tok = first + ch / CH;
-    const bool ok = pid >= 0 && tok >= 0 && tok < rows;
-    x[i] = ok ? __ldg(reinterpret_cast<const uint4*>(X + ((v.row0 + tok) * c.Hkv + h) * HD) + ch % CH)
-              : make_uint4(0, 0, 0, 0);
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) amax = umax2(amax, umax2(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-  }
-  const int64_t b = (int64_t)max(pid, 0) * c.Hkv + h;
-  float* sp = (kv ? c.vs : c.ks) + b;
-  uint8_t* codes = (kv ? c.v8 : c.k8) + b * c.page * HD;
-  float was = pid >= 0 && first < 0 ? *sp : 0.f;
-  amax = group_max(amax << 16, tps, red);
-  if (pid < 0) {
-    if (bad && tl == 0) atomicOr(p.status, bad);
-    return;
-  }
-  float sc = block_scale(amax);
-  if (first < 0) {  // the block already holds tokens: its scale never shrinks (NaN stays)
-    sc = (was != was || sc != sc) ? __uint_as_float(0x7fc00000u) : fmaxf(was, sc);
-  }
-  const bool pow2 = is_pow2(sc);
-  const float inv = pow2 ? __uint_as_float(0x7f000000u - __float_as_uint(sc)) : 0.f;
-  const bool regrade = first < 0 && sc != was;  // old codes to the new scale (true for NaN as well)
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ch = i * tps + tl, tok = first + ch / CH;
-    float f[8];
-    if (tok >= 0 && tok < rows) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[2 * k] = __uint_as_float(w[k] << 16);
-        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-      }
-    } else if (tok < 0 && regrade) {
-      const uint2 o = *(reinterpret_cast<const uint2*>(codes) + ch);
-      e4m3x4_to_float(o.x, f);
-      e4m3x4_to_float(o.y, f + 4);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= was;
-    } else {
-      continue;
-    }
-    *(reinterpret_cast<uint2*>(codes) + ch) = quantise8(f, sc, inv, pow2);
-  }
-  if (tl == 0) {
-    *sp = sc;
+  const int base = (v.len & ~(TT - 1)) + (int)blockIdx.x * TT;  // first position
+  const int first = base - v.len;                               // as a new token (negative: old tokens)
+  if (blockIdx.x == 0 && h == 0 && tid == 0) {
+    if (p.lens_out) p.lens_out[s] = v.len + rows;
     if (bad) atomicOr(p.status, bad);
+    bad = 0;
+  }
+  if (first >= rows) return;
+  if (tid < TT / 16) {
+    const int f = first + (tid << c.lp);  // new token of the block's first slot
+    int id = -1;
+    if (tid < (TT >> c.lp) && f < rows && f + c.page > 0) id = page_id(c, s, (base >> c.lp) + tid, bad);
+    s_page[tid] = id;
+    const int64_t b = (int64_t)max(id, 0) * c.Hkv + h;
+    s_was[0][tid] = id >= 0 && f < 0 ? c.ks[b] : 0.f;
+    s_was[1][tid] = id >= 0 && f < 0 ? c.vs[b] : 0.f;
+    s_amax[0][tid] = s_amax[1][tid] = 0;
+    if (bad) atomicOr(p.status, bad);
+  }
+  uint4 x[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kThreads + tid, tok = first + k / CH;
+    const bool ok = tok >= 0 && tok < rows;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv ? p.V : p.K) +
+                                                      ((v.row0 + (ok ? tok : 0)) * c.Hkv + h) * HD) + 2 * (k % CH);
+    x[i][0] = ok ? __ldg(src) : make_uint4(0, 0, 0, 0);
+    x[i][1] = ok ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int kv = i >= NT / 2, t = ((i % (NT / 2)) * kThreads + tid) / CH;
+    // bf16 magnitudes compare like integers
+    uint32_t m = 0;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i][y].x & 0x7fff7fffu, x[i][y].y & 0x7fff7fffu),
+                               __vmaxu2(x[i][y].z & 0x7fff7fffu, x[i][y].w & 0x7fff7fffu)));
+    m = umax2(m & 0xffffu, m >> 16);
+    // a warp's tokens belong to one block
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) atomicMax(&s_amax[kv][t >> c.lp], m << 16);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kThreads + tid, t = k / CH, j = t >> c.lp, tok = first + t;
+    const int id = s_page[j];
+    if (id < 0 || tok >= rows) continue;
+    float sc = block_scale(s_amax[kv][j]);
+    const bool had = first + (j << c.lp) < 0;  // the block already holds tokens: its scale never shrinks, NaN stays
+    const float was = s_was[kv][j];
+    if (had) sc = (was != was || sc != sc) ? __uint_as_float(0x7fc00000u) : fmaxf(was, sc);
+    const int64_t b = (int64_t)id * c.Hkv + h;
+    uint4* code = reinterpret_cast<uint4*>((kv ? c.v8 : c.k8) + (b * c.page + (t & (c.page - 1))) * HD) + k % CH;
+    if (k % CH == 0 && (t & (c.page - 1)) == (had ? v.len & (c.page - 1) : 0)) (kv ? c.vs : c.ks)[b] = sc;
+    const bool pow2 = is_pow2(sc);
+    const float inv = pow2 ? __uint_as_float(0x7f000000u - __float_as_uint(sc)) : 0.f;
+    if (tok >= 0) {
+      uint2 o[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t w[4] = {x[i][y].x, x[i][y].y, x[i][y].z, x[i][y].w};
+        float f[8];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          f[2 * z] = __uint_as_float(w[z] << 16);
+          f[2 * z + 1] = __uint_as_float(w[z] & 0xffff0000u);
+        }
+        o[y] = quantise8(f, sc, inv, pow2);
+      }
+      *code = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
+    } else if (sc != was) {  // old codes to the new scale (true for NaN as well)
+      const uint4 u = *code;
+      float f[16];
+      e4m3x4_to_float(u.x, f);
+      e4m3x4_to_float(u.y, f + 4);
+      e4m3x4_to_float(u.z, f + 8);
+      e4m3x4_to_float(u.w, f + 12);
+#pragma unroll
+      for (int y = 0; y < 16; ++y) f[y] *= was;
+      const uint2 lo = quantise8(*reinterpret_cast<const float(*)[8]>(f), sc, inv, pow2);
+      const uint2 hi = quantise8(*reinterpret_cast<const float(*)[8]>(f + 8), sc, inv, pow2);
+      *code = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
   }
 }
 
 // ------------------------------------------------------------------- evict
-// Selection, one block per (sequence, KV head).  A weight's rank key is an
-// unsigned number of the same order (NaN the largest weight, -0 equal to 0);
-// protected tokens take the largest key.  Four passes over 8-bit digits find
-// the key of the last token kept and how many tokens of exactly that key
-// are; those with the lowest positions are.
+// Selection, one cluster of CTAs per (sequence, KV head), each CTA a run of
+// positions whose rank keys it holds in shared memory, so that the weights are
+// read once.  A weight's rank key is an unsigned number of the same order (NaN
+// the largest weight, -0 equal to 0); protected tokens take the largest key.
+// Three passes over 11-, 11- and 10-bit digits find the key of the last token
+// kept (every CTA adds up the cluster's histograms through distributed shared
+// memory) and how many tokens of exactly that key are; those with the lowest
+// positions are.  A prefix sum over threads and CTAs then places the kept
+// tokens in order.
 constexpr int kSelThreads = 1024;
+constexpr int kSelHeld = 44 * 1024;  // keys that a CTA holds; longer runs read the weights again
+constexpr int kSelBins = 2048, kSelCopies = 5, kSelHist = kSelCopies * kSelBins;
+constexpr int kSelRun = 16 * 1024;   // positions per CTA, while a cluster can grow
 
 __device__ __forceinline__ uint32_t rank_key(float w) {
   if (w != w) return 0xfffffffeu;
   const uint32_t b = __float_as_uint(w + 0.f);  // -0 -> 0
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// The weight of a rank key (of a token that is neither protected nor NaN).
+__device__ __forceinline__ float rank_weight(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
 // Exclusive prefix sum over the block's threads; *total gets the sum.
@@ -175,13 +201,17 @@ __device__ __forceinline__ int block_scan(int x, int* red, int* total) {
   return v - x + (w ? red[w - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kSelThreads) bdlm_evict_select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
+__global__ void __launch_bounds__(kSelThreads, 1) bdlm_evict_select_kernel(const EvictParams p, int held) {
+  extern __shared__ __align__(16) uint32_t sel_smem[];
+  uint32_t* hist = sel_smem;                     // [kSelCopies][kSelBins]
+  uint32_t* keys = sel_smem + kSelHist;          // [held]
   __shared__ int red[32];
   __shared__ uint32_t s_digit;
-  __shared__ int s_need;
+  __shared__ int s_need, s_count[2];
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const CacheDesc& c = p.c;
-  const int s = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+  const int s = blockIdx.y, h = blockIdx.x / C, tid = threadIdx.x;
   uint32_t bad = 0;
   const SeqView v = seq_view(c, RowsDesc{nullptr, 0, 0}, s, bad);
   const int64_t cap = (int64_t)c.max_pages << c.lp;
@@ -189,144 +219,229 @@ __global__ void __launch_bounds__(kSelThreads) bdlm_evict_select_kernel(const Ev
   float* wo = p.W_out + ((int64_t)s * c.Hkv + h) * cap;
   int32_t* kept = p.kept + ((int64_t)s * c.Hkv + h) * p.keep;
   const int len = v.len, left = len < p.keep ? len : p.keep;
-  auto key_of = [&](int i) { return i < p.sinks || i >= len - p.recent ? 0xffffffffu : rank_key(w[i]); };
+  // this CTA's positions
+  const int run = (len + C - 1) / C, b0 = min(rank * run, len), n = min(run, len - b0);
+  auto weigh = [&](int i) {  // i: position in the run
+    const int at = b0 + i;
+    return at < p.sinks || at >= len - p.recent ? 0xffffffffu : rank_key(w[at]);
+  };
+  for (int i = tid; i < min(n, held); i += 8 * kSelThreads) {  // (eight loads in flight)
+    uint32_t k[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) k[y] = i + y * kSelThreads < n ? weigh(i + y * kSelThreads) : 0u;
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      if (i + y * kSelThreads < min(n, held)) keys[i + y * kSelThreads] = k[y];
+  }
+  auto key_of = [&](int i) { return i < held ? keys[i] : weigh(i); };
+  for (int i = tid; i < kSelHist; i += kSelThreads) hist[i] = 0;
+  __syncthreads();
   uint32_t thr = 0, mask = 0;
   int need = left;  // tokens still to take among those that match thr under mask
   if (left < len) {
-    for (int sh = 24; sh >= 0; sh -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int i = tid; i < len; i += kSelThreads) {
+    for (int pass = 0; pass < 3; ++pass) {
+      const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, bins = 1 << bits;
+      // the first pass counts every key, most of them in a few digits: its
+      // warps share out kSelCopies - 1 histograms (the last copy is pass 1's)
+      uint32_t* mine = hist + (pass == 1 ? kSelCopies - 1 : 0) * kSelBins;
+      uint32_t* count = pass == 0 ? hist + ((tid >> 5) % (kSelCopies - 1)) * kSelBins : mine;
+      for (int i = tid; i < n; i += kSelThreads) {
         const uint32_t k = key_of(i);
-        if ((k & mask) == thr) atomicAdd(&hist[(k >> sh) & 255], 1);
+        if ((k & mask) == thr) atomicAdd(&count[(k >> sh) & (bins - 1)], 1u);
       }
-      __syncthreads();
-      // digits from the top: the one where the count reaches need
-      int n = tid < 256 ? hist[255 - tid] : 0, total;
-      const int above = block_scan(n, red, &total);
-      if (tid < 256 && above < need && above + n >= need) {
-        s_digit = 255 - tid;
+      if (pass == 0) {
+        __syncthreads();
+        for (int i = tid; i < kSelBins; i += kSelThreads)
+          for (int y = 1; y < kSelCopies - 1; ++y) mine[i] += hist[y * kSelBins + i];
+      }
+      cl.sync();
+      // two bins per thread, digits from the top: the one where the count reaches need
+      const int top = bins - 1 - 2 * tid;
+      int n0 = 0, n1 = 0;
+      if (top > 0)
+        for (int r = 0; r < C; ++r) {
+          const uint2 x = *reinterpret_cast<const uint2*>(cl.map_shared_rank(mine, r) + top - 1);
+          n0 += (int)x.y;
+          n1 += (int)x.x;
+        }
+      int total;
+      const int above = block_scan(n0 + n1, red, &total);
+      if (above < need && above + n0 >= need) {
+        s_digit = (uint32_t)top;
         s_need = need - above;
+      } else if (above + n0 < need && above + n0 + n1 >= need) {
+        s_digit = (uint32_t)top - 1;
+        s_need = need - above - n0;
+      }
+      if (pass == 1) {  // every CTA of the cluster has read the first pass's counts
+        for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
       }
       __syncthreads();
       thr |= s_digit << sh;
-      mask |= 0xffu << sh;
+      mask |= (uint32_t)(bins - 1) << sh;
       need = s_need;
+      __syncthreads();
     }
   }
-  // kept tokens in order of position: a thread takes a run of positions
-  const int per = (len + kSelThreads - 1) / kSelThreads;
-  const int i0 = min(tid * per, len), i1 = min(i0 + per, len);
+  // kept tokens in order of position: a warp takes a run of positions, 32 at a time
+  const int lane = tid & 31, warp = tid >> 5;
+  const unsigned below = (1u << lane) - 1;
+  const int per = ((n + kSelThreads - 1) / kSelThreads) * 32;
+  const int i0 = min(warp * per, n), i1 = min(i0 + per, n);
+  const bool cut = left < len;
   int gt = 0, eq = 0;
-  if (left < len)
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = key_of(i);
-      gt += k > thr;
-      eq += k == thr;
+  if (cut)
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+      const uint32_t k = i < i1 ? key_of(i) : 0u;
+      gt += __popc(__ballot_sync(0xffffffffu, i < i1 && k > thr));
+      eq += __popc(__ballot_sync(0xffffffffu, i < i1 && k == thr));
     }
   else
     gt = i1 - i0;
-  int total;
-  const int eq0 = block_scan(eq, red, &total);
-  const int eq_take = min(max(need - eq0, 0), eq);
-  int at = block_scan(gt + (left < len ? eq_take : 0), red, &total);
-  int eq_left = eq_take;
-  for (int i = i0; i < i1; ++i) {
-    bool take = true;
-    if (left < len) {
-      const uint32_t k = key_of(i);
-      take = k > thr || (k == thr && eq_left > 0);
-      if (k == thr) --eq_left;
-    }
-    if (take) {
-      kept[at] = i;
-      wo[at] = w[i];
-      ++at;
-    }
+  int gt_all, eq_all;
+  int eq0 = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? eq : 0, red, &eq_all), 0);
+  int at = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? gt : 0, red, &gt_all), 0);
+  if (tid == 0) {
+    s_count[0] = gt_all;
+    s_count[1] = eq_all;
   }
-  for (int i = left + tid; i < p.keep; i += kSelThreads) kept[i] = -1;
-  for (int64_t i = left + tid; i < cap; i += kSelThreads) wo[i] = 0.f;
-  if (h == 0 && tid == 0) p.lens_out[s] = left;
+  cl.sync();
+  // what the CTAs before this one keep: all above the key, and of those equal to it the first `need`
+  for (int r = 0; r < rank; ++r) {
+    const int* o = cl.map_shared_rank(s_count, r);
+    at += o[0];
+    eq0 += o[1];
+  }
+  if (cut) at += min(need, eq0);
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    bool take = i < i1;
+    const uint32_t k = take ? key_of(i) : 0u;
+    if (cut) {
+      const unsigned same = __ballot_sync(0xffffffffu, take && k == thr);
+      take = take && (k > thr || (k == thr && eq0 + __popc(same & below) < need));
+      eq0 += __popc(same);
+    }
+    const unsigned taken = __ballot_sync(0xffffffffu, take);
+    if (take) {
+      const int o = at + __popc(taken & below);
+      kept[o] = b0 + i;
+      wo[o] = k >= 0xfffffffeu ? w[b0 + i] : rank_weight(k);
+    }
+    at += __popc(taken);
+  }
+  const int step = C * kSelThreads;
+  for (int i = left + rank * kSelThreads + tid; i < p.keep; i += step) kept[i] = -1;
+  for (int64_t i = left + rank * kSelThreads + tid; i < cap; i += step) wo[i] = 0.f;
+  if (h == 0 && rank == 0 && tid == 0) p.lens_out[s] = left;
   if (bad && tid == 0) atomicOr(p.status, bad);
+  cl.sync();  // no CTA leaves while another may still read its counts
 }
 
-// Moves one block of kept tokens: gathers their codes, finds the new scale,
-// writes the codes in it.  The slab layout is append's.
-template <int HD>
-__global__ void __launch_bounds__(kAppendThreads) bdlm_evict_move_kernel(const EvictParams p, int pages_per_seq) {
-  __shared__ uint32_t red[kAppendThreads / 32];
-  constexpr int CH = HD / 8;
+// Moves the kept tokens of TT = max(page, 64) destination slots, K and V: one
+// thread per token finds its old row and scales, then the CTA gathers all rows
+// with 16-byte loads (HD / 16 lanes to a row), finds each destination block's
+// scale and writes the codes, unchanged where the block's scale is the row's
+// (e4m3 magnitudes compare like integers, so the maximum needs no conversion).
+constexpr int kMoveThreads = 256;
+template <int HD, int TT>
+__global__ void __launch_bounds__(kMoveThreads) bdlm_evict_move_kernel(const EvictParams p) {
+  constexpr int CH = HD / 16;                            // 16-byte chunks of a row
+  constexpr int NT = 2 * TT * CH / kMoveThreads;         // chunks per thread, the first half K's
+  __shared__ int64_t s_row[TT];                          // old row ((page, head) block * page + slot), -1: none
+  __shared__ float s_scale[2][TT];
+  __shared__ uint32_t s_amax[2][TT / 16];
+  __shared__ int s_dst[TT / 16];
   const CacheDesc& c = p.c;
-  const int tps = c.page * HD / 64;
-  const int64_t slab = (int64_t)blockIdx.x * (kAppendThreads / tps) + threadIdx.x / tps;
-  const int tl = threadIdx.x % tps;
-  const int64_t n_slabs = (int64_t)c.n_seqs * pages_per_seq * c.Hkv * 2;
+  const int s = blockIdx.z, h = blockIdx.y, t0 = (int)blockIdx.x * TT, tid = threadIdx.x;
   uint32_t bad = 0;
-  const bool in = slab < n_slabs;
-  const int64_t id = in ? slab : 0;
-  const int kv = (int)(id & 1);
-  const int h = (int)((id >> 1) % c.Hkv);
-  const int64_t sj = (id >> 1) / c.Hkv;
-  const int j = (int)(sj % pages_per_seq), s = (int)(sj / pages_per_seq);
   const SeqView v = seq_view(c, RowsDesc{nullptr, 0, 0}, s, bad);
   const int left = v.len < p.keep ? v.len : p.keep;
-  const int first = j << c.lp;
-  int pid = -1;
-  if (in && first < left) {
-    pid = p.dst[(int64_t)s * c.max_pages + j];
-    if (pid < 0 || pid >= c.n_pages) {
-      bad |= kStatusBadPage;
-      pid = -1;
-    }
-  }
-  const int32_t* kept = p.kept + ((int64_t)s * c.Hkv + h) * p.keep;
-  const uint8_t* from = kv ? c.v8 : c.k8;
-  const float* scales = kv ? c.vs : c.ks;
-  uint2 x[8];
-  float sc[8];
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ch = i * tps + tl, slot = first + ch / CH;
-    x[i] = make_uint2(0, 0);
-    sc[i] = 0.f;
-    if (pid >= 0 && slot < left) {
-      const int pos = kept[slot];
+  if (t0 >= left) return;
+  float a = 0.f, b = 0.f;
+  if (tid < TT) {
+    const int slot = t0 + tid;
+    int64_t row = -1;
+    if (slot < left) {
+      const int pos = p.kept[((int64_t)s * c.Hkv + h) * p.keep + slot];
       const int sp = page_id(c, s, pos >> c.lp, bad);
       if (sp >= 0) {
-        const int64_t b = (int64_t)sp * c.Hkv + h;
-        x[i] = __ldg(reinterpret_cast<const uint2*>(from + (b * c.page + (pos & (c.page - 1))) * HD) + ch % CH);
-        sc[i] = __ldg(scales + b);
+        const int64_t blk = (int64_t)sp * c.Hkv + h;
+        row = blk * c.page + (pos & (c.page - 1));
+        a = c.ks[blk];
+        b = c.vs[blk];
       }
     }
+    s_row[tid] = row;
+  } else if (tid - TT < TT / 16) {
+    const int j = tid - TT, slot = t0 + (j << c.lp);  // destination page j of this CTA
+    int id = -1;
+    if (j < (TT >> c.lp) && slot < left) {
+      id = p.dst[(int64_t)s * c.max_pages + (slot >> c.lp)];
+      if (id < 0 || id >= c.n_pages) {
+        bad |= kStatusBadPage;
+        id = -1;
+      }
+    }
+    s_dst[j] = id;
+    s_amax[0][j] = s_amax[1][j] = 0;
   }
+  __syncthreads();
+  uint4 x[NT];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float f[8];
-    e4m3x4_to_float(x[i].x, f);
-    e4m3x4_to_float(x[i].y, f + 4);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) amax = umax2(amax, __float_as_uint(f[k] * sc[i]) & 0x7fffffffu);
+  for (int i = 0; i < NT; ++i) {
+    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kMoveThreads + tid;
+    const int64_t row = s_row[k / CH];
+    x[i] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>((kv ? c.v8 : c.k8) + row * HD) + k % CH)
+                    : make_uint4(0, 0, 0, 0);
   }
-  amax = group_max(amax, tps, red);
-  if (pid >= 0) {
-    const float ns = block_scale(amax);
-    const bool pow2 = is_pow2(ns);
-    const float inv = pow2 ? __uint_as_float(0x7f000000u - __float_as_uint(ns)) : 0.f;
-    const int64_t b = (int64_t)pid * c.Hkv + h;
-    uint2* codes = reinterpret_cast<uint2*>((kv ? c.v8 : c.k8) + b * c.page * HD);
+  if (tid < TT) {  // (the scales arrive while the rows do)
+    s_scale[0][tid] = a;
+    s_scale[1][tid] = b;
+  }
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ch = i * tps + tl;
-      if (first + ch / CH >= left) continue;
+  for (int i = 0; i < NT; ++i) {
+    const int kv = i >= NT / 2, tok = ((i % (NT / 2)) * kMoveThreads + tid) / CH;
+    const uint32_t m4 = __vmaxu4(__vmaxu4(x[i].x & 0x7f7f7f7fu, x[i].y & 0x7f7f7f7fu),
+                                 __vmaxu4(x[i].z & 0x7f7f7f7fu, x[i].w & 0x7f7f7f7fu));
+    uint32_t top = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) top = umax2(top, (m4 >> (8 * b)) & 0xffu);
+    const uint32_t hv = e4m3x2_to_half2(top);
+    const float val = __half22float2(*reinterpret_cast<const __half2*>(&hv)).x * s_scale[kv][tok];
+    uint32_t bits = s_row[tok] >= 0 ? __float_as_uint(val) & 0x7fffffffu : 0u;
+    // a warp's rows belong to one destination page
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) bits = umax2(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+    if ((tid & 31) == 0) atomicMax(&s_amax[kv][tok >> c.lp], bits);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kMoveThreads + tid, tok = k / CH, j = tok >> c.lp;
+    const int id = s_dst[j];
+    if (t0 + tok >= left || id < 0) continue;
+    const float ns = block_scale(s_amax[kv][j]), sc = s_scale[kv][tok];
+    uint4 o = x[i];
+    if (sc != ns) {
+      const bool pow2 = is_pow2(ns);
+      const float inv = pow2 ? __uint_as_float(0x7f000000u - __float_as_uint(ns)) : 0.f;
       float f[8];
       e4m3x4_to_float(x[i].x, f);
       e4m3x4_to_float(x[i].y, f + 4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= sc[i];
-      codes[ch] = quantise8(f, ns, inv, pow2);
+      for (int y = 0; y < 8; ++y) f[y] *= sc;
+      const uint2 lo = quantise8(f, ns, inv, pow2);
+      e4m3x4_to_float(x[i].z, f);
+      e4m3x4_to_float(x[i].w, f + 4);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) f[y] *= sc;
+      const uint2 hi = quantise8(f, ns, inv, pow2);
+      o = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
-    if (tl == 0) (kv ? c.vs : c.ks)[b] = ns;
+    const int64_t blk = (int64_t)id * c.Hkv + h;
+    *(reinterpret_cast<uint4*>((kv ? c.v8 : c.k8) + (blk * c.page + (tok & (c.page - 1))) * HD) + k % CH) = o;
+    if (k % CH == 0 && (tok & (c.page - 1)) == 0) (kv ? c.vs : c.ks)[blk] = ns;
   }
   if (bad) atomicOr(p.status, bad);
 }
@@ -334,31 +449,49 @@ __global__ void __launch_bounds__(kAppendThreads) bdlm_evict_move_kernel(const E
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* launches) {
-  const int per = (p.r.max_rows + p.c.page - 2) / p.c.page + 1;  // pages that max_rows new tokens can touch
-  const int64_t slabs = (int64_t)p.c.n_seqs * per * p.c.Hkv * 2;
-  const int in_block = kAppendThreads / (p.c.page * p.c.d / 64);
-  const int64_t blocks = (slabs + in_block - 1) / in_block;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (p.c.d == 128) bdlm_cache_append_kernel<128><<<(unsigned)blocks, kAppendThreads, 0, st>>>(p, per);
-  else bdlm_cache_append_kernel<64><<<(unsigned)blocks, kAppendThreads, 0, st>>>(p, per);
+  const int TT = p.c.page > 64 ? 128 : 64;
+  // groups of TT slots that max_rows new tokens can touch
+  const dim3 grid((unsigned)((p.r.max_rows + TT - 2) / TT + 1), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
+  auto k = p.c.d == 128 ? (TT == 128 ? bdlm_cache_append_kernel<128, 128> : bdlm_cache_append_kernel<128, 64>)
+                        : (TT == 128 ? bdlm_cache_append_kernel<64, 128> : bdlm_cache_append_kernel<64, 64>);
+  k<<<grid, kAppendThreads * TT / 64, 0, st>>>(p);
   ++*launches;
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t st, int* launches) {
-  bdlm_evict_select_kernel<<<dim3(p.c.Hkv, p.c.n_seqs), kSelThreads, 0, st>>>(p);
-  ++*launches;
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const int64_t cap = (int64_t)p.c.max_pages << p.c.lp;
+  // a CTA for each kSelRun positions of the longest sequence, up to the portable
+  // cluster size; more, down to kSelRun / 8 positions, while the GPU has room
+  int C = 1;
+  while (C < 8 && (int64_t)C * kSelRun < cap) C *= 2;
+  while (C < 8 && (int64_t)C * kSelRun / 8 < cap && (int64_t)p.c.n_seqs * p.c.Hkv * C * 2 <= 152) C *= 2;
+  const int64_t run = (cap + C - 1) / C;
+  const int held = (int)(run < kSelHeld ? run : kSelHeld);
+  const int bytes = (kSelHist + held) * (int)sizeof(uint32_t);
+  cudaError_t e = cudaFuncSetAttribute(bdlm_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (kSelHist + kSelHeld) * (int)sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.c.Hkv * C), (unsigned)p.c.n_seqs);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, bdlm_evict_select_kernel, p, held);
+  if (e != cudaSuccess) return e;
+  ++*launches;
   const int64_t most = p.keep < cap ? p.keep : cap;
-  const int per = (int)((most + p.c.page - 1) / p.c.page);
-  const int64_t slabs = (int64_t)p.c.n_seqs * per * p.c.Hkv * 2;
-  const int in_block = kAppendThreads / (p.c.page * p.c.d / 64);
-  const int64_t blocks = (slabs + in_block - 1) / in_block;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (p.c.d == 128) bdlm_evict_move_kernel<128><<<(unsigned)blocks, kAppendThreads, 0, st>>>(p, per);
-  else bdlm_evict_move_kernel<64><<<(unsigned)blocks, kAppendThreads, 0, st>>>(p, per);
+  const int TT = p.c.page > 64 ? 128 : 64;
+  const dim3 grid((unsigned)((most + TT - 1) / TT), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
+  auto move = p.c.d == 128 ? (TT == 128 ? bdlm_evict_move_kernel<128, 128> : bdlm_evict_move_kernel<128, 64>)
+                           : (TT == 128 ? bdlm_evict_move_kernel<64, 128> : bdlm_evict_move_kernel<64, 64>);
+  move<<<grid, kMoveThreads, 0, st>>>(p);
   ++*launches;
   return cudaGetLastError();
 }

@@ -609,7 +609,7 @@ class BdlmCache:
 
 
 def _check_tensor(name, t, dtype, shape, device):
-    if t.device != device or not t.is_cuda or not t.is_contiguous() or t.dtype != dtype or tuple(t.shape) != shape:
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device} (a CUDA "
                          f"device), not {t.dtype} {list(t.shape)} on {t.device}"
                          f"{'' if t.is_contiguous() else ', not contiguous'}")
@@ -627,23 +627,27 @@ def _cache_rows(cache, row_offsets, max_rows, T):
     return row_offsets.data_ptr(), T if max_rows is None else max_rows
 
 
-def _cache_call(name, cache, stream, args, tensors=()):
-    """Calls entry point `name` with the current (or given) stream of the cache's device appended; `tensors` made by
-    this call are marked as used on a given stream."""
-    cuda = _torch().cuda
+def _cache_call(fn, cache, stream, args, tensors=()):
+    """Calls an entry point with the current (or given) stream of the cache's device appended; `tensors` made by this
+    call are marked as used on a given stream."""
+    torch = _torch()
+    cuda = torch.cuda
     if stream is None:
-        stream = cuda.current_stream(cache.device)
+        raw = torch._C._cuda_getCurrentRawStream(cache.device.index)  # (torch.cuda.current_stream costs 2 us a call)
     else:
         if stream.device != cache.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
-        for t in tensors:
-            t.record_stream(stream)
-    fn = getattr(load_library(), name)
+        raw = stream.cuda_stream
+        if tensors:
+            # made on the current stream, where their memory may have had other users: the call waits for those
+            stream.wait_stream(cuda.current_stream(cache.device))
+            for t in tensors:
+                t.record_stream(stream)
     if cuda.current_device() == cache.device.index:
-        status = fn(*args, stream.cuda_stream)
+        status = fn(*args, raw)
     else:
         with cuda.device(cache.device):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, raw)
     if status:
         _check(status)
 
@@ -693,7 +697,7 @@ def bdlm_cache_append(cache, K, V, row_offsets=None, max_rows: int | None = None
     else:
         _check_tensor("lens_out", lens_out, torch.int32, (cache.n_seqs,), cache.device)
     ws = _cache_workspace(cache, workspace, made, 256)
-    _cache_call("bdlm_cache_append", cache, stream,
+    _cache_call(load_library().bdlm_cache_append, cache, stream,
                 (K.data_ptr(), V.data_ptr(), cache._ref, off, T, max_rows, lens_out.data_ptr(), ws.data_ptr(),
                  ws.numel()), made)
     return lens_out
@@ -715,8 +719,8 @@ def bdlm_attn_cached(Qn, Kn, Vn, cache, row_offsets=None, max_rows: int | None =
     off, max_rows = _cache_rows(cache, row_offsets, max_rows, T)
     made = []
     if out is None:
-        O = torch.empty((T, Hq, d), dtype=torch.bfloat16 if o_dtype is None else o_dtype, device=cache.device)
-        LSE = torch.empty((Hq, T), dtype=torch.float32, device=cache.device)
+        O = torch.empty_like(Qn) if o_dtype is None or o_dtype is torch.bfloat16 else Qn.new_empty((T, Hq, d), dtype=o_dtype)
+        LSE = Qn.new_empty((Hq, T), dtype=torch.float32)
         made += [O, LSE]
     else:
         O, LSE = out
@@ -727,7 +731,7 @@ def bdlm_attn_cached(Qn, Kn, Vn, cache, row_offsets=None, max_rows: int | None =
     ws = _cache_workspace(cache, workspace, made,
                           max(bdlm_workspace_size_cache(cache.n_seqs, Hq, cache.Hkv, d, max_rows), 256)
                           if workspace is None else 0)
-    _cache_call("bdlm_attn_cached", cache, stream,
+    _cache_call(load_library().bdlm_attn_cached, cache, stream,
                 (Qn.data_ptr(), None if Kn is None else Kn.data_ptr(), None if Vn is None else Vn.data_ptr(), cache._ref,
                  off, T, max_rows, Hq, 1.0 / math.sqrt(d) if scale is None else scale, O.data_ptr(),
                  F32 if O.dtype == torch.float32 else BF16, LSE.data_ptr(), ws.data_ptr(), ws.numel()), made)
@@ -748,7 +752,7 @@ def bdlm_cache_weights(Qn, LSE, cache, weights, row_offsets=None, max_rows: int 
     off, max_rows = _cache_rows(cache, row_offsets, max_rows, T)
     made = []
     ws = _cache_workspace(cache, workspace, made, 256)
-    _cache_call("bdlm_cache_weights", cache, stream,
+    _cache_call(load_library().bdlm_cache_weights, cache, stream,
                 (Qn.data_ptr(), LSE.data_ptr(), cache._ref, off, T, max_rows, Hq,
                  1.0 / math.sqrt(d) if scale is None else scale, weights.data_ptr(), ws.data_ptr(), ws.numel()), made)
     return weights
@@ -775,7 +779,7 @@ def bdlm_cache_evict(cache, weights, dst_table, keep: int, sinks: int = 0, recen
     _check_tensor("weights_out", weights_out, torch.float32, shape, cache.device)
     _check_tensor("kept", kept, torch.int32, (cache.n_seqs, cache.Hkv, max(int(keep), 0)), cache.device)
     ws = _cache_workspace(cache, workspace, made, 256)
-    _cache_call("bdlm_cache_evict", cache, stream,
+    _cache_call(load_library().bdlm_cache_evict, cache, stream,
                 (cache._ref, weights.data_ptr(), dst_table.data_ptr(), keep, sinks, recent, lens_out.data_ptr(),
                  weights_out.data_ptr(), kept.data_ptr() or None, ws.data_ptr(), ws.numel()), made)
     return lens_out, weights_out, kept

@@ -212,7 +212,13 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     p.sp.tile_rows = cached_tile_rows(flat);
     p.sp.extra = p.sp.tile_rows == kSmallRows ? kSmallExtra : kTcExtra;
     p.sp.keyed = 0;
+    p.whole = 0;
     p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
+    const int64_t segs = (flat + kSmallRows - 1) / kSmallRows * p.c.Hkv * p.c.n_seqs;
+    if (p.sp.tile_rows == kSmallRows && (int64_t)p.c.max_pages * p.c.page <= kWholeKeys && segs <= 0x7fffffff) {
+      p.whole = (int)((flat + kSmallRows - 1) / kSmallRows);
+      p.G = (int)segs;
+    }
     CachedMaps maps;
     if (p.sp.tile_rows != kSmallRows) {
       EncodeTiledFn enc;
@@ -228,7 +234,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     cudaError_t e = p.sp.tile_rows == kSmallRows ? launch_cached_small(p, st, &launches)
                                                  : launch_cached_tc(maps, p, st, &launches);
     abi_timer_end(tm);
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && !p.whole) {
       tm = abi_timer_begin(ABI_T_CACHED_MERGE, st);
       e = launch_cached_merge(p, st, &launches);
       abi_timer_end(tm);

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 
 #include "cache_ops.h"
+#include "kernels.h"
 #include "ptx.cuh"
 
 namespace cg = cooperative_groups;
@@ -448,6 +449,17 @@ __global__ void __launch_bounds__(kMoveThreads) bdlm_evict_move_kernel(const Evi
 
 }  // namespace
 
+cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* launches) {
   const int TT = p.c.page > 64 ? 128 : 64;
   // groups of TT slots that max_rows new tokens can touch
@@ -469,8 +481,9 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t st, int* launc
   const int64_t run = (cap + C - 1) / C;
   const int held = (int)(run < kSelHeld ? run : kSelHeld);
   const int bytes = (kSelHist + held) * (int)sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(bdlm_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (kSelHist + kSelHeld) * (int)sizeof(uint32_t));
+  static std::atomic<uint64_t> raised{0};
+  cudaError_t e = raise_smem(reinterpret_cast<const void*>(bdlm_evict_select_kernel),
+                             (kSelHist + kSelHeld) * (int)sizeof(uint32_t), raised);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.c.Hkv * C), (unsigned)p.c.n_seqs);

@@ -20,6 +20,7 @@ struct CachedParams {
   float* LSE;
   float* part;  // two partial results per CTA of G
   int G;
+  int whole;    // not 0: a CTA per segment, that many row tiles for each (sequence, KV head)
   uint32_t* status;
   uint64_t limit_ns;
 };
@@ -31,6 +32,10 @@ __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (i
 
 constexpr int kSmallRows = 16;      // row tile of the mma.sync kernel
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
+// Longest cache, in tokens, up to which the mma.sync kernel gives each segment
+// one CTA: no work list to walk and nothing to merge, against a split of so
+// few keys.
+constexpr int kWholeKeys = 512;
 constexpr int kSmallExtra = 1, kTcExtra = 3;  // AttnSplit::extra: what a segment costs beside its units
 
 // Row tile of a call whose sequences have at most `flat` rows times heads of

@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 
 #include "cached_attn.h"
+#include "kernels.h"
 #include "ptx.cuh"
 
 namespace bdlm {
@@ -136,12 +137,28 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint32_t bad = 0;
   const CacheDesc& c = p.c;
-  const int64_t U = total_units(c, p.r, p.sp, bad);
-  const int G = split_ctas(U, p.G), cta = blockIdx.x;
-  if (cta < G) {
-    const int64_t u0 = split_begin(U, G, cta), u1 = split_begin(U, G, cta + 1);
-    UnitPos pos = locate_unit(c, p.r, p.sp, u0, bad);
-    SegInfo seg = seg_info(c, p.r, p.sp, pos.s, bad);
+  const int cta = blockIdx.x;
+  int64_t u0 = 0, u1 = 0;
+  UnitPos pos{0, 0, 0, 0};
+  SegInfo seg;
+  launch_dependents();
+  if (p.whole) {  // CTA per segment: (sequence, KV head, row tile), p.whole row tiles for each
+    pos.rt = cta % p.whole;
+    pos.h = cta / p.whole % c.Hkv;
+    pos.s = cta / p.whole / c.Hkv;
+    seg = seg_info(c, p.r, p.sp, pos.s, bad);
+    u1 = pos.rt < seg.rtiles ? seg.span : 0;
+  } else {
+    const int64_t U = total_units(c, p.r, p.sp, bad);
+    const int G = split_ctas(U, p.G);
+    if (cta < G) {
+      u0 = split_begin(U, G, cta);
+      u1 = split_begin(U, G, cta + 1);
+      pos = locate_unit(c, p.r, p.sp, u0, bad);
+      seg = seg_info(c, p.r, p.sp, pos.s, bad);
+    }
+  }
+  {
     for (int64_t u = u0; u < u1;) {
       int jb, je;
       split_units(seg, p.sp, pos, u, u1, jb, je);
@@ -469,6 +486,9 @@ __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const 
   const int cta = blockIdx.x;
   const int64_t U = total_units(c, p.r, p.sp, bad);
   const int G = split_ctas(U, p.G);
+  // (the kernel before this one may still run; every thread waits for it, so
+  // that this grid's end implies that one's)
+  dependency_wait();
   if (cta >= G - 1) return;
   const int64_t u0 = split_begin(U, G, cta), u1 = split_begin(U, G, cta + 1);
   const UnitPos pos = locate_unit(c, p.r, p.sp, u1 - 1, bad);
@@ -538,22 +558,29 @@ __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const 
 }  // namespace
 
 cudaError_t launch_cached_small(const CachedParams& p, cudaStream_t st, int* launches) {
+  // (at most 34.3 KB: within the default limit)
   const int bytes = (kWarps * kSmallRows * (p.c.d + 4) + kWarps * kSmallRows * 2) * (int)sizeof(float);
   auto k = p.c.d == 128 ? (p.o_f32 ? bdlm_cached_small_kernel<128, true> : bdlm_cached_small_kernel<128, false>)
                         : (p.o_f32 ? bdlm_cached_small_kernel<64, true> : bdlm_cached_small_kernel<64, false>);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
   k<<<p.G, 32 * kWarps, bytes, st>>>(p);
   ++*launches;
   return cudaGetLastError();
 }
 
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches) {
-  const dim3 grid(p.G, p.sp.tile_rows / kMergeRows);
-  if (p.c.d == 128) bdlm_cached_merge_kernel<128><<<grid, kMergeThreads, 0, st>>>(p);
-  else bdlm_cached_merge_kernel<64><<<grid, kMergeThreads, 0, st>>>(p);
-  ++*launches;
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.G, (unsigned)(p.sp.tile_rows / kMergeRows));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // may start before the attention kernel's end
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = p.c.d == 128 ? cudaLaunchKernelEx(&cfg, bdlm_cached_merge_kernel<128>, p)
+                                     : cudaLaunchKernelEx(&cfg, bdlm_cached_merge_kernel<64>, p);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 }  // namespace bdlm

@@ -42,6 +42,7 @@
 
 #include "cached_attn.h"
 #include "cached_tc.cuh"
+#include "kernels.h"
 
 namespace bdlm {
 namespace {
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  launch_dependents();
   const Watchdog wd{p.status, p.limit_ns, abort_flag};
   const CacheDesc& c = p.c;
   // the n-th piece (null: none left, or gave up); its slot stays this thread's until done(n)
@@ -951,7 +953,8 @@ cudaError_t launch(const CachedMaps& m, const CachedParams& p, cudaStream_t st) 
     return fa.numRegs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
   }();
   if (ready != cudaSuccess) return ready;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<HD>::kAlloc);
+  static std::atomic<uint64_t> raised{0};
+  const cudaError_t e = raise_smem(reinterpret_cast<const void*>(k), Lay<HD>::kAlloc, raised);
   if (e != cudaSuccess) return e;
   k<<<p.G, kThreads, Lay<HD>::kAlloc, st>>>(m.k8, m.k, m.v, p);
   return cudaGetLastError();

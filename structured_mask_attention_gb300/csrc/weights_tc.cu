@@ -17,6 +17,7 @@
 // together and then take alternate key tiles (256 TMEM columns each).
 #include "cache_ops.h"
 #include "cached_tc.cuh"
+#include "kernels.h"
 
 namespace bdlm {
 namespace {
@@ -350,14 +351,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_cache_weights(const CUtensorMap& k8, const WeightsParams& p, cudaStream_t st, int* launches) {
-  auto k = p.c.d == 128 ? bdlm_cache_weights_kernel<128> : bdlm_cache_weights_kernel<64>;
-  const int bytes = p.c.d == 128 ? LayW<128>::kAlloc : LayW<64>::kAlloc;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <int HD>
+static cudaError_t launch(const CUtensorMap& k8, const WeightsParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  const cudaError_t e =
+      raise_smem(reinterpret_cast<const void*>(bdlm_cache_weights_kernel<HD>), LayW<HD>::kAlloc, raised);
   if (e != cudaSuccess) return e;
-  k<<<p.G, kThreads, bytes, st>>>(k8, p);
-  ++*launches;
+  bdlm_cache_weights_kernel<HD><<<p.G, kThreads, LayW<HD>::kAlloc, st>>>(k8, p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_cache_weights(const CUtensorMap& k8, const WeightsParams& p, cudaStream_t st, int* launches) {
+  const cudaError_t e = p.c.d == 128 ? launch<128>(k8, p, st) : launch<64>(k8, p, st);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 }  // namespace bdlm

@@ -129,24 +129,32 @@ __device__ __forceinline__ void scores16(uint32_t (&a)[32], float f, float lf, f
   }
 }
 
-// p = exp2(s f + n) of 32 scores in place, and the sums of the first and the last 16.
+// p = exp2(s f + n) of 32 scores in place, and the sums of the first and the
+// last 16.  The exponentials are issued side by side (volatile: in this order),
+// not each followed by its use.
 __device__ __forceinline__ void exp32(uint32_t (&a)[32], float f, float n, float& s0, float& s1) {
   const uint64_t f2x = f2(f, f), n2 = f2(n, n);
-  uint64_t r[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     float x0, x1;
     f2_split(f2_fma(f2(__uint_as_float(a[c]), __uint_as_float(a[c + 1])), f2x, n2), x0, x1);
-    x0 = ex2_approx(x0);
-    x1 = ex2_approx(x1);
-    r[c >> 4] = f2_add(r[c >> 4], f2(x0, x1));
     a[c] = __float_as_uint(x0);
     a[c + 1] = __float_as_uint(x1);
   }
+#pragma unroll
+  for (int c = 0; c < 32; ++c) asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+r"(a[c]));
+  uint64_t r[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) r[y] = f2(__uint_as_float(a[8 * y]), __uint_as_float(a[8 * y + 1]));
+#pragma unroll
+  for (int c = 2; c < 8; c += 2)
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      r[y] = f2_add(r[y], f2(__uint_as_float(a[8 * y + c]), __uint_as_float(a[8 * y + c + 1])));
   float x, y;
-  f2_split(r[0], x, y);
+  f2_split(f2_add(r[0], r[1]), x, y);
   s0 = x + y;
-  f2_split(r[1], x, y);
+  f2_split(f2_add(r[2], r[3]), x, y);
   s1 = x + y;
 }
 
@@ -483,14 +491,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ts(tmem + 256 + t * 128, tmem + t * 128 + col + p_col(kk), v + kk * 128, desc_hi(2, 1024), id,
                    (kk > 0 || !first) ? 1u : 0u);
         };
-        auto issue_pv = [&](int t, uint32_t w, bool own, bool first) {
+        // (first: the piece's first product; fresh: the last piece's O may still be read)
+        auto issue_pv = [&](int t, uint32_t w, bool own, bool first, bool fresh) {
           if (!mbar_wait(BAR(B_PF + t), bit(pph, t), wd, 31)) return false;
           flip(pph, t);
-          if (first) {
+          if (fresh) {
             if (!mbar_wait(BAR(B_OE + t), bit(oph, t), wd, 32)) return false;
             flip(oph, t);
           }
-          if (!mbar_wait(BAR(B_WF + (w & 1)), (w >> 1) & 1, wd, 33)) return false;
+          if ((KS || t == 0) && !mbar_wait(BAR(B_WF + (w & 1)), (w >> 1) & 1, wd, 33)) return false;
           tc_fence_after();
           pv(t, w, 0, own, first);
           if (FINE) pv(t, w, 16, own, false);
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = start_s(0) && (n < 2 || start_s(1));
             for (int j = 0; ok && j < n; ++j, ++wc) {
               const int t = j & 1;
-              ok = issue_pv(t, wc, own(j), j < 2);
+              ok = issue_pv(t, wc, own(j), j < 2, j < 2);
               if (!ok) break;
               tc_commit(BAR(B_WE + (wc & 1)));
               if (j + 2 >= n) tc_commit(BAR(B_OD + t));
@@ -542,9 +551,53 @@ __global__ void __launch_bounds__(kThreads, 1)
               issue_s(1, own(0));
               free_k(own(0));
             }
-            for (int j = 0; ok && j < n; ++j, ++wc) {
+            int j = 0;
+            // cached tiles that a cached tile follows: the waits, products and
+            // commits alone (whatever else this thread does idles the tensor
+            // cores: their queue holds about one product)
+            if (!FINE && nk > 1) {
+              ok = ok && mbar_wait(BAR(B_OE + 0), oph & 1, wd, 32) && mbar_wait(BAR(B_OE + 1), oph & 1, wd, 32);
+              oph ^= 1;
+              for (; ok && j + 1 < nk; ++j, ++wc) {
+                const uint32_t acc = j > 0, vt = desc_lo(base + LY::kW + (wc & 1) * LY::kWBytes, kSlot);
+                const uint32_t kt = desc_lo(base + LY::kK + ks * kSlot, 16), q = desc_lo(base + LY::kQ, 16);
+                constexpr uint32_t HV = desc_hi(2, 1024), HQ = desc_hi(SWQ, SBO8);
+                ok = mbar_wait(BAR(B_WF + (wc & 1)), (wc >> 1) & 1, wd, 33) && mbar_wait(BAR(B_KF + ks), kph, wd, 30) &&
+                     mbar_wait(BAR(B_PF + 0), pph & 1, wd, 31);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_ts(tmem + 256, tmem + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                  constexpr int n8 = HD / 32;
+                  mma_ss<true>(tmem, q + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ, kt + (kk % n8) * 2, HQ, kId8, kk > 0);
+                }
+                tc_commit(BAR(B_SF + 0));
+                ok = mbar_wait(BAR(B_PF + 1), pph & 1, wd, 31);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_ts(tmem + 384, tmem + 128 + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+                tc_commit(BAR(B_WE + (wc & 1)));
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                  constexpr int n8 = HD / 32;
+                  mma_ss<true>(tmem + 128, q + (LY::kQBytes >> 4) + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ,
+                               kt + (kk % n8) * 2, HQ, kId8, kk > 0);
+                }
+                tc_commit(BAR(B_SF + 1));
+                tc_commit(BAR(B_KE + ks));
+                if (++ks == NK) ks = 0, kph ^= 1;
+                pph ^= 1;
+              }
+            }
+            const bool opened = !FINE && nk > 1;
+            for (; ok && j < n; ++j, ++wc) {
               const bool last = j == n - 1, swap = j + 1 == nk && !last;
-              ok = issue_pv(0, wc, own(j), j == 0);
+              ok = issue_pv(0, wc, own(j), j == 0, j == 0 && !opened);
               if (!ok) break;
               if (last) tc_commit(BAR(B_OD + 0));
               if (!last) {
@@ -552,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 issue_s(0, own(j + 1));
               }
-              ok = issue_pv(1, wc, own(j), j == 0);
+              ok = issue_pv(1, wc, own(j), j == 0, j == 0 && !opened);
               if (!ok) break;
               tc_commit(BAR(B_WE + (wc & 1)));
               if (last) {

@@ -105,13 +105,13 @@ size_t attn_space(int64_t flat, int d) {
   return (size_t)cached_ctas(tile, kSmsMax) * 2 * part_floats(tile, d) * sizeof(float);
 }
 
-// K's codes: boxes of one (page, KV head) block, swizzled by the row's bytes.
-bdlm_status encode_codes(EncodeTiledFn fn, CUtensorMap* m, const CacheDesc& c) {
+// Codes: boxes of one (page, KV head) block, swizzled by the row's bytes.
+bdlm_status encode_codes(EncodeTiledFn fn, CUtensorMap* m, const CacheDesc& c, uint8_t* codes) {
   cuuint64_t dims[3] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)(c.n_pages * c.Hkv)};
   cuuint64_t strides[2] = {(cuuint64_t)c.d, (cuuint64_t)c.d * c.page};
   cuuint32_t box[3] = {(cuuint32_t)c.d, (cuuint32_t)c.page, 1};
   cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k8, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return abi_fail(BDLM_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
@@ -210,20 +210,23 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
     p.limit_ns = abi_wait_limit_ns();
     p.sp.tile_rows = cached_tile_rows(flat);
-    p.sp.extra = p.sp.tile_rows == kSmallRows ? kSmallExtra : kTcExtra;
+    const bool small = p.sp.tile_rows <= kSmallRows;
+    p.sp.extra = small ? kSmallExtra : kTcExtra;
     p.sp.keyed = 0;
     p.whole = 0;
     p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
-    const int64_t segs = (flat + kSmallRows - 1) / kSmallRows * p.c.Hkv * p.c.n_seqs;
-    if (p.sp.tile_rows == kSmallRows && (int64_t)p.c.max_pages * p.c.page <= kWholeKeys && segs <= 0x7fffffff) {
-      p.whole = (int)((flat + kSmallRows - 1) / kSmallRows);
-      p.G = (int)segs;
+    const int64_t rt = (flat + p.sp.tile_rows - 1) / p.sp.tile_rows;
+    if (small && (int64_t)p.c.max_pages * p.c.page <= kWholeKeys && rt * p.c.Hkv * p.c.n_seqs <= 0x7fffffff) {
+      p.whole = (int)rt;
+      p.G = (int)(rt * p.c.Hkv * p.c.n_seqs);
     }
     CachedMaps maps;
-    if (p.sp.tile_rows != kSmallRows) {
-      EncodeTiledFn enc;
-      CACHE_CHECK(abi_encoder(&enc));
-      CACHE_CHECK(encode_codes(enc, &maps.k8, p.c));
+    EncodeTiledFn enc;
+    CACHE_CHECK(abi_encoder(&enc));
+    CACHE_CHECK(encode_codes(enc, &maps.k8, p.c, p.c.k8));
+    if (small) {
+      CACHE_CHECK(encode_codes(enc, &maps.v8, p.c, p.c.v8));
+    } else {
       // without own keys these maps are not used: any valid tensor encodes
       CACHE_CHECK(encode_rows(enc, &maps.k, Kn ? Kn : Qn, rows, Kn ? p.c.Hkv : Hq, p.c.d));
       CACHE_CHECK(encode_rows(enc, &maps.v, Vn ? Vn : Qn, rows, Vn ? p.c.Hkv : Hq, p.c.d));
@@ -231,8 +234,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int launches = 0;
     void* tm = abi_timer_begin(ABI_T_ATTN_CACHED, st);
-    cudaError_t e = p.sp.tile_rows == kSmallRows ? launch_cached_small(p, st, &launches)
-                                                 : launch_cached_tc(maps, p, st, &launches);
+    cudaError_t e = small ? launch_cached_small(maps, p, st, &launches) : launch_cached_tc(maps, p, st, &launches);
     abi_timer_end(tm);
     if (e == cudaSuccess && !p.whole) {
       tm = abi_timer_begin(ABI_T_CACHED_MERGE, st);
@@ -270,7 +272,7 @@ bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cach
     EncodeTiledFn enc;
     CUtensorMap k8;
     CACHE_CHECK(abi_encoder(&enc));
-    CACHE_CHECK(encode_codes(enc, &k8, p.c));
+    CACHE_CHECK(encode_codes(enc, &k8, p.c, p.c.k8));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int launches = 0;
     void* tm = abi_timer_begin(ABI_T_WEIGHTS, st);

@@ -30,27 +30,29 @@ struct CachedParams {
 // side by side), then the rows' reference maxima (log2 units) and sums.
 __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (int64_t)tile_rows * (d + 2); }
 
-constexpr int kSmallRows = 16;      // row tile of the mma.sync kernel
+constexpr int kSmallRows = 64;      // rows up to which the mma.sync kernel takes a call
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
+
+// Row tile of a call whose sequences have at most `flat` rows times heads of
+// a group: 16, 32 or 64 (mma.sync), 128 or 256 (tcgen05, split and pairs).
+inline int cached_tile_rows(int64_t flat) {
+  return flat <= 16 ? 16 : flat <= 32 ? 32 : flat <= kSmallRows ? 64 : flat <= 128 ? 128 : 256;
+}
+inline int cached_ctas(int tile_rows, int sms) { return tile_rows <= kSmallRows ? sms * kSmallCtasPerSm : sms; }
+
+// Tensor maps: the codes as [n_pages * Hkv, page, d] (V's for the mma.sync
+// kernel), the new rows' K and V as [T, Hkv, d] bf16 (for the tcgen05 kernel).
+struct CachedMaps {
+  CUtensorMap k8, v8, k, v;
+};
+cudaError_t launch_cached_tc(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 // Longest cache, in tokens, up to which the mma.sync kernel gives each segment
 // one CTA: no work list to walk and nothing to merge, against a split of so
 // few keys.
 constexpr int kWholeKeys = 512;
 constexpr int kSmallExtra = 1, kTcExtra = 3;  // AttnSplit::extra: what a segment costs beside its units
 
-// Row tile of a call whose sequences have at most `flat` rows times heads of
-// a group: 16 (mma.sync), 128 or 256 (tcgen05, split and pairs).
-inline int cached_tile_rows(int64_t flat) { return flat <= kSmallRows ? kSmallRows : flat <= 128 ? 128 : 256; }
-inline int cached_ctas(int tile_rows, int sms) { return tile_rows == kSmallRows ? sms * kSmallCtasPerSm : sms; }
-
-// Tensor maps of the tcgen05 kernel: K's codes as [n_pages * Hkv, page, d],
-// the new rows' K and V as [T, Hkv, d] bf16.
-struct CachedMaps {
-  CUtensorMap k8, k, v;
-};
-cudaError_t launch_cached_tc(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
-
-cudaError_t launch_cached_small(const CachedParams& p, cudaStream_t st, int* launches);
+cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches);
 
 }  // namespace bdlm

@@ -1,9 +1,14 @@
-// cached_small.cu -- attention of few rows over the 8-bit cache: mma.sync
-// tiles of 16 rows, and the merge of partial results.
+// cached_small.cu -- attention of up to 64 rows over the 8-bit cache on mma.sync
+// tiles, and the merge of partial results.
 //
-// One token of a sequence gives Hq / Hkv rows per KV head, a handful against
-// thousands of keys: every cached byte is read once and used for one or two
-// 16-row MMA tiles, so the kernel's only bound is the stream of codes.
+// One token of a sequence, or a short block, gives Hq / Hkv rows per token and
+// KV head, a handful against thousands of keys: the stream of codes bounds the
+// call, and a tcgen05 tile of 128 rows would be mostly padding.  A CTA of four
+// warps takes 16, 32 or 64 rows (MT 16-row tiles); its warps are MT row tiles by
+// 4 / MT groups of keys.  A fifth warp keeps a ring of K and V tiles of 128 keys
+// filled by TMA, codes as they lie, so that 128 KB per SM (two CTAs) are in flight
+// whatever the warps do; they turn codes into fp16 on the way from shared
+// memory to the MMA.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -14,7 +19,8 @@
 namespace bdlm {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                       // warps that compute; one more loads
+constexpr int kThreads = 32 * (kWarps + 1);
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -36,17 +42,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-// Codes: read once, kept out of L1.
-__device__ __forceinline__ uint4 ldg16_stream(const void* p) {
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 ldg8_stream(const void* p) {
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -60,6 +63,9 @@ __device__ __forceinline__ uint32_t rest_half2(uint32_t hi, float a, float b) {
 __device__ __forceinline__ uint32_t rest_bf16x2(uint32_t hi, float a, float b) {
   return pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
 }
+
+// Barrier of the computing warps.
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 // Online-softmax state of a warp's 16 x HD tile.  A thread (g = lane / 4,
 // t = lane % 4) holds rows g and g + 8; its O values are HD / 4 consecutive
@@ -112,36 +118,85 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
 }
 
 // MMA columns.  The contraction index of S = Q K^T may visit the head
-// dimension in any order that both operands share, and the columns of O may
-// stand for the head dimension in any order: a thread takes 16 consecutive
-// bytes of a key (16 codes) and uses them, word by word, as the fragments of
-// four k-steps (word i, bytes 0-1 and 2-3: the two halves of step 4 h + i of
-// 64-byte half h), so every load is 16 bytes wide and no operand is
-// transposed.  For P V, thread (g, t) takes codes HD/8 g .. + HD/8 - 1 of keys
-// 2 t, 2 t + 1, 2 t + 8, 2 t + 9 and pairs the codes of two keys by byte
-// permutes: column tile j of O is then element j of every thread's piece, and
-// O's fragment of thread t holds columns HD/4 t .. HD/4 (t + 1) - 1 in order.
+// dimension in any order that both operands share, keys may take any order
+// that S's columns and V's rows share, and the columns of O may stand for the
+// head dimension in any order.  So a thread takes 16 consecutive bytes of a key
+// (16 codes) and uses them, word by word, as the fragments of four k-steps
+// (word i, bytes 0-1 and 2-3: the two halves of step 4 h + i of 64-byte half h):
+// every load is 16 bytes wide and no operand is transposed.  For P V, thread
+// (g, t) takes HD / 8 codes of the keys at contraction indices 2 t, 2 t + 1,
+// 2 t + 8, 2 t + 9 and pairs the codes of two keys by byte permutes: column tile j
+// of O is element j of every thread's piece.  In the 128-byte swizzle of the
+// tiles (HD = 128) MMA column c is key perm(c) = c / 2 + 4 (c % 2) of its eight
+// and thread g's piece of V is chunk perm(g): the eight lanes of a load phase
+// then touch all 32 banks.  (HD = 64, 64-byte swizzle: perm is the identity.)
 //
 // P is rounded to fp16 (2^-11) for cached keys and bf16 for own ones, below a
 // bf16 output's own rounding.  FINE, for an fp32 output: P goes in two (three)
 // parts, each what the rounding of the one before left, so that O is off by
 // fp32 sums alone.
-template <int HD, bool FINE>
-__global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_small_kernel(const CachedParams p) {
-  constexpr int KH = HD / 64;  // 64-byte halves of a key's codes
-  constexpr int VW = HD / 32;  // words of a thread's piece of a value row
-  extern __shared__ __align__(16) float red[];
-  float(*red_o)[kSmallRows][HD + 4] = reinterpret_cast<float(*)[kSmallRows][HD + 4]>(red);
-  float(*red_ml)[kSmallRows][2] =
-      reinterpret_cast<float(*)[kSmallRows][2]>(red + kWarps * kSmallRows * (HD + 4));
+struct SInfo {  // of each 16 keys of a tile: K's scale, log2 and inverse of V's (1, 0, 1 without a page)
+  float s[8], lv[8], iv[8];
+  int gone;     // bit x: no page
+};
+
+template <int HD>
+struct LayS {
+  static constexpr int NS = HD == 128 ? 2 : 4;    // slots of K and of V
+  static constexpr int kTile = 128 * HD;
+  static constexpr int kK = 0, kV = NS * kTile;
+  static constexpr int kRed = 2 * NS * kTile;     // [kWarps][16][HD + 4] fp32
+  static constexpr int kML = kRed + kWarps * 16 * (HD + 4) * 4;  // [kWarps][16][2]
+  static constexpr int kInfo = kML + kWarps * 16 * 2 * 4;
+  static constexpr int kBar = (kInfo + NS * (int)sizeof(SInfo) + 15) & ~15;
+  static constexpr int kBytes = kBar + 4 * NS * 8 + 16;
+  static constexpr int kAlloc = kBytes + 1024;    // (aligned to 1024)
+};
+
+template <int HD, int MT, bool FINE>
+__global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
+    bdlm_cached_small_kernel(const __grid_constant__ CUtensorMap tK8, const __grid_constant__ CUtensorMap tV8,
+                             const CachedParams p) {
+  using LY = LayS<HD>;
+  constexpr int NS = LY::NS;
+  constexpr int KH = HD / 64;   // 64-byte halves of a key's codes
+  constexpr int VW = HD / 32;   // words of a thread's piece of a value row
+  constexpr int KG = kWarps / MT;         // key groups
+  constexpr int kStep = 128 / KG / 32;    // 32-key steps of a warp per tile
+  constexpr int kRows = 16 * MT;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* bp = smem_raw + (base - raw);
+  float(*red_o)[16][HD + 4] = reinterpret_cast<float(*)[16][HD + 4]>(bp + LY::kRed);
+  float(*red_ml)[16][2] = reinterpret_cast<float(*)[16][2]>(bp + LY::kML);
+  SInfo* infos = reinterpret_cast<SInfo*>(bp + LY::kInfo);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bp + LY::kBar + 4 * NS * 8);
+  auto KF = [&](uint32_t i) -> uint32_t { return base + LY::kBar + 8 * i; };
+  auto KE = [&](uint32_t i) -> uint32_t { return base + LY::kBar + 8 * (NS + i); };
+  auto VF = [&](uint32_t i) -> uint32_t { return base + LY::kBar + 8 * (2 * NS + i); };
+  auto VE = [&](uint32_t i) -> uint32_t { return base + LY::kBar + 8 * (3 * NS + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < NS; ++i) {
+      mbar_init(KF(i), 1);
+      mbar_init(VF(i), 1);
+      mbar_init(KE(i), kWarps);
+      mbar_init(VE(i), kWarps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  launch_dependents();
+  const Watchdog wd{p.status, p.limit_ns, abort_flag};
   uint32_t bad = 0;
   const CacheDesc& c = p.c;
+  // every warp walks the CTA's pieces on its own
   const int cta = blockIdx.x;
   int64_t u0 = 0, u1 = 0;
   UnitPos pos{0, 0, 0, 0};
   SegInfo seg;
-  launch_dependents();
   if (p.whole) {  // CTA per segment: (sequence, KV head, row tile), p.whole row tiles for each
     pos.rt = cta % p.whole;
     pos.h = cta / p.whole % c.Hkv;
@@ -158,138 +213,189 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
       seg = seg_info(c, p.r, p.sp, pos.s, bad);
     }
   }
-  {
-    for (int64_t u = u0; u < u1;) {
+
+  if (warp == kWarps) {
+    // -------------------------------------------------- loader
+    uint32_t slot = 0, ph = 1;
+    bool ok = true;
+    for (int64_t u = u0; ok && u < u1;) {
       int jb, je;
       split_units(seg, p.sp, pos, u, u1, jb, je);
       u += seg.span - pos.j;
-      if (je == 0) break;  // only the segment's opening lies here: the next CTA begins it
-      // ---- the tile's rows: fp16, each scaled by a power of two that puts
-      // its largest magnitude in [2^14, 2^15): exact down to 2^-28 of it
-      uint32_t q[KH * 4][4];
-      float cq[2];
-      int64_t qoff[2];
-      bool live[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int fr = pos.rt * kSmallRows + g + 8 * r, tok = fr / p.sp.group;
-        live[r] = tok < seg.v.rows;
-        const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
-        qoff[r] = ((seg.v.row0 + (live[r] ? tok : 0)) * p.Hq + head) * HD;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) + qoff[r];
-        uint32_t w[KH][8];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int h = 0; h < KH; ++h) {
-          const uint4 x = live[r] ? ldg16(src + 64 * h + 16 * t) : make_uint4(0, 0, 0, 0);
-          const uint4 y = live[r] ? ldg16(src + 64 * h + 16 * t + 8) : make_uint4(0, 0, 0, 0);
-          w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
-          w[h][4] = y.x; w[h][5] = y.y; w[h][6] = y.z; w[h][7] = y.w;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) amax = max(amax, max(w[h][i] & 0x7fffu, (w[h][i] >> 16) & 0x7fffu));
-        }
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int e = 14 + 127 - (int)(amax >> 7);  // bf16 exponent field
-        if (amax >= 0x7f80u || amax == 0) e = 0;
-        e = min(e, 126);
-        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-        cq[r] = p.sl2 * __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int h = 0; h < KH; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            q[4 * h + i][r] = pack_half2(bf_lo(w[h][2 * i]) * f, bf_hi(w[h][2 * i]) * f);
-            q[4 * h + i][2 + r] = pack_half2(bf_lo(w[h][2 * i + 1]) * f, bf_hi(w[h][2 * i + 1]) * f);
+      if (je == 0) break;
+      const int len = seg.v.len, n = min(je, seg.ktiles) - jb, h = pos.h;
+      const int32_t* table = c.table + (int64_t)pos.s * c.max_pages;
+      // lane 8 a + x: page and scales of keys 16 x of tile a of a batch of 4 tiles, one batch ahead
+      auto lookup = [&](int b) {
+        const int tile = 4 * b + (lane >> 3), key = (jb + tile) * kUnit + 16 * (lane & 7);
+        if (tile >= n || key >= len) return -1;
+        const int id = __ldg(table + (key >> c.lp));
+        if (id >= 0 && id < c.n_pages) return id;
+        bad |= kStatusBadPage;
+        return -1;
+      };
+      auto scale_of = [&](const float* sc, int id) { return id >= 0 ? __ldg(sc + (int64_t)id * c.Hkv + h) : 1.f; };
+      int id = lookup(0), id1 = lookup(1);
+      float sk = scale_of(c.ks, id), sv = scale_of(c.vs, id);
+      for (int b = 0; ok && 4 * b < n; ++b) {
+        const float sk1 = scale_of(c.ks, id1), sv1 = scale_of(c.vs, id1);
+        const int id2 = lookup(b + 2);
+        for (int a = 0; a < 4 && 4 * b + a < n; ++a) {
+          ok = mbar_wait(KE(slot), ph, wd, 70);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int x = lane & 7;
+          const int cid = __shfl_sync(0xffffffffu, id, 8 * a + x);
+          const float ck = __shfl_sync(0xffffffffu, sk, 8 * a + x), cv = __shfl_sync(0xffffffffu, sv, 8 * a + x);
+          const unsigned none = __ballot_sync(0xffffffffu, cid < 0) & 0xffu;
+          SInfo& si = infos[slot];
+          if (lane < 8) {
+            si.s[x] = ck;
+            si.lv[x] = log2f(cv);
+            si.iv[x] = 1.f / cv;
           }
-      }
-      State<HD> st;
-#pragma unroll
-      for (int j = 0; j < HD / 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[j][i] = 0.f;
-      st.m[0] = st.m[1] = -INFINITY;
-      st.l[0] = st.l[1] = 0.f;
-
-      // ---- cached keys: this warp's 32 of every unit of 128
-      const int kc = min(je, seg.ktiles);
-      uint4 kw[4][KH];
-      uint32_t vw[2][4][VW];
-      int pid[2] = {-1, -1}, npid[2] = {-1, -1};
-      auto pages = [&](int j, int (&id)[2]) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = j * kUnit + warp * 32 + 16 * x;
-          id[x] = j < kc && key < seg.v.len ? page_id(c, pos.s, key >> c.lp, bad) : -1;
+          if (lane == 0) si.gone = (int)none;
+          const int per = kUnit >> c.lp, step = c.page >> 4;
+          int cnt = 0;
+          for (int q = 0; q < per; ++q) cnt += !((none >> (q * step)) & 1u);
+          __syncwarp();
+          const int pid = __shfl_sync(0xffffffffu, cid, (lane * step) & 7);
+          const int blk = (int)((int64_t)pid * c.Hkv + h);
+          const bool mine = lane < per && pid >= 0;
+          if (lane == 0) {
+            if (cnt) mbar_arrive_expect_tx(KF(slot), (uint32_t)(cnt * c.page * HD));
+            else mbar_arrive(KF(slot));
+          }
+          __syncwarp();
+          if (mine) tma_load_3d(base + LY::kK + slot * LY::kTile + lane * c.page * HD, &tK8, KF(slot), 0, 0, blk);
+          ok = mbar_wait(VE(slot), ph, wd, 71);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            if (cnt) mbar_arrive_expect_tx(VF(slot), (uint32_t)(cnt * c.page * HD));
+            else mbar_arrive(VF(slot));
+          }
+          __syncwarp();
+          if (mine) tma_load_3d(base + LY::kV + slot * LY::kTile + lane * c.page * HD, &tV8, VF(slot), 0, 0, blk);
+          if (++slot == NS) slot = 0, ph ^= 1;
         }
-      };
-      auto row_at = [&](int64_t page, int key) -> int64_t {
-        return ((page * c.Hkv + pos.h) * c.page + (key & (c.page - 1))) * HD;
-      };
-      auto load_k = [&](int j, const int (&id)[2]) {
+        id = id1; id1 = id2; sk = sk1; sv = sv1;
+      }
+      if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
+    }
+    if (bad) atomicOr(p.status, bad);
+    // (copies that a timeout left in flight land before the CTA's shared memory is given up)
+    if (*abort_flag) drain_after_abort(200);
+    return;
+  }
+
+  // ---------------------------------------------------- the computing warps
+  // After a timeout (ok false) they go on without waiting, so that all of them
+  // meet at the same barriers; the call reports the timeout.
+  const int mt = warp / KG, kg = warp % KG;
+  auto perm = [](int x) { return HD == 128 ? (x >> 1) | ((x & 1) << 2) : x; };
+  uint32_t slot = 0, ph = 0;
+  bool ok = true;
+  for (int64_t u = u0; u < u1;) {
+    int jb, je;
+    split_units(seg, p.sp, pos, u, u1, jb, je);
+    u += seg.span - pos.j;
+    if (je == 0) break;  // only the segment's opening lies here: the next CTA begins it
+    // ---- the warp's rows: fp16, each scaled by a power of two that puts its
+    // largest magnitude in [2^14, 2^15): exact down to 2^-28 of it
+    uint32_t q[KH * 4][4];
+    float cq[2];
+    int64_t qoff[2];
+    bool live[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int fr = pos.rt * kRows + 16 * mt + g + 8 * r, tok = fr / p.sp.group;
+      live[r] = tok < seg.v.rows;
+      const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
+      qoff[r] = ((seg.v.row0 + (live[r] ? tok : 0)) * p.Hq + head) * HD;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) + qoff[r];
+      uint32_t w[KH][8];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int h = 0; h < KH; ++h) {
+        const uint4 x = live[r] ? ldg16(src + 64 * h + 16 * t) : make_uint4(0, 0, 0, 0);
+        const uint4 y = live[r] ? ldg16(src + 64 * h + 16 * t + 8) : make_uint4(0, 0, 0, 0);
+        w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
+        w[h][4] = y.x; w[h][5] = y.y; w[h][6] = y.z; w[h][7] = y.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max(amax, max(w[h][i] & 0x7fffu, (w[h][i] >> 16) & 0x7fffu));
+      }
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      int e = 14 + 127 - (int)(amax >> 7);  // bf16 exponent field
+      if (amax >= 0x7f80u || amax == 0) e = 0;
+      e = min(e, 126);
+      const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+      cq[r] = p.sl2 * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int h = 0; h < KH; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = j * kUnit + warp * 32 + 8 * i + g;
-          const bool ok = id[i >> 1] >= 0 && key < seg.v.len;
-          const uint8_t* src = c.k8 + (ok ? row_at(id[i >> 1], key) + 16 * t : 0);
-#pragma unroll
-          for (int h = 0; h < KH; ++h) kw[i][h] = ok ? ldg16_stream(src + 64 * h) : make_uint4(0, 0, 0, 0);
+          q[4 * h + i][r] = pack_half2(bf_lo(w[h][2 * i]) * f, bf_hi(w[h][2 * i]) * f);
+          q[4 * h + i][2 + r] = pack_half2(bf_lo(w[h][2 * i + 1]) * f, bf_hi(w[h][2 * i + 1]) * f);
         }
-      };
-      auto load_v = [&](int j, const int (&id)[2]) {
+    }
+    State<HD> st;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+    for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = j * kUnit + warp * 32 + 16 * x + 2 * t + (i & 1) + 8 * (i >> 1);
-            const bool ok = id[x] >= 0 && key < seg.v.len;
-            const uint8_t* src = c.v8 + (ok ? row_at(id[x], key) + (HD / 8) * g : 0);
-            if (HD == 128) {
-              const uint4 v = ok ? ldg16_stream(src) : make_uint4(0, 0, 0, 0);
-              vw[x][i][0] = v.x; vw[x][i][1] = v.y; vw[x][i][VW - 2] = v.z; vw[x][i][VW - 1] = v.w;
-            } else {
-              const uint2 v = ok ? ldg8_stream(src) : make_uint2(0, 0);
-              vw[x][i][0] = v.x; vw[x][i][1] = v.y;
-            }
-          }
-      };
-      if (jb < kc) {
-        pages(jb, pid);
-        load_k(jb, pid);
-        load_v(jb, pid);
-      }
-      for (int j = jb; j < kc; ++j) {
-        pages(j + 1, npid);
+      for (int i = 0; i < 4; ++i) st.o[j][i] = 0.f;
+    st.m[0] = st.m[1] = -INFINITY;
+    st.l[0] = st.l[1] = 0.f;
+
+    // ---- cached keys
+    const int kc = min(je, seg.ktiles);
+    for (int j = jb; j < kc; ++j) {
+      const int left = seg.v.len - j * kUnit;  // keys of the tile
+      if (ok) ok = mbar_wait(KF(slot), ph, wd, 72);
+      const SInfo& si = infos[slot];
+      const int gone = si.gone;
+      const bool full = left >= kUnit && gone == 0;
+#pragma unroll 1
+      for (int step = 0; step < kStep; ++step) {
+        const int kb = (kg * kStep + step) * 32;  // first key of the step in the tile
         float s[4][4];
+        const uint32_t sk = base + LY::kK + slot * LY::kTile;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+          const int row = kb + 8 * i + perm(g);
 #pragma unroll
           for (int h = 0; h < KH; ++h) {
-            const uint32_t w[4] = {kw[i][h].x, kw[i][h].y, kw[i][h].z, kw[i][h].w};
+            const uint4 k4 = lds16(sk + (HD == 128 ? row * 128 + (((4 * h + t) ^ (row & 7)) << 4)
+                                                   : row * 64 + ((t ^ ((row >> 1) & 3)) << 4)));
+            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_f16(s[i], q[4 * h + k][0], q[4 * h + k][1], q[4 * h + k][2], q[4 * h + k][3],
                       e4m3x2_to_half2(w[k]), e4m3x2_to_half2(w[k] >> 16));
           }
         }
-        load_k(j + 1, npid);  // (ids of -1 past the end: nothing is read)
         float iv[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int64_t b = (int64_t)max(pid[x], 0) * c.Hkv + pos.h;
-          const float ks = pid[x] >= 0 ? __ldg(c.ks + b) : 0.f;
-          const float vs = pid[x] >= 0 ? __ldg(c.vs + b) : 1.f;
-          const float lv = log2f(vs);
-          iv[x] = 1.f / vs;
-          const int key = j * kUnit + warp * 32 + 16 * x + 2 * t;
+          const int b = (kb >> 4) + x;
+          const float ks = si.s[b], lv = si.lv[b];
+          iv[x] = si.iv[b];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool ok = pid[x] >= 0 && key + 8 * i + (e & 1) < seg.v.len;
-              s[2 * x + i][e] = ok ? fmaf(s[2 * x + i][e], cq[e >> 1] * ks, lv) : -INFINITY;
-            }
+            for (int e = 0; e < 4; ++e) s[2 * x + i][e] = fmaf(s[2 * x + i][e], cq[e >> 1] * ks, lv);
+          if (!full)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (kb + 16 * x + 8 * i + perm(2 * t + (e & 1)) >= left || ((gone >> b) & 1)) s[2 * x + i][e] = -INFINITY;
+        }
+        if (step == kStep - 1) {  // K's slot and its info are read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(KE(slot));
         }
         softmax_step<HD, 4>(st, s, iv);
         uint32_t pa[2][4], pr[2][4];
@@ -301,14 +407,32 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
             pa[x][i] = pack_half2(a, b);
             if (FINE) pr[x][i] = rest_half2(pa[x][i], a, b);
           }
+        if (step == 0 && ok) ok = mbar_wait(VF(slot), ph, wd, 73);
+        const uint32_t sv = base + LY::kV + slot * LY::kTile;
 #pragma unroll
-        for (int w = 0; w < VW; ++w)
+        for (int x = 0; x < 2; ++x) {
+          uint32_t vw[4][VW];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {  // bytes 2 hf, 2 hf + 1 of word w: column tiles 4 w + 2 hf, + 1
+          for (int i = 0; i < 4; ++i) {
+            const int row = kb + 16 * x + 8 * (i >> 1) + perm(2 * t + (i & 1));
+            if (HD == 128) {
+              const uint4 v = lds16(sv + row * 128 + ((perm(g) ^ (row & 7)) << 4));
+              vw[i][0] = v.x; vw[i][1] = v.y; vw[i][VW - 2] = v.z; vw[i][VW - 1] = v.w;
+            } else {
+              const uint2 v = lds8(sv + row * 64 + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+              vw[i][0] = v.x; vw[i][1] = v.y;
+            }
+            if (!full && (row >= left || ((gone >> (row >> 4)) & 1))) {  // stale codes
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t lo = __byte_perm(vw[x][0][w], vw[x][1][w], hf ? 0x7362 : 0x5140);
-              const uint32_t hi = __byte_perm(vw[x][2][w], vw[x][3][w], hf ? 0x7362 : 0x5140);
+              for (int w = 0; w < VW; ++w) vw[i][w] = 0;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {  // bytes 2 hf, 2 hf + 1 of word w: column tiles 4 w + 2 hf, + 1
+              const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140);
+              const uint32_t hi = __byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140);
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const uint32_t b0 = e4m3x2_to_half2(lo >> (16 * y)), b1 = e4m3x2_to_half2(hi >> (16 * y));
@@ -316,158 +440,158 @@ __global__ void __launch_bounds__(32 * kWarps, kSmallCtasPerSm) bdlm_cached_smal
                 if (FINE) mma_f16(st.o[4 * w + 2 * hf + y], pr[x][0], pr[x][1], pr[x][2], pr[x][3], b0, b1);
               }
             }
-          }
-        load_v(j + 1, npid);
-        pid[0] = npid[0];
-        pid[1] = npid[1];
-      }
-
-      // ---- the rows' own block (bf16), in groups of 16 keys
-      if (p.sp.local) {
-        int k0 = 0, k1 = 0;  // own keys of this piece
-        if (seg.ltiles == 0) {
-          if (je == seg.units) k1 = seg.v.rows;
-        } else {
-          k0 = max(jb - seg.ktiles, 0) * kUnit;
-          k1 = min(max(je - seg.ktiles, 0) * kUnit, seg.v.rows);
         }
-        for (int key0 = k0 + 16 * warp; key0 < k1; key0 += 16 * kWarps) {
-          float s[2][4];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(VE(slot));
+      if (++slot == NS) slot = 0, ph ^= 1;
+    }
+
+    // ---- the rows' own block (bf16), in groups of 16 keys
+    if (p.sp.local) {
+      int k0 = 0, k1 = 0;  // own keys of this piece
+      if (seg.ltiles == 0) {
+        if (je == seg.units) k1 = seg.v.rows;
+      } else {
+        k0 = max(jb - seg.ktiles, 0) * kUnit;
+        k1 = min(max(je - seg.ktiles, 0) * kUnit, seg.v.rows);
+      }
+      for (int key0 = k0 + 16 * kg; key0 < k1; key0 += 16 * KG) {
+        float s[2][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
-          for (int h = 0; h < HD / 32; ++h) {
-            uint4 a[2], b[2];
+        for (int h = 0; h < HD / 32; ++h) {
+          uint4 a[2], b[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              a[r] = live[r] ? ldg16(static_cast<const __nv_bfloat16*>(p.Q) + qoff[r] + 32 * h + 8 * t)
-                             : make_uint4(0, 0, 0, 0);
+          for (int r = 0; r < 2; ++r)
+            a[r] = live[r] ? ldg16(static_cast<const __nv_bfloat16*>(p.Q) + qoff[r] + 32 * h + 8 * t)
+                           : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int key = key0 + 8 * i + g;
-              b[i] = key < seg.v.rows
-                         ? ldg16(static_cast<const __nv_bfloat16*>(p.K) +
-                                 ((seg.v.row0 + key) * c.Hkv + pos.h) * HD + 32 * h + 8 * t)
-                         : make_uint4(0, 0, 0, 0);
-              mma_bf16(s[i], a[0].x, a[1].x, a[0].y, a[1].y, b[i].x, b[i].y);
-              mma_bf16(s[i], a[0].z, a[1].z, a[0].w, a[1].w, b[i].z, b[i].w);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const int key = key0 + 8 * i + g;
+            b[i] = key < seg.v.rows
+                       ? ldg16(static_cast<const __nv_bfloat16*>(p.K) +
+                               ((seg.v.row0 + key) * c.Hkv + pos.h) * HD + 32 * h + 8 * t)
+                       : make_uint4(0, 0, 0, 0);
+            mma_bf16(s[i], a[0].x, a[1].x, a[0].y, a[1].y, b[i].x, b[i].y);
+            mma_bf16(s[i], a[0].z, a[1].z, a[0].w, a[1].w, b[i].z, b[i].w);
           }
+        }
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[i][e] = key0 + 8 * i + 2 * t + (e & 1) < seg.v.rows ? s[i][e] * p.sl2 : -INFINITY;
-          const float one[1] = {1.f};
-          softmax_step<HD, 2>(st, s, one);
-          uint32_t pa[4], pr[4], pq[4];
+          for (int e = 0; e < 4; ++e)
+            s[i][e] = key0 + 8 * i + 2 * t + (e & 1) < seg.v.rows ? s[i][e] * p.sl2 : -INFINITY;
+        const float one[1] = {1.f};
+        softmax_step<HD, 2>(st, s, one);
+        uint32_t pa[4], pr[4], pq[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = s[i >> 1][2 * (i & 1)], b = s[i >> 1][2 * (i & 1) + 1];
+          pa[i] = pack_bf16x2(a, b);
+          if (FINE) {
+            pr[i] = rest_bf16x2(pa[i], a, b);
+            pq[i] = rest_bf16x2(pr[i], a - bf_lo(pa[i]), b - bf_hi(pa[i]));
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < HD / 64; ++w) {  // 8 columns of the thread's HD / 8 (16 bytes) at a time
+          uint4 v[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float a = s[i >> 1][2 * (i & 1)], b = s[i >> 1][2 * (i & 1) + 1];
-            pa[i] = pack_bf16x2(a, b);
-            if (FINE) {
-              pr[i] = rest_bf16x2(pa[i], a, b);
-              pq[i] = rest_bf16x2(pr[i], a - bf_lo(pa[i]), b - bf_hi(pa[i]));
-            }
+            const int key = key0 + 2 * t + (i & 1) + 8 * (i >> 1);
+            v[i] = key < seg.v.rows
+                       ? ldg16(static_cast<const __nv_bfloat16*>(p.V) +
+                               ((seg.v.row0 + key) * c.Hkv + pos.h) * HD + (HD / 8) * perm(g) + 8 * w)
+                       : make_uint4(0, 0, 0, 0);
           }
+          const uint32_t x0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, x1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+          const uint32_t y0[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, y1[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
-          for (int w = 0; w < HD / 64; ++w) {  // 8 columns of the thread's HD / 8 (16 bytes) at a time
-            uint4 v[4];
+          for (int k = 0; k < 4; ++k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = key0 + 2 * t + (i & 1) + 8 * (i >> 1);
-              v[i] = key < seg.v.rows
-                         ? ldg16(static_cast<const __nv_bfloat16*>(p.V) +
-                                 ((seg.v.row0 + key) * c.Hkv + pos.h) * HD + (HD / 8) * g + 8 * w)
-                         : make_uint4(0, 0, 0, 0);
-            }
-            const uint32_t x0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, x1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-            const uint32_t y0[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, y1[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t sel = y ? 0x7632 : 0x5410;
-                const uint32_t b0 = __byte_perm(x0[k], x1[k], sel), b1 = __byte_perm(y0[k], y1[k], sel);
-                mma_bf16(st.o[8 * w + 2 * k + y], pa[0], pa[1], pa[2], pa[3], b0, b1);
-                if (FINE) {
-                  mma_bf16(st.o[8 * w + 2 * k + y], pr[0], pr[1], pr[2], pr[3], b0, b1);
-                  mma_bf16(st.o[8 * w + 2 * k + y], pq[0], pq[1], pq[2], pq[3], b0, b1);
-                }
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t sel = y ? 0x7632 : 0x5410;
+              const uint32_t b0 = __byte_perm(x0[k], x1[k], sel), b1 = __byte_perm(y0[k], y1[k], sel);
+              mma_bf16(st.o[8 * w + 2 * k + y], pa[0], pa[1], pa[2], pa[3], b0, b1);
+              if (FINE) {
+                mma_bf16(st.o[8 * w + 2 * k + y], pr[0], pr[1], pr[2], pr[3], b0, b1);
+                mma_bf16(st.o[8 * w + 2 * k + y], pq[0], pq[1], pq[2], pq[3], b0, b1);
               }
             }
           }
         }
       }
+    }
 
-      // ---- the four warps' states joined through shared memory
+    // ---- the warps' states through shared memory, a row tile's key groups joined
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float l = st.l[r];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (t == 0) {
-          red_ml[warp][g + 8 * r][0] = st.m[r];
-          red_ml[warp][g + 8 * r][1] = l;
-        }
-        // tile j, element e: column (HD / 4) t + (HD / 8) e + j
-        float* o = &red_o[warp][g + 8 * r][(HD / 4) * t];
+    for (int r = 0; r < 2; ++r) {
+      float l = st.l[r];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (t == 0) {
+        red_ml[warp][g + 8 * r][0] = st.m[r];
+        red_ml[warp][g + 8 * r][1] = l;
+      }
+      // tile j, element e: column HD / 8 perm(2 t + e) + j
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* o = &red_o[warp][g + 8 * r][(HD / 8) * perm(2 * t + e)];
 #pragma unroll
         for (int j = 0; j < HD / 8; j += 4)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float4*>(o + (HD / 8) * e + j) =
-                make_float4(st.o[j][2 * r + e], st.o[j + 1][2 * r + e], st.o[j + 2][2 * r + e], st.o[j + 3][2 * r + e]);
+          *reinterpret_cast<float4*>(o + j) =
+              make_float4(st.o[j][2 * r + e], st.o[j + 1][2 * r + e], st.o[j + 2][2 * r + e], st.o[j + 3][2 * r + e]);
       }
-      __syncthreads();
-      {
-        const int row = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * 4;
-        float M = -INFINITY, w[kWarps], L = 0.f;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) M = fmaxf(M, red_ml[x][row][0]);
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-          w[x] = M == -INFINITY ? 0.f : ex2_approx(red_ml[x][row][0] - M);
-          L = fmaf(w[x], red_ml[x][row][1], L);
-        }
-        const int fr = pos.rt * kSmallRows + row, tok = fr / p.sp.group;
-        const bool whole = jb == 0 && je == seg.units;
-        float* slot = p.part + (2 * (int64_t)cta + (jb == 0 ? 1 : 0)) * part_floats(kSmallRows, HD);
-        if (tok < seg.v.rows) {
-          const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
-          const int64_t o0 = ((seg.v.row0 + tok) * p.Hq + head) * HD;
-          const float inv = whole ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
-#pragma unroll
-          for (int k = 0; k < HD / 32; ++k) {
-            const int col = c0 + 32 * k;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int x = 0; x < kWarps; ++x) {
-              const float4 b = *reinterpret_cast<const float4*>(&red_o[x][row][col]);
-              a.x = fmaf(w[x], b.x, a.x); a.y = fmaf(w[x], b.y, a.y);
-              a.z = fmaf(w[x], b.z, a.z); a.w = fmaf(w[x], b.w, a.w);
-            }
-            a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
-            if (!whole) reinterpret_cast<float4*>(slot)[(col >> 2) * kSmallRows + row] = a;
-            else if (p.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o0 + col) = a;
-            else
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + o0 + col) =
-                  make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-          }
-          if ((threadIdx.x & 7) == 0) {
-            if (whole) p.LSE[(int64_t)head * p.r.T + seg.v.row0 + tok] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-            else {
-              slot[kSmallRows * HD + row] = M;
-              slot[kSmallRows * HD + kSmallRows + row] = L;
-            }
-          }
-        }
-      }
-      __syncthreads();
-      if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
     }
+    compute_sync();
+    const bool whole = jb == 0 && je == seg.units;
+    float* part = p.part + (2 * (int64_t)cta + (jb == 0 ? 1 : 0)) * part_floats(kRows, HD);
+#pragma unroll 1
+    for (int item = threadIdx.x; item < kRows * 8; item += 32 * kWarps) {
+      const int row = item >> 3, c0 = (item & 7) * 4, w0 = (row >> 4) * KG, r = row & 15;
+      float M = -INFINITY, w[KG], L = 0.f;
+#pragma unroll
+      for (int x = 0; x < KG; ++x) M = fmaxf(M, red_ml[w0 + x][r][0]);
+#pragma unroll
+      for (int x = 0; x < KG; ++x) {
+        w[x] = M == -INFINITY ? 0.f : ex2_approx(red_ml[w0 + x][r][0] - M);
+        L = fmaf(w[x], red_ml[w0 + x][r][1], L);
+      }
+      const int fr = pos.rt * kRows + row, tok = fr / p.sp.group;
+      if (tok >= seg.v.rows) continue;
+      const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
+      const int64_t o0 = ((seg.v.row0 + tok) * p.Hq + head) * HD;
+      const float inv = whole ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
+#pragma unroll
+      for (int k = 0; k < HD / 32; ++k) {
+        const int col = c0 + 32 * k;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < KG; ++x) {
+          const float4 b = *reinterpret_cast<const float4*>(&red_o[w0 + x][r][col]);
+          a.x = fmaf(w[x], b.x, a.x); a.y = fmaf(w[x], b.y, a.y);
+          a.z = fmaf(w[x], b.z, a.z); a.w = fmaf(w[x], b.w, a.w);
+        }
+        a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
+        if (!whole) reinterpret_cast<float4*>(part)[(col >> 2) * kRows + row] = a;
+        else if (p.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o0 + col) = a;
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + o0 + col) =
+              make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+      }
+      if ((item & 7) == 0) {
+        if (whole) p.LSE[(int64_t)head * p.r.T + seg.v.row0 + tok] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+        else {
+          part[kRows * HD + row] = M;
+          part[kRows * HD + kRows + row] = L;
+        }
+      }
+    }
+    compute_sync();
+    if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
   }
-  if (bad) atomicOr(p.status, bad);
 }
 
 // Joins the partial results of the segments that span CTAs.  Block c takes
@@ -557,14 +681,27 @@ __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const 
 
 }  // namespace
 
-cudaError_t launch_cached_small(const CachedParams& p, cudaStream_t st, int* launches) {
-  // (at most 34.3 KB: within the default limit)
-  const int bytes = (kWarps * kSmallRows * (p.c.d + 4) + kWarps * kSmallRows * 2) * (int)sizeof(float);
-  auto k = p.c.d == 128 ? (p.o_f32 ? bdlm_cached_small_kernel<128, true> : bdlm_cached_small_kernel<128, false>)
-                        : (p.o_f32 ? bdlm_cached_small_kernel<64, true> : bdlm_cached_small_kernel<64, false>);
-  k<<<p.G, 32 * kWarps, bytes, st>>>(p);
-  ++*launches;
+template <int HD, int MT, bool FINE>
+static cudaError_t launch(const CachedMaps& m, const CachedParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  const cudaError_t e = raise_smem(reinterpret_cast<const void*>(bdlm_cached_small_kernel<HD, MT, FINE>),
+                                   LayS<HD>::kAlloc, raised);
+  if (e != cudaSuccess) return e;
+  bdlm_cached_small_kernel<HD, MT, FINE><<<p.G, kThreads, LayS<HD>::kAlloc, st>>>(m.k8, m.v8, p);
   return cudaGetLastError();
+}
+template <int HD, bool FINE>
+static cudaError_t launch_mt(const CachedMaps& m, const CachedParams& p, cudaStream_t st) {
+  return p.sp.tile_rows == 16   ? launch<HD, 1, FINE>(m, p, st)
+         : p.sp.tile_rows == 32 ? launch<HD, 2, FINE>(m, p, st)
+                                : launch<HD, 4, FINE>(m, p, st);
+}
+
+cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches) {
+  const cudaError_t e = p.c.d == 128 ? (p.o_f32 ? launch_mt<128, true>(m, p, st) : launch_mt<128, false>(m, p, st))
+                                     : (p.o_f32 ? launch_mt<64, true>(m, p, st) : launch_mt<64, false>(m, p, st));
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches) {

@@ -30,13 +30,13 @@ struct CachedParams {
 // side by side), then the rows' reference maxima (log2 units) and sums.
 __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (int64_t)tile_rows * (d + 2); }
 
-constexpr int kSmallRows = 64;      // rows up to which the mma.sync kernel takes a call
+constexpr int kSmallRows = 32;      // rows up to which the mma.sync kernel takes a call
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
 
 // Row tile of a call whose sequences have at most `flat` rows times heads of
-// a group: 16, 32 or 64 (mma.sync), 128 or 256 (tcgen05, split and pairs).
+// a group: 16 or 32 (mma.sync), 128 or 256 (tcgen05, split and pairs).
 inline int cached_tile_rows(int64_t flat) {
-  return flat <= 16 ? 16 : flat <= 32 ? 32 : flat <= kSmallRows ? 64 : flat <= 128 ? 128 : 256;
+  return flat <= 16 ? 16 : flat <= kSmallRows ? 32 : flat <= 128 ? 128 : 256;
 }
 inline int cached_ctas(int tile_rows, int sms) { return tile_rows <= kSmallRows ? sms * kSmallCtasPerSm : sms; }
 

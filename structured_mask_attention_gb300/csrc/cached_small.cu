@@ -145,7 +145,7 @@ struct LayS {
   static constexpr int NS = HD == 128 ? 2 : 4;    // slots of K and of V
   static constexpr int kTile = 128 * HD;
   static constexpr int kK = 0, kV = NS * kTile;
-  static constexpr int kRed = 2 * NS * kTile;     // [kWarps][16][HD + 4] fp32
+  static constexpr int kRed = 2 * NS * kTile;     // [kWarps][16][HD + 4] fp32; before, each warp's Q fragments
   static constexpr int kML = kRed + kWarps * 16 * (HD + 4) * 4;  // [kWarps][16][2]
   static constexpr int kInfo = kML + kWarps * 16 * 2 * 4;
   static constexpr int kBar = (kInfo + NS * (int)sizeof(SInfo) + 15) & ~15;
@@ -303,10 +303,13 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
     if (je == 0) break;  // only the segment's opening lies here: the next CTA begins it
     // ---- the warp's rows: fp16, each scaled by a power of two that puts its
     // largest magnitude in [2^14, 2^15): exact down to 2^-28 of it
-    uint32_t q[KH * 4][4];
+    // (their fragments stay in the warp's part of the reduction buffer: registers
+    // go to the keys in flight)
+    const uint32_t qs = base + LY::kRed + warp * (16 * (HD + 4) * 4) + lane * 16;
     float cq[2];
     int64_t qoff[2];
     bool live[2];
+    uint32_t q[KH * 4][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int fr = pos.rt * kRows + 16 * mt + g + 8 * r, tok = fr / p.sp.group;
@@ -340,6 +343,9 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           q[4 * h + i][2 + r] = pack_half2(bf_lo(w[h][2 * i + 1]) * f, bf_hi(w[h][2 * i + 1]) * f);
         }
     }
+#pragma unroll
+    for (int k = 0; k < KH * 4; ++k) st_shared_v4(qs + k * 512, q[k][0], q[k][1], q[k][2], q[k][3]);
+    __syncwarp();
     State<HD> st;
 #pragma unroll
     for (int j = 0; j < HD / 8; ++j)
@@ -362,18 +368,23 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
         float s[4][4];
         const uint32_t sk = base + LY::kK + slot * LY::kTile;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-          const int row = kb + 8 * i + perm(g);
+        for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
-          for (int h = 0; h < KH; ++h) {
+        for (int h = 0; h < KH; ++h) {
+          uint32_t w[4][4];  // four columns' halves; their sums advance side by side
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = kb + 8 * i + perm(g);
             const uint4 k4 = lds16(sk + (HD == 128 ? row * 128 + (((4 * h + t) ^ (row & 7)) << 4)
                                                    : row * 64 + ((t ^ ((row >> 1) & 3)) << 4)));
-            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+            w[i][0] = k4.x; w[i][1] = k4.y; w[i][2] = k4.z; w[i][3] = k4.w;
+          }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16(s[i], q[4 * h + k][0], q[4 * h + k][1], q[4 * h + k][2], q[4 * h + k][3],
-                      e4m3x2_to_half2(w[k]), e4m3x2_to_half2(w[k] >> 16));
+          for (int k = 0; k < 4; ++k) {
+            const uint4 a = lds16(qs + (4 * h + k) * 512);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f16(s[i], a.x, a.y, a.z, a.w, e4m3x2_to_half2(w[i][k]), e4m3x2_to_half2(w[i][k] >> 16));
           }
         }
         float iv[2];
@@ -692,9 +703,7 @@ static cudaError_t launch(const CachedMaps& m, const CachedParams& p, cudaStream
 }
 template <int HD, bool FINE>
 static cudaError_t launch_mt(const CachedMaps& m, const CachedParams& p, cudaStream_t st) {
-  return p.sp.tile_rows == 16   ? launch<HD, 1, FINE>(m, p, st)
-         : p.sp.tile_rows == 32 ? launch<HD, 2, FINE>(m, p, st)
-                                : launch<HD, 4, FINE>(m, p, st);
+  return p.sp.tile_rows == 16 ? launch<HD, 1, FINE>(m, p, st) : launch<HD, 2, FINE>(m, p, st);
 }
 
 cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches) {

@@ -535,9 +535,44 @@ __global__ void __launch_bounds__(kThreads, 1)
               return true;
             };
             ok = start_s(0) && (n < 2 || start_s(1));
-            for (int j = 0; ok && j < n; ++j, ++wc) {
+            int j = 0;
+            // (as in pairs, below: while the tile after next is a cached one)
+            const bool opened = !FINE && nk > 3;
+            if (opened) {
+              ok = ok && mbar_wait(BAR(B_OE + 0), oph & 1, wd, 32) && mbar_wait(BAR(B_OE + 1), (oph >> 1) & 1, wd, 32);
+              oph ^= 3;
+              auto lean = [&](auto sub) {
+                constexpr int t = decltype(sub)::value;
+                const uint32_t acc = j > 0, vs = wc & 1, vt = desc_lo(base + LY::kW + vs * LY::kWBytes, kSlot);
+                const uint32_t kt = desc_lo(base + LY::kK + ks * kSlot, 16), q = desc_lo(base + LY::kQ, 16);
+                constexpr uint32_t HV = desc_hi(2, 1024), HQ = desc_hi(SWQ, SBO8);
+                constexpr int n8 = HD / 32;
+                if (!(mbar_wait(BAR(B_WF + vs), (wc >> 1) & 1, wd, 33) && mbar_wait(BAR(B_KF + ks), kph, wd, 30) &&
+                      mbar_wait(BAR(B_PF + t), bit(pph, t), wd, 31)))
+                  return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+                tc_commit(BAR(B_WE + vs));
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk)
+                  mma_ss<true>(tmem + t * 128, q + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ, kt + (kk % n8) * 2, HQ, kId8,
+                               kk > 0);
+                tc_commit(BAR(B_SF + t));
+                tc_commit(BAR(B_KE + ks));
+                if (++ks == NK) ks = 0, kph ^= 1;
+                ++wc;
+                return true;
+              };
+              for (; ok && j + 3 < nk; j += 2) {
+                ok = lean(std::integral_constant<int, 0>{}) && lean(std::integral_constant<int, 1>{});
+                pph ^= 3;
+              }
+            }
+            for (; ok && j < n; ++j, ++wc) {
               const int t = j & 1;
-              ok = issue_pv(t, wc, own(j), j < 2, j < 2);
+              ok = issue_pv(t, wc, own(j), j < 2, j < 2 && !opened);
               if (!ok) break;
               tc_commit(BAR(B_WE + (wc & 1)));
               if (j + 2 >= n) tc_commit(BAR(B_OD + t));

@@ -215,6 +215,66 @@ __device__ __forceinline__ UnitPos locate_unit(const CacheDesc& c, const RowsDes
 // CTAs that take part: no more than there are units, so that none is empty.
 __device__ __forceinline__ int split_ctas(int64_t U, int G) { return U < G ? (int)U : G; }
 __device__ __forceinline__ int64_t split_begin(int64_t U, int G, int c) { return U * c / G; }
+// What CTA `cta` of G takes: list positions [u0, u1) and the first's segment
+// (u0 = u1: nothing).  By a whole warp.  Up to 32 sequences are looked at once.
+struct SplitOpen {
+  int64_t u0, u1;
+  UnitPos pos;
+  SegInfo seg;
+};
+__device__ __forceinline__ SplitOpen split_open(const CacheDesc& c, const RowsDesc& r, const AttnSplit& a, int G, int cta,
+                                                uint32_t& bad) {
+  SplitOpen o;
+  o.u0 = o.u1 = 0;
+  o.pos = UnitPos{0, 0, 0, 0};
+  o.seg = SegInfo{};
+  if (c.n_seqs > 32) {
+    const int64_t U = total_units(c, r, a, bad);
+    G = split_ctas(U, G);
+    if (cta < G) {
+      o.u0 = split_begin(U, G, cta);
+      o.u1 = split_begin(U, G, cta + 1);
+      o.pos = locate_unit(c, r, a, o.u0, bad);
+      o.seg = seg_info(c, r, a, o.pos.s, bad);
+    }
+    return o;
+  }
+  const int lane = threadIdx.x & 31;
+  SegInfo g{};
+  int64_t n = 0;
+  if (lane < c.n_seqs) {
+    g = seg_info(c, r, a, lane, bad);
+    n = (int64_t)g.rtiles * c.Hkv * g.span;
+  }
+  int64_t cum = n;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, cum, k);
+    if (lane >= k) cum += x;
+  }
+  const int64_t U = __shfl_sync(0xffffffffu, cum, 31);
+  G = split_ctas(U, G);
+  if (cta >= G) return o;
+  o.u0 = split_begin(U, G, cta);
+  o.u1 = split_begin(U, G, cta + 1);
+  const int l = __ffs(__ballot_sync(0xffffffffu, o.u0 < cum)) - 1;
+  const int64_t left = o.u0 - __shfl_sync(0xffffffffu, cum - n, l);
+  o.seg.v.row0 = __shfl_sync(0xffffffffu, g.v.row0, l);
+  o.seg.v.rows = __shfl_sync(0xffffffffu, g.v.rows, l);
+  o.seg.v.len = __shfl_sync(0xffffffffu, g.v.len, l);
+  o.seg.rtiles = __shfl_sync(0xffffffffu, g.rtiles, l);
+  o.seg.ktiles = __shfl_sync(0xffffffffu, g.ktiles, l);
+  o.seg.ltiles = __shfl_sync(0xffffffffu, g.ltiles, l);
+  o.seg.units = __shfl_sync(0xffffffffu, g.units, l);
+  o.seg.span = __shfl_sync(0xffffffffu, g.span, l);
+  const int64_t seg = left / o.seg.span;
+  o.pos.s = l;
+  o.pos.h = (int)(seg / o.seg.rtiles);
+  o.pos.rt = (int)(seg % o.seg.rtiles);
+  o.pos.j = (int)(left % o.seg.span);
+  return o;
+}
+
 // The units [b, e) of the segment at pos (whose info is g) that lie below list position u1, pos being at u.
 __device__ __forceinline__ void split_units(const SegInfo& g, const AttnSplit& a, const UnitPos& pos, int64_t u, int64_t u1,
                                             int& b, int& e) {

@@ -50,7 +50,7 @@ cudaError_t launch_cached_tc(const CachedMaps& m, const CachedParams& p, cudaStr
 // one CTA: no work list to walk and nothing to merge, against a split of so
 // few keys.
 constexpr int kWholeKeys = 512;
-constexpr int kSmallExtra = 1, kTcExtra = 3;  // AttnSplit::extra: what a segment costs beside its units
+constexpr int kSmallExtra = 1, kTcExtra = 6;  // AttnSplit::extra: what a segment costs beside its units
 
 cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches);

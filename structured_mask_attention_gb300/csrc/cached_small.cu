@@ -204,14 +204,11 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
     seg = seg_info(c, p.r, p.sp, pos.s, bad);
     u1 = pos.rt < seg.rtiles ? seg.span : 0;
   } else {
-    const int64_t U = total_units(c, p.r, p.sp, bad);
-    const int G = split_ctas(U, p.G);
-    if (cta < G) {
-      u0 = split_begin(U, G, cta);
-      u1 = split_begin(U, G, cta + 1);
-      pos = locate_unit(c, p.r, p.sp, u0, bad);
-      seg = seg_info(c, p.r, p.sp, pos.s, bad);
-    }
+    const SplitOpen o = split_open(c, p.r, p.sp, p.G, cta, bad);
+    u0 = o.u0;
+    u1 = o.u1;
+    pos = o.pos;
+    seg = o.seg;
   }
 
   if (warp == kWarps) {

@@ -84,7 +84,7 @@ struct Lay {
   static constexpr int kKI = kBar + ((8 * B_COUNT + 8 + 15) & ~15);
   static constexpr int kML = kKI + NI * (int)sizeof(KInfo);
   static constexpr int kCQ = kML + 2 * 128 * 8;
-  static constexpr int kPC = kCQ + 128 * 4;
+  static constexpr int kPC = kCQ + 256 * 4;
   static constexpr int kBytes = kPC + 4 * 64;
   // 1024 bytes to align; at least 120 KB so that no second CTA shares the SM (each holds all of TMEM)
   static constexpr int kAlloc = kBytes + 1024 > 120 * 1024 ? kBytes + 1024 : 120 * 1024;
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bp + LY::kBar + 8 * B_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bp + LY::kBar + 8 * B_COUNT + 4);
   KInfo* kinfo = reinterpret_cast<KInfo*>(bp + LY::kKI);
-  // split only: both sub-tiles' states of the rows, and the rows' score factors
-  float2* ml = reinterpret_cast<float2*>(bp + LY::kML);  // [2][128]
+  float2* ml = reinterpret_cast<float2*>(bp + LY::kML);  // split: both sub-tiles' states of the rows, [2][128]
+  // the rows' score factors
   float* row_cq = reinterpret_cast<float*>(bp + LY::kCQ);
   Piece* pieces = reinterpret_cast<Piece*>(bp + LY::kPC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(B_KE + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(BAR(B_QF + i), 128);
+      mbar_init(BAR(B_QF + i), KS ? 256 : 128);
       mbar_init(BAR(B_VF + i), 1);
       mbar_init(BAR(B_VE + i), 128);
       mbar_init(BAR(B_WF + i), 128);
@@ -379,17 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 3) {
       // ---------------------------------------------- walk over the CTA's pieces
       uint32_t bad = 0;
-      const int64_t U = total_units(c, p.r, p.sp, bad);
-      const int G = split_ctas(U, p.G), cta = blockIdx.x;
-      int64_t u = 0, u1 = 0;
-      UnitPos pos{0, 0, 0, 0};
-      SegInfo seg;
-      if (cta < G) {
-        u = split_begin(U, G, cta);
-        u1 = split_begin(U, G, cta + 1);
-        pos = locate_unit(c, p.r, p.sp, u, bad);
-        seg = seg_info(c, p.r, p.sp, pos.s, bad);
-      }
+      const SplitOpen open = split_open(c, p.r, p.sp, p.G, blockIdx.x, bad);
+      int64_t u = open.u0;
+      const int64_t u1 = open.u1;
+      UnitPos pos = open.pos;
+      SegInfo seg = open.seg;
       if (lane == 0) {
         for (uint32_t n = 0;; ++n) {
           if (n >= NP && !mbar_wait(BAR(B_PCE + n % NP), (n / NP - 1) & 1, wd, 11)) break;
@@ -663,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + tl + t * 128, tO = tmem + tl + 256;
-    uint32_t sc = 0, tcount = 0, itn[2] = {0, 0}, mlc = 0, q8c = 0, p2 = 0;
+    uint32_t sc = 0, tcount = 0, itn[2] = {0, 0}, mlc = 0, qfc = 0, p2 = 0;
     bool ok = true;
     for (uint32_t np = 0; ok; ++np) {
       const Piece* pp = piece(np);
@@ -683,68 +677,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.at = pp->row0 + (r.live ? tok : 0);
         return r;
       };
-      float cq = p.sl2;
-
-      // Q's row to shared memory: e4m3 in two parts, or bf16
+      // Q's rows to shared memory, HD / 16 (HD / 8) lanes to a row: e4m3 in two
+      // parts with the rows' factors, or bf16.  Pairs: the sub-tile's 128 rows by its
+      // threads; split: the tile's 128 rows by both sub-tiles' threads.
+      constexpr int kTeam = KS ? 256 : 128;
+      const int tid = (KS ? t * 128 : 0) + row, first = pp->rt * kTileRows + (KS ? 0 : t * 128);
+      auto row_of = [&](int r, bool& live) {
+        const int fr = first + r, tok = fr / p.sp.group, head = pp->h * p.sp.group + fr - tok * p.sp.group;
+        live = tok < pp->rows;
+        return static_cast<const __nv_bfloat16*>(p.Q) + ((pp->row0 + (live ? tok : 0)) * p.Hq + head) * HD;
+      };
       auto put_q8 = [&]() {
-        const Row r = my_row();
-        const bool live = r.live;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q) + (r.at * p.Hq + r.head) * HD;
         const uint32_t dst = base + LY::kQ + (KS ? 0 : t) * LY::kQBytes;
-        uint32_t w[HD / 2], amax = 0;
+        constexpr int PER = HD / 16;
+        const int i = tid % PER;
+#pragma unroll 2
+        for (int r = tid / PER; r < 128; r += kTeam / PER) {
+          bool live;
+          const uint4* src = reinterpret_cast<const uint4*>(row_of(r, live)) + 2 * i;
+          const uint4 x = live ? __ldg(src) : make_uint4(0, 0, 0, 0), y = live ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          uint32_t amax = 0, hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
-          w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-        }
+          for (int k = 0; k < 8; ++k) amax = __vmaxu2(amax, w[k] & 0x7fff7fffu);
+          amax = max(amax & 0xffffu, amax >> 16);
 #pragma unroll
-        for (int i = 0; i < HD / 2; ++i) amax = max(amax, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        float inv;
-        const float f = row_factor(amax, inv);
-        cq = p.sl2 * inv;
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          uint32_t hi[4], lo[4];
-          split_e4m3(w + 8 * i, f, hi, lo);
-          const uint32_t at = e4m3_chunk<HD>(row, i);
-          st_shared_v4(dst + at, hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(dst + 128 * HD + at, lo[0], lo[1], lo[2], lo[3]);
+          for (int o = PER / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float inv;
+          const float f = row_factor(amax, inv);
+          split_e4m3(w, f, hi, lo);
+          const uint32_t at = dst + e4m3_chunk<HD>(r, i);
+          st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(at + 128 * HD, lo[0], lo[1], lo[2], lo[3]);
+          if (i == 0) row_cq[(KS ? 0 : t * 128) + r] = p.sl2 * inv;
         }
       };
       auto put_q16 = [&]() {
-        const Row r = my_row();
-        const bool live = r.live;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q) + (r.at * p.Hq + r.head) * HD;
         const uint32_t dst = base + LY::kQ + (KS ? 1 : t) * LY::kQBytes;
+        constexpr int PER = HD / 8;
+        const int i = tid % PER;
 #pragma unroll 4
-        for (int i = 0; i < HD / 8; ++i) {
-          const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
-          st_shared_v4(dst + (i >> 3) * kSlot + row * 128 + (((i & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
+        for (int r = tid / PER; r < 128; r += kTeam / PER) {
+          bool live;
+          const uint4* src = reinterpret_cast<const uint4*>(row_of(r, live)) + i;
+          const uint4 x = live ? __ldg(src) : make_uint4(0, 0, 0, 0);
+          st_shared_v4(dst + (i >> 3) * kSlot + r * 128 + (((i & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
         }
       };
+      float cq = p.sl2;
       if (n > 0) {
-        if (KS) {
-          // sub-tile 0's threads write the codes, sub-tile 1's the bf16 rows
-          if (t == 0 && nk > 0) {
-            put_q8();
-            row_cq[row] = cq;
-            fence_proxy_async_smem();
-            mbar_arrive(BAR(B_QF + 0));
-          }
-          if (t == 1 && nl > 0) {
-            put_q16();
-            fence_proxy_async_smem();
-            mbar_arrive(BAR(B_QF + 1));
-          }
-        } else {
-          if (nk > 0) put_q8();
+        if (KS ? nk > 0 : true) {
+          if (KS || nk > 0) put_q8();
           else put_q16();
           fence_proxy_async_smem();
-          mbar_arrive(BAR(B_QF + t));
+          mbar_arrive(BAR(B_QF + (KS ? 0 : t)));
         }
+        if (KS && nl > 0) {
+          put_q16();
+          fence_proxy_async_smem();
+          mbar_arrive(BAR(B_QF + 1));
+        }
+        if (nk > 0) {  // the factor of this thread's row, found by another thread
+          ok = mbar_wait(BAR(B_QF + (KS ? 0 : t)), qfc & 1, wd, 42);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          cq = row_cq[(KS ? 0 : t * 128) + row];
+        }
+        if (!KS || nk > 0) ++qfc;
       }
       float m_ref = -INFINITY, l = 0.f;
-      bool have_cq = !KS || t == 0;
       // keys left from the piece's first cached (own) tile on
       const int left_k = pp->len - pp->k0 * kUnit, left_l = pp->rows - pp->l0 * kUnit;
       for (int j = KS ? t : 0; j < n; j += KS ? 2 : 1, ++sc) {
@@ -761,15 +762,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        if (KS && !have_cq && !own) {
-          // the factor that sub-tile 0's thread found (this phase of QF cannot
-          // be followed by the next before the piece's end, which needs this thread)
-          ok = mbar_wait(BAR(B_QF + 0), q8c & 1, wd, 42);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          cq = row_cq[row];
-          have_cq = true;
-        }
         const int hi = own ? left_l - (j - nk) * kUnit : left_k - j * kUnit;
         const float rf = own ? p.sl2 : cq;
         float f[4] = {rf * ks4.x, rf * ks4.y, rf * ks4.z, rf * ks4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
@@ -855,11 +847,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           put_q16();
           fence_proxy_async_smem();
           mbar_arrive(BAR(B_QF + t));
+          ++qfc;
         }
       }
       if (!ok) break;
       tcount += (uint32_t)n;
-      if (nk > 0) ++q8c;
 
       // ---- the piece's result
       if (FINE) m_ref -= kFineShift;  // the reference of the weights as they were kept

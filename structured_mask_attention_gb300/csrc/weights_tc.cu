@@ -206,17 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     // ---------------------------------------------- walk over the CTA's pieces
     uint32_t bad = 0;
-    const int64_t U = total_units(c, p.r, p.sp, bad);
-    const int G = split_ctas(U, p.G), cta = blockIdx.x;
-    int64_t u = 0, u1 = 0;
-    UnitPos pos{0, 0, 0, 0};
-    SegInfo seg;
-    if (cta < G) {
-      u = split_begin(U, G, cta);
-      u1 = split_begin(U, G, cta + 1);
-      pos = locate_unit(c, p.r, p.sp, u, bad);
-      seg = seg_info(c, p.r, p.sp, pos.s, bad);
-    }
+    const SplitOpen open = split_open(c, p.r, p.sp, p.G, blockIdx.x, bad);
+    int64_t u = open.u0;
+    const int64_t u1 = open.u1;
+    UnitPos pos = open.pos;
+    SegInfo seg = open.seg;
     if (lane == 0) {
       for (uint32_t n = 0;; ++n) {
         WPiece q;

@@ -225,18 +225,24 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
       // lane 8 a + x: page and scales of keys 16 x of tile a of a batch of 4 tiles, one batch ahead
       auto lookup = [&](int b) {
         const int tile = 4 * b + (lane >> 3), key = (jb + tile) * kUnit + 16 * (lane & 7);
-        if (tile >= n || key >= len) return -1;
-        const int id = __ldg(table + (key >> c.lp));
+        return tile < n && key < len ? __ldg(table + (key >> c.lp)) : -1;
+      };
+      // (a batch's entries are looked at a batch after they were asked for)
+      auto checked = [&](int id, int b) {
         if (id >= 0 && id < c.n_pages) return id;
-        bad |= kStatusBadPage;
+        const int tile = 4 * b + (lane >> 3), key = (jb + tile) * kUnit + 16 * (lane & 7);
+        if (tile < n && key < len) bad |= kStatusBadPage;
         return -1;
       };
       auto scale_of = [&](const float* sc, int id) { return id >= 0 ? __ldg(sc + (int64_t)id * c.Hkv + h) : 1.f; };
-      int id = lookup(0), id1 = lookup(1);
+      const int raw0 = lookup(0);
+        int raw1 = lookup(1);
+      int id = checked(raw0, 0);
       float sk = scale_of(c.ks, id), sv = scale_of(c.vs, id);
       for (int b = 0; ok && 4 * b < n; ++b) {
+        const int id1 = checked(raw1, b + 1);
         const float sk1 = scale_of(c.ks, id1), sv1 = scale_of(c.vs, id1);
-        const int id2 = lookup(b + 2);
+        const int raw2 = lookup(b + 2);
         for (int a = 0; a < 4 && 4 * b + a < n; ++a) {
           ok = mbar_wait(KE(slot), ph, wd, 70);
           ok = __all_sync(0xffffffffu, ok);
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           if (mine) tma_load_3d(base + LY::kV + slot * LY::kTile + lane * c.page * HD, &tV8, VF(slot), 0, 0, blk);
           if (++slot == NS) slot = 0, ph ^= 1;
         }
-        id = id1; id1 = id2; sk = sk1; sv = sv1;
+        id = id1; raw1 = raw2; sk = sk1; sv = sv1;
       }
       if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
     }

@@ -272,19 +272,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t* table = c.table + (int64_t)pp->s * c.max_pages;
         auto lookup = [&](int b) {  // page of this lane's 16 keys of batch b, -1: none
           const int tile = 4 * b + (lane >> 3), key = (k0 + tile) * kUnit + 16 * (lane & 7);
-          if (tile >= nk || key >= len) return -1;
-          const int id = __ldg(table + (key >> c.lp));
+          return tile < nk && key < len ? __ldg(table + (key >> c.lp)) : -1;
+        };
+        // (a batch's entries are looked at a batch after they were asked for)
+        auto checked = [&](int id, int b) {
           if (id >= 0 && id < c.n_pages) return id;
-          bad |= kStatusBadPage;
+          const int tile = 4 * b + (lane >> 3), key = (k0 + tile) * kUnit + 16 * (lane & 7);
+          if (tile < nk && key < len) bad |= kStatusBadPage;
           return -1;
         };
         auto scale_of = [&](const float* sc, int id) { return id >= 0 ? __ldg(sc + (int64_t)id * c.Hkv + h) : 1.f; };
-        int id = lookup(0), id1 = lookup(1);
+        const int raw0 = lookup(0);
+        int raw1 = lookup(1);
+        int id = checked(raw0, 0);
         float sk = 1.f, sv = 1.f, sk1 = 1.f, sv1 = 1.f;
         if (!isV) sk = scale_of(c.ks, id), sv = scale_of(c.vs, id);
         for (int b = 0; ok && 4 * b < nk; ++b) {
+          const int id1 = checked(raw1, b + 1);
           if (!isV) sk1 = scale_of(c.ks, id1), sv1 = scale_of(c.vs, id1);
-          const int id2 = lookup(b + 2);
+          const int raw2 = lookup(b + 2);
           for (int a = 0; a < 4 && 4 * b + a < nk; ++a, ++tc) {
             const int key0 = (k0 + 4 * b + a) * kUnit;
             ok = mbar_wait(BAR((isV ? B_VE : B_KE) + slot), sph, wd, 20 + warp);
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (++slot == (uint32_t)nslots) slot = 0, sph ^= 1;
           }
-          id = id1; id1 = id2; sk = sk1; sv = sv1;
+          id = id1; raw1 = raw2; sk = sk1; sv = sv1;
         }
         // own tiles: K by panels through the K slots; V straight into the bf16 slot that its tile has
         const int nl = pp->nl;

@@ -119,19 +119,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // lane 8 a + x: keys 16 x of tile a of a batch of 4 tiles, one batch ahead
       auto lookup = [&](int b) {
         const int tile = 4 * b + (lane >> 3), key = (j0 + tile) * kUnit + 16 * (lane & 7);
-        if (tile >= n || key >= len) return -1;
-        const int id = __ldg(table + (key >> c.lp));
+        return tile < n && key < len ? __ldg(table + (key >> c.lp)) : -1;
+      };
+      // (a batch's entries are looked at a batch after they were asked for)
+      auto checked = [&](int id, int b) {
         if (id >= 0 && id < c.n_pages) return id;
-        bad |= kStatusBadPage;
+        const int tile = 4 * b + (lane >> 3), key = (j0 + tile) * kUnit + 16 * (lane & 7);
+        if (tile < n && key < len) bad |= kStatusBadPage;
         return -1;
       };
       auto scale_of = [&](int id) { return id >= 0 ? __ldg(c.ks + (int64_t)id * c.Hkv + h) : 0.f; };
       for (int ch = 0; ok && ch < chunks; ++ch) {
-        int id = lookup(0), id1 = lookup(1);
+        const int raw0 = lookup(0);
+        int raw1 = lookup(1);
+      int id = checked(raw0, 0);
         float sc = scale_of(id);
         for (int b = 0; ok && 4 * b < n; ++b) {
+          const int id1 = checked(raw1, b + 1);
           const float sc1 = scale_of(id1);
-          const int id2 = lookup(b + 2);
+          const int raw2 = lookup(b + 2);
           for (int a = 0; a < 4 && 4 * b + a < n; ++a, ++tc) {
             ok = mbar_wait(BAR(B_KE + slot), sph, wd, 61);
             ok = __all_sync(0xffffffffu, ok);
@@ -160,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           (int)((int64_t)pid * c.Hkv + h));
             if (++slot == NK) slot = 0, sph ^= 1;
           }
-          id = id1; id1 = id2; sc = sc1;
+          id = id1; raw1 = raw2; sc = sc1;
         }
       }
       done(np);
@@ -289,40 +295,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(BAR(B_QF), qd & 1, wd, 66);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t rows = base + LY::kRow;
+        const float4* rowc = reinterpret_cast<const float4*>(bp + LY::kRow);
+        // (a tile's weights are read a tile ahead)
+        auto old = [&](int j) { return j < n && (j0 + j) * kUnit + key < len ? W[(j0 + j) * kUnit + key] : 0.f; };
+        float next = old((int)((tc ^ (uint32_t)t) & 1));
         for (int j = 0; j < n; ++j, ++tc) {
           if ((tc & 1) != (uint32_t)t) continue;
           const int at = (j0 + j) * kUnit + key;
+          const float was = next;
+          next = old(j + 2);
           ok = mbar_wait(BAR(B_KI + tc % NI), (tc / NI) & 1, wd, 67);
           const float ks = infos[tc % NI].s[key >> 4];
           const bool mine = at < len && !((infos[tc % NI].gone >> (key >> 4)) & 1);
-          const float was = mine ? W[at] : 0.f;
           if (ok) ok = mbar_wait(BAR(B_SF + t), sph, wd, 68);
           sph ^= 1;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           const uint64_t ks2 = f2(ks, ks);
-          uint64_t sum = f2(0.f, 0.f);
-          for (int x = 0; x < N; x += 32) {
+          uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+          auto add32 = [&](const uint32_t (&a)[32], int x) {
+            float4 rc[16];  // {c0, c1, n0, n1} of two rows
+#pragma unroll
+            for (int y = 0; y < 16; ++y) rc[y] = rowc[(x >> 1) + y];
+            float e[32];
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              f2_split(f2_fma(f2_mul(f2(__uint_as_float(a[2 * y]), __uint_as_float(a[2 * y + 1])), ks2),
+                              f2(rc[y].x, rc[y].y), f2(rc[y].z, rc[y].w)),
+                       e[2 * y], e[2 * y + 1]);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) e[y] = ex2_approx(e[y]);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) sum[y & 1] = f2_add(sum[y & 1], f2(e[2 * y], e[2 * y + 1]));
+          };
+          int x = 0;
+          for (; x + 64 <= N; x += 64) {
+            uint32_t a[32], b[32];
+            tmem_ld32x2(tS + x, tS + x + 32, a, b);
+            add32(a, x);
+            add32(b, x + 32);
+          }
+          if (x < N) {
             uint32_t a[32];
             tmem_ld32(tS + x, a);
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              float c0, c1, n0, n1;
-              asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                           : "=f"(c0), "=f"(c1), "=f"(n0), "=f"(n1)
-                           : "r"(rows + (x + y) * 8));
-              float e0, e1;
-              f2_split(f2_fma(f2_mul(f2(__uint_as_float(a[y]), __uint_as_float(a[y + 1])), ks2), f2(c0, c1), f2(n0, n1)),
-                       e0, e1);
-              sum = f2_add(sum, f2(ex2_approx(e0), ex2_approx(e1)));
-            }
+            add32(a, x);
           }
           tc_fence_before();
           mbar_arrive(BAR(B_SE + t));
           float s0, s1;
-          f2_split(sum, s0, s1);
+          f2_split(f2_add(sum[0], sum[1]), s0, s1);
           if (mine) W[at] = was + (s0 + s1);
         }
         if (!ok) break;

@@ -79,6 +79,11 @@ __device__ __forceinline__ int page_id(const CacheDesc& c, int s, int j, uint32_
   return -1;
 }
 
+// Of the eight groups of 16 keys of a unit, those that open a page (a bit each).
+__device__ __forceinline__ uint32_t first_groups(int page) {
+  return page == 16 ? 0xffu : page == 32 ? 0x55u : page == 64 ? 0x11u : 0x01u;
+}
+
 // The scale of a block whose largest magnitude has the fp32 bits `amax`
 // (NaN when the block holds a value that is not finite).
 __device__ __forceinline__ float block_scale(uint32_t amax) {

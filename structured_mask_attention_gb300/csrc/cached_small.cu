@@ -140,6 +140,8 @@ struct SInfo {  // of each 16 keys of a tile: K's scale, log2 and inverse of V's
   int gone;     // bit x: no page
 };
 
+constexpr int NI = 16;  // info slots: the tiles in the ring, and a batch of four ahead
+
 template <int HD>
 struct LayS {
   static constexpr int NS = HD == 128 ? 2 : 4;    // slots of K and of V
@@ -148,7 +150,7 @@ struct LayS {
   static constexpr int kRed = 2 * NS * kTile;     // [kWarps][16][HD + 4] fp32; before, each warp's Q fragments
   static constexpr int kML = kRed + kWarps * 16 * (HD + 4) * 4;  // [kWarps][16][2]
   static constexpr int kInfo = kML + kWarps * 16 * 2 * 4;
-  static constexpr int kBar = (kInfo + NS * (int)sizeof(SInfo) + 15) & ~15;
+  static constexpr int kBar = (kInfo + NI * (int)sizeof(SInfo) + 15) & ~15;
   static constexpr int kBytes = kBar + 4 * NS * 8 + 16;
   static constexpr int kAlloc = kBytes + 1024;    // (aligned to 1024)
 };
@@ -213,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
 
   if (warp == kWarps) {
     // -------------------------------------------------- loader
-    uint32_t slot = 0, ph = 1;
+    uint32_t slot = 0, ph = 1, tc = 0;
+    const uint32_t page_bytes = (uint32_t)(c.page * HD), page_groups = first_groups(c.page);
     bool ok = true;
     for (int64_t u = u0; ok && u < u1;) {
       int jb, je;
@@ -243,43 +246,39 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
         const int id1 = checked(raw1, b + 1);
         const float sk1 = scale_of(c.ks, id1), sv1 = scale_of(c.vs, id1);
         const int raw2 = lookup(b + 2);
-        for (int a = 0; a < 4 && 4 * b + a < n; ++a) {
+        // the batch's tiles, a group of eight lanes each
+        const int grp = lane >> 3, x = lane & 7;
+        const unsigned none = __ballot_sync(0xffffffffu, id < 0);
+        SInfo& si = infos[(tc + grp) % NI];
+        if (4 * b + grp < n) {
+          si.s[x] = sk;
+          si.lv[x] = log2f(sv);
+          si.iv[x] = 1.f / sv;
+          if (x == 0) si.gone = (int)((none >> lane) & 0xffu);
+        }
+        const uint32_t bytes = (uint32_t)__popc(~(none >> (lane & 24)) & page_groups) * page_bytes;
+        const bool loads = id >= 0 && ((page_groups >> x) & 1);
+        const int blk = (int)((int64_t)id * c.Hkv + h);
+        for (int a = 0; a < 4 && 4 * b + a < n; ++a, ++tc) {
           ok = mbar_wait(KE(slot), ph, wd, 70);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const int x = lane & 7;
-          const int cid = __shfl_sync(0xffffffffu, id, 8 * a + x);
-          const float ck = __shfl_sync(0xffffffffu, sk, 8 * a + x), cv = __shfl_sync(0xffffffffu, sv, 8 * a + x);
-          const unsigned none = __ballot_sync(0xffffffffu, cid < 0) & 0xffu;
-          SInfo& si = infos[slot];
-          if (lane < 8) {
-            si.s[x] = ck;
-            si.lv[x] = log2f(cv);
-            si.iv[x] = 1.f / cv;
-          }
-          if (lane == 0) si.gone = (int)none;
-          const int per = kUnit >> c.lp, step = c.page >> 4;
-          int cnt = 0;
-          for (int q = 0; q < per; ++q) cnt += !((none >> (q * step)) & 1u);
-          __syncwarp();
-          const int pid = __shfl_sync(0xffffffffu, cid, (lane * step) & 7);
-          const int blk = (int)((int64_t)pid * c.Hkv + h);
-          const bool mine = lane < per && pid >= 0;
-          if (lane == 0) {
-            if (cnt) mbar_arrive_expect_tx(KF(slot), (uint32_t)(cnt * c.page * HD));
+          if (lane == 8 * a) {
+            if (bytes) mbar_arrive_expect_tx(KF(slot), bytes);
             else mbar_arrive(KF(slot));
           }
           __syncwarp();
-          if (mine) tma_load_3d(base + LY::kK + slot * LY::kTile + lane * c.page * HD, &tK8, KF(slot), 0, 0, blk);
+          const bool mine = grp == a && loads;  // the lane of a page's first keys loads it
+          if (mine) tma_load_3d(base + LY::kK + slot * LY::kTile + 16 * x * HD, &tK8, KF(slot), 0, 0, blk);
           ok = mbar_wait(VE(slot), ph, wd, 71);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) {
-            if (cnt) mbar_arrive_expect_tx(VF(slot), (uint32_t)(cnt * c.page * HD));
+          if (lane == 8 * a) {
+            if (bytes) mbar_arrive_expect_tx(VF(slot), bytes);
             else mbar_arrive(VF(slot));
           }
           __syncwarp();
-          if (mine) tma_load_3d(base + LY::kV + slot * LY::kTile + lane * c.page * HD, &tV8, VF(slot), 0, 0, blk);
+          if (mine) tma_load_3d(base + LY::kV + slot * LY::kTile + 16 * x * HD, &tV8, VF(slot), 0, 0, blk);
           if (++slot == NS) slot = 0, ph ^= 1;
         }
         id = id1; raw1 = raw2; sk = sk1; sv = sv1;
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
   // meet at the same barriers; the call reports the timeout.
   const int mt = warp / KG, kg = warp % KG;
   auto perm = [](int x) { return HD == 128 ? (x >> 1) | ((x & 1) << 2) : x; };
-  uint32_t slot = 0, ph = 0;
+  uint32_t slot = 0, ph = 0, tc = 0;
   bool ok = true;
   for (int64_t u = u0; u < u1;) {
     int jb, je;
@@ -359,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
 
     // ---- cached keys
     const int kc = min(je, seg.ktiles);
-    for (int j = jb; j < kc; ++j) {
+    for (int j = jb; j < kc; ++j, ++tc) {
       const int left = seg.v.len - j * kUnit;  // keys of the tile
       if (ok) ok = mbar_wait(KF(slot), ph, wd, 72);
-      const SInfo& si = infos[slot];
+      const SInfo& si = infos[tc % NI];
       const int gone = si.gone;
       const bool full = left >= kUnit && gone == 0;
 #pragma unroll 1

@@ -56,7 +56,7 @@ constexpr float kRescale = 8.0f;  // log2 units: the reference maximum moves in 
 // (fp32 outputs) weights are kept 2^7 larger, up to 2^15: the second part's smallest step, 2^-24, is so much finer
 constexpr float kFineShift = 7.0f;
 constexpr int NK = 3;             // K slots: 128 keys of codes, or one 64-column panel of own keys
-constexpr int NI = 8;             // tile-info slots (more than any two roles are apart)
+constexpr int NI = 16;            // tile-info slots (more than any two roles are apart, and a batch of four)
 constexpr int kSlot = 128 * 128;  // bytes of a K slot, of a V slot and of a bf16 panel
 
 enum { B_QF = 0, B_KF = 2, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + 2, B_WF = B_VE + 2, B_WE = B_WF + 2,
@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t bad = 0;
       uint32_t slot = 0, sph = 1, tc = 0;  // slot and its phase parity to wait for, tiles so far
       constexpr int nslots = isV ? 2 : NK;
+      const uint32_t page_bytes = (uint32_t)(c.page * HD), page_groups = first_groups(c.page);
       bool ok = true;
       for (uint32_t np = 0; ok; ++np) {
         const Piece* pp = piece(np);
@@ -291,47 +292,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int id1 = checked(raw1, b + 1);
           if (!isV) sk1 = scale_of(c.ks, id1), sv1 = scale_of(c.vs, id1);
           const int raw2 = lookup(b + 2);
+          // the batch's tiles, a group of eight lanes each
+          const int grp = lane >> 3, x = lane & 7, key = (k0 + 4 * b) * kUnit + 16 * lane;
+          const bool on = 4 * b + grp < nk;
+          const unsigned none = __ballot_sync(0xffffffffu, id < 0);
+          if (!isV) {
+            const float pk = __shfl_xor_sync(0xffffffffu, sk, 1), pv = __shfl_xor_sync(0xffffffffu, sv, 1);
+            const unsigned gone = __ballot_sync(0xffffffffu, id < 0 && key < len);
+            const unsigned odd = __ballot_sync(0xffffffffu, (key | 16) < len && (sk != pk || sv != pv));
+            KInfo& ki = kinfo[(tc + grp) % NI];
+            if (on) {
+              ki.s[x & 1][x >> 1] = sk;
+              ki.lv[x & 1][x >> 1] = log2f(sv);
+              ki.iv[x & 1][x >> 1] = 1.f / sv;
+            }
+            if (on && x == 0) {
+              ki.fine = (((gone | odd) >> lane) & 0xffu) != 0;
+              ki.gone = (int)((gone >> lane) & 0xffu);
+            }
+            __syncwarp();
+            if (on && x == 0) mbar_arrive(BAR(B_KI + (tc + grp) % NI));
+          }
+          const uint32_t bytes = (uint32_t)__popc(~(none >> (lane & 24)) & page_groups) * page_bytes;
+          const bool loads = id >= 0 && ((page_groups >> x) & 1);
+          const int64_t blk = (int64_t)id * c.Hkv + h;
           for (int a = 0; a < 4 && 4 * b + a < nk; ++a, ++tc) {
-            const int key0 = (k0 + 4 * b + a) * kUnit;
             ok = mbar_wait(BAR((isV ? B_VE : B_KE) + slot), sph, wd, 20 + warp);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const int x = lane & 7;
-            const int cid = __shfl_sync(0xffffffffu, id, 8 * a + x);
-            const unsigned none = __ballot_sync(0xffffffffu, cid < 0) & 0xffu;
             const uint32_t fb = BAR((isV ? B_VF : B_KF) + slot);
-            if (!isV) {
-              const float ck = __shfl_sync(0xffffffffu, sk, 8 * a + x), cv = __shfl_sync(0xffffffffu, sv, 8 * a + x);
-              const float pk = __shfl_xor_sync(0xffffffffu, ck, 1), pv = __shfl_xor_sync(0xffffffffu, cv, 1);
-              const unsigned gone = __ballot_sync(0xffffffffu, cid < 0 && key0 + 16 * x < len) & 0xffu;
-              const unsigned odd = __ballot_sync(0xffffffffu, key0 + 16 * (x | 1) < len && (ck != pk || cv != pv)) & 0xffu;
-              KInfo& ki = kinfo[tc % NI];
-              if (lane < 8) {
-                ki.s[x & 1][x >> 1] = ck;
-                ki.lv[x & 1][x >> 1] = log2f(cv);
-                ki.iv[x & 1][x >> 1] = 1.f / cv;
-              }
-              if (lane == 0) {
-                ki.fine = (gone | odd) != 0;
-                ki.gone = (int)gone;
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(BAR(B_KI + tc % NI));
-            }
-            // pages of the tile that hold keys: lane q loads page q
-            const int per = kUnit >> c.lp, step = c.page >> 4;  // pages per tile, 16-key groups per page
-            int n = 0;
-            for (int q = 0; q < per; ++q) n += !((none >> (q * step)) & 1u);
-            if (lane == 0) {
-              if (n) mbar_arrive_expect_tx(fb, (uint32_t)(n * c.page * HD));
+            if (lane == 8 * a) {
+              if (bytes) mbar_arrive_expect_tx(fb, bytes);
               else mbar_arrive(fb);
             }
             __syncwarp();
-            const int pid = __shfl_sync(0xffffffffu, cid, (lane * step) & 7);
-            if (lane < per && pid >= 0) {
-              const uint32_t dst = base + (isV ? LY::kV : LY::kK) + slot * kSlot + lane * c.page * HD;
-              const int64_t blk = (int64_t)pid * c.Hkv + h;
-              if (isV) bulk_load(dst, c.v8 + blk * c.page * HD, (uint32_t)(c.page * HD), fb);
+            if (grp == a && loads) {  // the lane of a page's first keys loads it
+              const uint32_t dst = base + (isV ? LY::kV : LY::kK) + slot * kSlot + 16 * x * HD;
+              if (isV) bulk_load(dst, c.v8 + blk * page_bytes, page_bytes, fb);
               else tma_load_3d(dst, &tK8, fb, 0, 0, (int)blk);
             }
             if (++slot == (uint32_t)nslots) slot = 0, sph ^= 1;

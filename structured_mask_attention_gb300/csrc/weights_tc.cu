@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int NK = 6;              // K slots of 128 keys
-constexpr int NI = 16;             // tile-info slots
+constexpr int NI = 16;             // tile-info slots (the K and S slots ahead of a reader, and a batch of four)
 constexpr int NP = 4;              // piece slots
 constexpr int kChunk = 256;        // rows at a time
 constexpr int kSlot = 128 * 128;
@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------- K loader
     uint32_t bad = 0, slot = 0, sph = 1, tc = 0;
+    const uint32_t page_bytes = (uint32_t)(c.page * HD), page_groups = first_groups(c.page);
     bool ok = true;
     for (uint32_t np = 0; ok; ++np) {
       const WPiece* pp = piece(np);
@@ -138,32 +139,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int id1 = checked(raw1, b + 1);
           const float sc1 = scale_of(id1);
           const int raw2 = lookup(b + 2);
+          // the batch's tiles, a group of eight lanes each
+          const int grp = lane >> 3, x = lane & 7;
+          const bool on = 4 * b + grp < n;
+          const unsigned none = __ballot_sync(0xffffffffu, id < 0);
+          WInfo& wi = infos[(tc + grp) % NI];
+          if (on) wi.s[x] = sc;
+          if (on && x == 0) wi.gone = (int)((none >> lane) & 0xffu);
+          __syncwarp();
+          if (on && x == 0) mbar_arrive(BAR(B_KI + (tc + grp) % NI));
+          const uint32_t bytes = (uint32_t)__popc(~(none >> (lane & 24)) & page_groups) * page_bytes;
+          const bool loads = id >= 0 && ((page_groups >> x) & 1);
+          const int blk = (int)((int64_t)id * c.Hkv + h);
           for (int a = 0; a < 4 && 4 * b + a < n; ++a, ++tc) {
             ok = mbar_wait(BAR(B_KE + slot), sph, wd, 61);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const int x = lane & 7;
-            const int cid = __shfl_sync(0xffffffffu, id, 8 * a + x);
-            const float csc = __shfl_sync(0xffffffffu, sc, 8 * a + x);
-            const unsigned none = __ballot_sync(0xffffffffu, cid < 0) & 0xffu;
-            const uint32_t fb = BAR(B_KF + slot);
-            WInfo& wi = infos[tc % NI];
-            if (lane < 8) wi.s[x] = csc;
-            if (lane == 0) wi.gone = (int)none;
-            const int per = kUnit >> c.lp, step = c.page >> 4;
-            int cnt = 0;
-            for (int q = 0; q < per; ++q) cnt += !((none >> (q * step)) & 1u);
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(BAR(B_KI + tc % NI));
-              if (cnt) mbar_arrive_expect_tx(fb, (uint32_t)(cnt * c.page * HD));
-              else mbar_arrive(fb);
+            if (lane == 8 * a) {
+              if (bytes) mbar_arrive_expect_tx(BAR(B_KF + slot), bytes);
+              else mbar_arrive(BAR(B_KF + slot));
             }
             __syncwarp();
-            const int pid = __shfl_sync(0xffffffffu, cid, (lane * step) & 7);
-            if (lane < per && pid >= 0)
-              tma_load_3d(base + LY::kK + slot * kSlot + lane * c.page * HD, &tK8, fb, 0, 0,
-                          (int)((int64_t)pid * c.Hkv + h));
+            if (grp == a && loads)  // the lane of a page's first keys loads it
+              tma_load_3d(base + LY::kK + slot * kSlot + 16 * x * HD, &tK8, BAR(B_KF + slot), 0, 0, blk);
             if (++slot == NK) slot = 0, sph ^= 1;
           }
           id = id1; raw1 = raw2; sc = sc1;

@@ -220,13 +220,17 @@ __device__ __forceinline__ UnitPos locate_unit(const CacheDesc& c, const RowsDes
 // CTAs that take part: no more than there are units, so that none is empty.
 __device__ __forceinline__ int split_ctas(int64_t U, int G) { return U < G ? (int)U : G; }
 __device__ __forceinline__ int64_t split_begin(int64_t U, int G, int c) { return U * c / G; }
-// What CTA `cta` of G takes: list positions [u0, u1) and the first's segment
-// (u0 = u1: nothing).  By a whole warp.  Up to 32 sequences are looked at once.
+// What CTA `cta` of G takes: list positions [u0, u1) (u0 = u1: nothing), and the
+// first position's segment (with `last`: the last position's); U and G: all
+// positions, the CTAs that take part.  By a whole warp.  Up to 32 sequences are
+// looked at once.
 struct SplitOpen {
-  int64_t u0, u1;
+  int64_t u0, u1, U;
+  int G;
   UnitPos pos;
   SegInfo seg;
 };
+template <bool last = false>
 __device__ __forceinline__ SplitOpen split_open(const CacheDesc& c, const RowsDesc& r, const AttnSplit& a, int G, int cta,
                                                 uint32_t& bad) {
   SplitOpen o;
@@ -236,10 +240,12 @@ __device__ __forceinline__ SplitOpen split_open(const CacheDesc& c, const RowsDe
   if (c.n_seqs > 32) {
     const int64_t U = total_units(c, r, a, bad);
     G = split_ctas(U, G);
+    o.U = U;
+    o.G = G;
     if (cta < G) {
       o.u0 = split_begin(U, G, cta);
       o.u1 = split_begin(U, G, cta + 1);
-      o.pos = locate_unit(c, r, a, o.u0, bad);
+      o.pos = locate_unit(c, r, a, last ? o.u1 - 1 : o.u0, bad);
       o.seg = seg_info(c, r, a, o.pos.s, bad);
     }
     return o;
@@ -259,11 +265,14 @@ __device__ __forceinline__ SplitOpen split_open(const CacheDesc& c, const RowsDe
   }
   const int64_t U = __shfl_sync(0xffffffffu, cum, 31);
   G = split_ctas(U, G);
+  o.U = U;
+  o.G = G;
   if (cta >= G) return o;
   o.u0 = split_begin(U, G, cta);
   o.u1 = split_begin(U, G, cta + 1);
-  const int l = __ffs(__ballot_sync(0xffffffffu, o.u0 < cum)) - 1;
-  const int64_t left = o.u0 - __shfl_sync(0xffffffffu, cum - n, l);
+  const int64_t at = last ? o.u1 - 1 : o.u0;
+  const int l = __ffs(__ballot_sync(0xffffffffu, at < cum)) - 1;
+  const int64_t left = at - __shfl_sync(0xffffffffu, cum - n, l);
   o.seg.v.row0 = __shfl_sync(0xffffffffu, g.v.row0, l);
   o.seg.v.rows = __shfl_sync(0xffffffffu, g.v.rows, l);
   o.seg.v.len = __shfl_sync(0xffffffffu, g.v.len, l);

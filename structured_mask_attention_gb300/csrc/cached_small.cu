@@ -621,15 +621,15 @@ __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const 
   uint32_t bad = 0;
   const CacheDesc& c = p.c;
   const int cta = blockIdx.x;
-  const int64_t U = total_units(c, p.r, p.sp, bad);
-  const int G = split_ctas(U, p.G);
+  const SplitOpen o = split_open<true>(c, p.r, p.sp, p.G, cta, bad);
   // (the kernel before this one may still run; every thread waits for it, so
   // that this grid's end implies that one's)
   dependency_wait();
-  if (cta >= G - 1) return;
-  const int64_t u0 = split_begin(U, G, cta), u1 = split_begin(U, G, cta + 1);
-  const UnitPos pos = locate_unit(c, p.r, p.sp, u1 - 1, bad);
-  const SegInfo seg = seg_info(c, p.r, p.sp, pos.s, bad);
+  if (cta >= o.G - 1) return;
+  const int64_t U = o.U, u0 = o.u0, u1 = o.u1;
+  const int G = o.G;
+  const UnitPos pos = o.pos;
+  const SegInfo seg = o.seg;
   const int64_t begin = u1 - 1 - pos.j, last = begin + seg.span - 1;
   // begun by another CTA (its first unit lies before or behind this CTA's range), or finished here
   if (begin + p.sp.extra < u0 || begin + p.sp.extra >= u1 || last < u1) return;

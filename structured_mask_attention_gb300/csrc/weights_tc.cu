@@ -257,34 +257,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cnt = min(flat - r0, kChunk), N = (cnt + 31) & ~31;
         // ---- HD / 16 lanes take a row, 16 values each
         constexpr int PER = HD / 16;
-        for (int r = tid / PER; r < N; r += 256 / PER) {
-          const int i = tid % PER, fr = r0 + r, tok = fr / p.sp.group, head = h * p.sp.group + fr - tok * p.sp.group;
-          const bool live = r < cnt;
-          uint32_t w[8], amax = 0;
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.Q) +
-                                                            ((row0 + (live ? tok : 0)) * p.Hq + head) * HD + 16 * i);
-          const uint4 a = live ? __ldg(src) : make_uint4(0, 0, 0, 0), b = live ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
-          w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-          float nl = -INFINITY;  // a row without a key, or none at all, adds nothing
-          if (live && i == 0) {
-            const float lse = __ldg(p.LSE + (int64_t)head * p.r.T + row0 + tok);
-            nl = lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
+        constexpr int RB = 4, RS = 256 / PER;  // rows in flight per thread, rows per pass
+        const int i = tid % PER;
+        for (int rb = tid / PER; rb < N; rb += RB * RS) {
+          uint4 x[RB], y[RB];
+          float lse[RB];
+#pragma unroll
+          for (int k = 0; k < RB; ++k) {
+            const int r = rb + k * RS, fr = r0 + r, tok = fr / p.sp.group, head = h * p.sp.group + fr - tok * p.sp.group;
+            const bool live = r < cnt;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.Q) +
+                                                              ((row0 + (live ? tok : 0)) * p.Hq + head) * HD + 16 * i);
+            x[k] = live ? __ldg(src) : make_uint4(0, 0, 0, 0);
+            y[k] = live ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+            lse[k] = live && i == 0 ? __ldg(p.LSE + (int64_t)head * p.r.T + row0 + tok) : -INFINITY;
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          for (int k = 0; k < RB; ++k) {
+            const int r = rb + k * RS;
+            if (r >= N) break;  // (N and RS are such that a warp's lanes agree)
+            const uint32_t w[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
+            // a row without a key, or none at all, adds nothing
+            const float nl = lse[k] == -INFINITY ? -INFINITY : lse[k] * -1.4426950408889634f;
+            uint32_t amax = 0;
 #pragma unroll
-          for (int o = PER / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          float inv;
-          const float f = row_factor(amax, inv);
-          uint32_t hi[4], lo[4];
-          split_e4m3(w, f, hi, lo);
-          const uint32_t at = base + LY::kQ + e4m3_chunk<HD>(r, i);
-          st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(at + LY::kPart, lo[0], lo[1], lo[2], lo[3]);
-          if (i == 0) {
-            float* rp = reinterpret_cast<float*>(bp + LY::kRow) + (r >> 1) * 4 + (r & 1);
-            rp[0] = p.sl2 * inv;
-            rp[2] = nl;
+            for (int q = 0; q < 8; ++q) amax = __vmaxu2(amax, w[q] & 0x7fff7fffu);
+            amax = max(amax & 0xffffu, amax >> 16);
+#pragma unroll
+            for (int o = PER / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            float inv;
+            const float f = row_factor(amax, inv);
+            uint32_t hi[4], lo[4];
+            split_e4m3(w, f, hi, lo);
+            const uint32_t at = base + LY::kQ + e4m3_chunk<HD>(r, i);
+            st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(at + LY::kPart, lo[0], lo[1], lo[2], lo[3]);
+            if (i == 0) {
+              float* rp = reinterpret_cast<float*>(bp + LY::kRow) + (r >> 1) * 4 + (r & 1);
+              rp[0] = p.sl2 * inv;
+              rp[2] = nl;
+            }
           }
         }
         fence_proxy_async_smem();

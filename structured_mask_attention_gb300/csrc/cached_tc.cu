@@ -694,35 +694,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dst = base + LY::kQ + (KS ? 0 : t) * LY::kQBytes;
         constexpr int PER = HD / 16;
         const int i = tid % PER;
-        constexpr int RB = KS ? 2 : 4, RS = kTeam / PER;  // rows in flight per thread, rows per pass
-#pragma unroll 1
-        for (int rb = tid / PER; rb < 128; rb += RB * RS) {
-          uint4 x[RB], y[RB];
+#pragma unroll 2
+        for (int r = tid / PER; r < 128; r += kTeam / PER) {
+          bool live;
+          const uint4* src = reinterpret_cast<const uint4*>(row_of(r, live)) + 2 * i;
+          const uint4 x = live ? __ldg(src) : make_uint4(0, 0, 0, 0), y = live ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          uint32_t amax = 0, hi[4], lo[4];
 #pragma unroll
-          for (int k = 0; k < RB; ++k) {
-            bool live;
-            const uint4* src = reinterpret_cast<const uint4*>(row_of(rb + k * RS, live)) + 2 * i;
-            x[k] = live ? __ldg(src) : make_uint4(0, 0, 0, 0);
-            y[k] = live ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
-          }
+          for (int k = 0; k < 8; ++k) amax = __vmaxu2(amax, w[k] & 0x7fff7fffu);
+          amax = max(amax & 0xffffu, amax >> 16);
 #pragma unroll
-          for (int k = 0; k < RB; ++k) {
-            const int r = rb + k * RS;
-            const uint32_t w[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
-            uint32_t amax = 0, hi[4], lo[4];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) amax = __vmaxu2(amax, w[q] & 0x7fff7fffu);
-            amax = max(amax & 0xffffu, amax >> 16);
-#pragma unroll
-            for (int o = PER / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            float inv;
-            const float f = row_factor(amax, inv);
-            split_e4m3(w, f, hi, lo);
-            const uint32_t at = dst + e4m3_chunk<HD>(r, i);
-            st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(at + 128 * HD, lo[0], lo[1], lo[2], lo[3]);
-            if (i == 0) row_cq[(KS ? 0 : t * 128) + r] = p.sl2 * inv;
-          }
+          for (int o = PER / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float inv;
+          const float f = row_factor(amax, inv);
+          split_e4m3(w, f, hi, lo);
+          const uint32_t at = dst + e4m3_chunk<HD>(r, i);
+          st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(at + 128 * HD, lo[0], lo[1], lo[2], lo[3]);
+          if (i == 0) row_cq[(KS ? 0 : t * 128) + r] = p.sl2 * inv;
         }
       };
       auto put_q16 = [&]() {

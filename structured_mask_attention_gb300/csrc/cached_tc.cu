@@ -417,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(BAR(B_PCF + n % NP));
           if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
         }
-        if (bad) atomicOr(p.status, bad);
       }
+      if (bad) atomicOr(p.status, bad);  // (each lane has looked at other sequences)
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issue
       if (lane == 0) {

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ch = 0; ok && ch < chunks; ++ch) {
         const int raw0 = lookup(0);
         int raw1 = lookup(1);
-      int id = checked(raw0, 0);
+        int id = checked(raw0, 0);
         float sc = scale_of(id);
         for (int b = 0; ok && 4 * b < n; ++b) {
           const int id1 = checked(raw1, b + 1);
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(BAR(B_PCF + n % NP));
         if (q.n < 0) break;
       }
-      if (bad) atomicOr(p.status, bad);
     }
+    if (bad) atomicOr(p.status, bad);  // (each lane has looked at other sequences)
   } else if (warp >= 4) {
     // ---------------------------------------------- queries, then a key per thread
     const int t = (warp - 4) >> 2, tid = threadIdx.x - 128;

@@ -340,6 +340,31 @@ def test_contents_out_of_range_are_left_out_and_reported(lib, rows):
         m.bdlm_sync_status(ws)
 
 
+@pytest.mark.parametrize("what", ["len", "rows"])
+@pytest.mark.parametrize("rows", [1, 20, 48, 150])
+@pytest.mark.parametrize("n,at", [(3, 2), (40, 0), (40, 37)])
+def test_whichever_sequence_is_out_of_range_is_reported(lib, what, rows, n, at):
+    m = lib
+    c, _ = make_cache([40] * n, 48, 1, 64, 16, seed=53)
+    dQ, dK = (to_dev(make_rows(n * rows, H, 64, H), torch) for H in (2, 1))
+    for name in ("attn", "weights", "append"):
+        cache = device_cache(m, torch, c)
+        ws, o = m.bdlm_cache_workspace(cache, 2, rows), torch.from_numpy(offsets_of([rows] * n)).cuda()
+        if what == "len":
+            cache.lens[at] = 1000
+        else:
+            o[at + 1] = n * rows + 5
+        if name == "attn":
+            m.bdlm_attn_cached(dQ, None, None, cache, o, rows, workspace=ws)
+        elif name == "weights":
+            m.bdlm_cache_weights(dQ, torch.zeros((2, n * rows), device="cuda"), cache,
+                                 torch.zeros((n, 1, 48), device="cuda"), o, rows, workspace=ws)
+        else:
+            m.bdlm_cache_append(cache, dK, dK, o, rows, workspace=ws)
+        with pytest.raises(m.BdlmError, match="length|row offsets"):
+            m.bdlm_sync_status(ws)
+
+
 # ------------------------------------------------------------ as they are used
 def decode(m, c, dst, blocks, B, Hq, Hkv, d, keep, step):
     """Blocks of B tokens, one after the other: attend, append, weigh; then evict."""

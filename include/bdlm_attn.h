@@ -430,6 +430,7 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
  * LSE [Hq, rows] fp32.  A row without a key gets O = 0, LSE = -inf.  For a
  * bf16 output the probabilities are rounded to 16 bits; for an fp32 one they
  * enter the product with V in several 16-bit parts (off by 2^-22 at most).
+ * O must not overlap Qn, Kn or Vn.
  * Deterministic: the keys are split over the GPU by their number, and the
  * parts are joined in a fixed order. */
 bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, const bdlm_cache* cache,
@@ -440,7 +441,8 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
  * that each cached token received from the rows of its sequence,
  *   weights[s, h, j] += sum_{i in rows of s} sum_{heads of h's group} exp(s_ij - LSE_i),
  * with the LSE of bdlm_attn_cached on the same rows.  Rows whose LSE is -inf
- * add nothing.  Deterministic. */
+ * add nothing.  Deterministic.  max_rows * Hq / Hkv by max_pages * page, both in
+ * tiles of 128, may be at most 2^30. */
 bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cache* cache, const int32_t* row_offsets,
                                int64_t rows, int64_t max_rows, int Hq, float scale, float* weights, void* workspace,
                                size_t ws_bytes, bdlm_stream stream);

@@ -624,7 +624,7 @@ def _cache_rows(cache, row_offsets, max_rows, T):
             max_rows = T // cache.n_seqs
         return None, max_rows
     _check_tensor("row_offsets", row_offsets, _torch().int32, (cache.n_seqs + 1,), cache.device)
-    return row_offsets.data_ptr(), T if max_rows is None else max_rows
+    return row_offsets.data_ptr(), max(T, 1) if max_rows is None else max_rows
 
 
 def _cache_call(fn, cache, stream, args, tensors=()):

@@ -93,6 +93,13 @@ bdlm_status check_heads(const CacheDesc& c, const RowsDesc& r, int Hq, float sca
   return BDLM_OK;
 }
 
+// An output must not share memory with an input that other CTAs still read.
+bdlm_status check_apart(const char* out, const void* a, int64_t na, const char* in, const void* b, int64_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  if (x && y && x < y + nb && y < x + na) return abi_fail(BDLM_ERR_INVALID_ARG, "%s overlaps %s", out, in);
+  return BDLM_OK;
+}
+
 bdlm_status check_space(void* ws, size_t bytes, size_t need) {
   if (!ws) return abi_fail(BDLM_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
   CACHE_CHECK(check_ptr("workspace", ws, 16));
@@ -192,6 +199,11 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     }
     CACHE_CHECK(check_ptr("O", O, 16));
     CACHE_CHECK(check_ptr("LSE", LSE, 4));
+    const int64_t nq = rows * Hq * p.c.d, nkv = rows * p.c.Hkv * p.c.d, no = nq * (o_dtype == BDLM_F32 ? 4 : 2);
+    CACHE_CHECK(check_apart("O", O, no, "Qn", Qn, 2 * nq));
+    CACHE_CHECK(check_apart("O", O, no, "Kn", Kn, 2 * nkv));
+    CACHE_CHECK(check_apart("O", O, no, "Vn", Vn, 2 * nkv));
+    CACHE_CHECK(check_apart("LSE", LSE, 4 * rows * Hq, "O", O, no));
     const int64_t flat = max_rows * (Hq / p.c.Hkv);
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(flat, p.c.d)));
     int sms;
@@ -258,6 +270,11 @@ bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cach
     CACHE_CHECK(check_ptr("LSE", LSE, 4));
     CACHE_CHECK(check_ptr("weights", weights, 16));
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
+    // a sequence's units are counted in 32 bits
+    const int64_t tiles = (max_rows * (Hq / p.c.Hkv) + 127) / 128, units = ((int64_t)p.c.max_pages * p.c.page + 127) / 128;
+    if (tiles * units > (int64_t)1 << 30)
+      return abi_fail(BDLM_ERR_SHAPE, "%lld row tiles by %lld key tiles of 128 exceed 2^30", (long long)tiles,
+                      (long long)units);
     int sms;
     CACHE_CHECK(abi_device(&sms));
     p.Q = Qn;

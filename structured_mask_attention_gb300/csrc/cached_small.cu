@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
       };
       auto scale_of = [&](const float* sc, int id) { return id >= 0 ? __ldg(sc + (int64_t)id * c.Hkv + h) : 1.f; };
       const int raw0 = lookup(0);
-        int raw1 = lookup(1);
+      int raw1 = lookup(1);
       int id = checked(raw0, 0);
       float sk = scale_of(c.ks, id), sv = scale_of(c.vs, id);
       for (int b = 0; ok && 4 * b < n; ++b) {
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           si.iv[x] = 1.f / sv;
           if (x == 0) si.gone = (int)((none >> lane) & 0xffu);
         }
+        __syncwarp();  // (before the arrivals that tell of them)
         const uint32_t bytes = (uint32_t)__popc(~(none >> (lane & 24)) & page_groups) * page_bytes;
         const bool loads = id >= 0 && ((page_groups >> x) & 1);
         const int blk = (int)((int64_t)id * c.Hkv + h);

@@ -55,6 +55,22 @@ def test_attn_is_checked(lib, kw, status):
     assert _attn(lib, **kw) == status, m.bdlm_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(O=0x400000), dict(O=0x400000 - 2048 + 16), dict(O=0x500000), dict(O=0x600000 + 512),
+                                dict(LSE=0x700000), dict(O=0x400000 - 4096 + 16, dt=1)])
+def test_attn_outputs_lie_apart(lib, kw):
+    """4 rows of 4 heads (K, V: 2) of 64: 2048 (1024) bytes, an fp32 O 4096."""
+    assert _attn(lib, **kw) == 1 and "overlaps" in m.bdlm_last_error(), m.bdlm_last_error()
+
+
+def test_weights_units_fit_32_bits(lib):
+    c = _cache(max_pages=1 << 26, page=16, Hkv=1)     # 2^23 key tiles
+    call = lambda Hq: lib.bdlm_cache_weights(0x400000, 0x500000, ctypes.cast(ctypes.pointer(c), ctypes.c_void_p),
+                                             0x340000, 4, 1 << 14, Hq, 0.125, 0x700000, 0x900000, 256, None)
+    assert call(2) == 2 and "2^30" in m.bdlm_last_error()  # by 2^8 row tiles: 2^31
+    if not torch.cuda.is_available():
+        assert call(1) in (5, 6)                           # 2^30 pass (and there is no device)
+
+
 def test_no_rows_is_no_work(lib):
     assert _attn(lib, off=0x340000, rows=0, Q=None, K=None, V=None) == 0
 

@@ -147,6 +147,70 @@ def test_attn_nan_scale_poisons_the_rows_that_see_it_only(lib, rows):
     assert torch.isnan(O[:rows]).all() and torch.isfinite(O[rows:]).all() and torch.isfinite(LSE[:, rows:]).all()
 
 
+@pytest.mark.parametrize("rows", [[1, 1, 1], [7, 3, 9], [40, 3, 70], [130, 200, 5]])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_attn_other_rows_stay_out(lib, rows, value):
+    """Whatever the rows of another sequence, or those behind the last one,
+    hold: a sequence's result does not know of them."""
+    m = lib
+    d, Hq, Hkv = 64, 4, 2
+    c, _ = make_cache([150, 20, 0], 150, Hkv, d, 16, seed=sum(rows))
+    off, T = offsets_of(rows), sum(rows) + 9
+    Q, K, V = (make_rows(T, H, d, 1 + i) for i, H in enumerate((Hq, Hkv, Hkv)))
+    ref = co.attn(c, Q[:T - 9], K[:T - 9], V[:T - 9], off, 0.125)
+    mine = np.r_[0:off[1], off[2]:off[3]]
+    for x in (Q, K, V):
+        x[off[1]:off[2]] = value
+        x[off[3]:] = value
+    cache = device_cache(m, torch, c)
+    O, LSE = m.bdlm_attn_cached(*(to_dev(x, torch) for x in (Q, K, V)), cache, torch.from_numpy(off).cuda(), max(rows),
+                                o_dtype=torch.float32)
+    check_attn(O[mine], LSE[:, mine], (ref[0][mine], ref[1][:, mine], ref[2][mine], ref[3][:, mine]), d, False)
+    W = torch.zeros((3, Hkv, c["table"].shape[1] * 16), device="cuda")
+    m.bdlm_cache_weights(to_dev(Q, torch), LSE, cache, W, torch.from_numpy(off).cuda(), max(rows))
+    assert torch.isfinite(W[0]).all() and (W[2] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [2, 30, 70, 140])
+def test_attn_query_row_that_is_not_finite(lib, rows):
+    m = lib
+    c, _ = make_cache([200], 200, 1, 128, 32, seed=29)
+    Q = make_rows(rows, 2, 128, 1)
+    ref = co.attn(c, Q, None, None, offsets_of([rows]), 0.125)
+    Q[1, 0, 5], Q[1, 1, 9] = math.inf, math.nan
+    O, LSE = m.bdlm_attn_cached(to_dev(Q, torch), None, None, device_cache(m, torch, c), scale=0.125,
+                                o_dtype=torch.float32)
+    mine = np.r_[0:1, 2:rows]
+    assert torch.isnan(O[1]).all()
+    check_attn(O[mine], LSE[:, mine], (ref[0][mine], ref[1][:, mine], ref[2][mine], ref[3][:, mine]), 128, False)
+
+
+@pytest.mark.parametrize("rows", [[90, 60], [400, 300]])
+@pytest.mark.parametrize("page,d", [(16, 128), (128, 64), (32, 128)])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+def test_attn_tiles_by_page(lib, rows, page, d, o_dtype):
+    run_attn(lib, [777, 1290], rows, 2, 1, d, page, o_dtype=o_dtype, seed=page + d, extra=1)
+
+
+@pytest.mark.parametrize("rows", [40, 150])
+def test_attn_blocks_of_many_sequences(lib, rows):
+    run_attn(lib, [(53 * i) % 300 for i in range(40)], [rows - i % 3 for i in range(40)], 2, 1, 64, 32, seed=rows)
+
+
+def test_no_rows_at_all(lib):
+    m = lib
+    c, _ = make_cache([20, 3], 32, 1, 64, 16, seed=37)
+    cache, off = device_cache(m, torch, c), torch.zeros(3, dtype=torch.int32, device="cuda")
+    Q, K = to_dev(make_rows(0, 2, 64, 1), torch), to_dev(make_rows(0, 1, 64, 1), torch)
+    O, LSE = m.bdlm_attn_cached(Q, K, K, cache, off)
+    assert O.shape == (0, 2, 64) and LSE.shape == (2, 0)
+    W = torch.ones((2, 1, 32), device="cuda")
+    m.bdlm_cache_weights(Q, LSE, cache, W, off)
+    assert (W == 1).all()
+    assert m.bdlm_cache_append(cache, K, K, off).tolist() == [20, 3]
+    same_cache(cache, c)
+
+
 def test_attn_repeats_bitwise(lib):
     m = lib
     c, _ = make_cache([3000, 17, 900], 3000, 2, 128, 64, seed=23)
@@ -293,6 +357,61 @@ def test_evict(lib, lens, keep, sinks, recent, page, d, kind):
     assert np.array_equal(lo.cpu().numpy(), rl)
     assert np.array_equal(wo.cpu().numpy(), rw, equal_nan=True)
     same_cache(cache, c)
+
+
+@pytest.mark.parametrize("lens,capacity,page,keep", [
+    ([30000, 9000], 33000, 64, 10000),       # clusters of CTAs
+    ([361000], 400000, 128, 200001),         # runs longer than a CTA holds
+    ([50] * 90, 64, 16, 20),                 # more selections than SMs
+])
+def test_evict_long_and_many(lib, lens, capacity, page, keep):
+    m = lib
+    c, (dst,) = make_cache(lens, capacity, 1, 64, page, seed=keep, sets=2)
+    cap = c["table"].shape[1] * page
+    W = np.random.default_rng(1).random((len(lens), 1, cap), dtype=np.float32) ** 8
+    W[:, :, ::5] = 0.25  # a tie around the cut
+    cache = device_cache(m, torch, c)
+    ws = m.bdlm_cache_workspace(cache)
+    lo, wo, kept = m.bdlm_cache_evict(cache, torch.from_numpy(W).cuda(), torch.from_numpy(dst).cuda(), keep, 3, 7,
+                                      workspace=ws)
+    m.bdlm_sync_status(ws)
+    rl, rw, rk = co.evict(c, W, dst, keep, 3, 7)
+    assert np.array_equal(kept.cpu().numpy(), rk) and lo.cpu().tolist() == rl.tolist()
+    assert np.array_equal(wo.cpu().numpy(), rw)
+    same_cache(cache, c)
+
+
+@pytest.mark.parametrize("rows", [1, 60])
+def test_weights_of_many_sequences(lib, rows):
+    m = lib
+    n = 45
+    c, _ = make_cache([(31 * i) % 280 for i in range(n)], 280, 2, 64, 16, seed=43)
+    off, T = offsets_of([rows] * n), n * rows
+    Q = make_rows(T, 4, 64, 3)
+    LSE = co.attn(c, Q, None, None, off, 0.125)[1].astype(np.float32)
+    W = torch.zeros((n, 2, c["table"].shape[1] * 16), device="cuda")
+    m.bdlm_cache_weights(to_dev(Q, torch), torch.from_numpy(LSE).cuda(), device_cache(m, torch, c), W)
+    ref, E = co.weights(c, Q, LSE, off, 0.125, np.zeros(W.shape, np.float32))
+    rel = score_error(64, E) + 2.0 ** -23 * (1 + np.abs(LSE[np.isfinite(LSE)]).max()) + (2 * rows + 4) * 2.0 ** -24
+    assert (np.abs(W.double().cpu().numpy() - ref) <= rel * ref + 2.0 ** -24).all()
+
+
+def test_two_streams_with_a_workspace_each(lib):
+    m = lib
+    c, _ = make_cache([5000, 30], 5000, 2, 64, 64, seed=87)
+    cache = device_cache(m, torch, c)
+    Qs = [to_dev(make_rows(2 * r, 8, 64, r), torch) for r in (1, 48)]
+    ref = [m.bdlm_attn_cached(q, None, None, cache) for q in Qs]
+    ws = [m.bdlm_cache_workspace(cache, 8, r) for r in (1, 48)]
+    out = [tuple(torch.empty_like(t) for t in r) for r in ref]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Qs]
+    for _ in range(20):
+        for q, w, o, st in zip(Qs, ws, out, streams):
+            m.bdlm_attn_cached(q, None, None, cache, out=o, workspace=w, stream=st)
+    torch.cuda.synchronize()
+    for o, r in zip(out, ref):
+        assert torch.equal(o[0], r[0]) and torch.equal(o[1], r[1])
 
 
 # -------------------------------------------------------- contents out of range

@@ -396,6 +396,46 @@ def test_weights_of_many_sequences(lib, rows):
     assert (np.abs(W.double().cpu().numpy() - ref) <= rel * ref + 2.0 ** -24).all()
 
 
+@pytest.mark.parametrize("rows", [1, 48, 150])
+def test_pool_past_32_bits(lib, rows):
+    """Pages at the end of a pool of 4.6 GB of codes: every call's offsets."""
+    m = lib
+    Hkv, d, page = 2, 128, 64
+    c, (dst,) = make_cache([300, 129], 700, Hkv, d, page, seed=91, sets=2)
+    n, n_pages = c["k8"].shape[0], 280_000
+    assert (n_pages - n) * Hkv * page * d > 2 ** 32 and n_pages * Hkv * page * d * 2 < 20e9
+    shift = n_pages - n
+    pool = [torch.empty((n_pages, Hkv, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    sc = [torch.empty((n_pages, Hkv), device="cuda") for _ in range(2)]
+    for w, p, s in zip("kv", pool, sc):
+        p[shift:] = torch.from_numpy(c[w + "8"]).cuda()
+        s[shift:] = torch.from_numpy(c[w + "s"]).cuda()
+    dev = lambda t: torch.from_numpy(t + np.int32(shift)).cuda()
+    cache = m.BdlmCache(*(p.view(torch.float8_e4m3fn) for p in pool), *sc, dev(c["table"]),
+                        torch.from_numpy(c["lens"]).cuda())
+    off = offsets_of([rows, rows])
+    Q, K, V = (make_rows(2 * rows, H, d, 1 + i) for i, H in enumerate((4, Hkv, Hkv)))
+    dq, dk, dv = (to_dev(x, torch) for x in (Q, K, V))
+    ws = m.bdlm_cache_workspace(cache, 4, rows, 200)
+    O, LSE = m.bdlm_attn_cached(dq, dk, dv, cache, workspace=ws)
+    check_attn(O, LSE, co.attn(c, Q, K, V, off, 1 / math.sqrt(d)), d, True)
+    W = torch.zeros((2, Hkv, c["table"].shape[1] * page), device="cuda")
+    m.bdlm_cache_weights(dq, LSE, cache, W, workspace=ws)
+    ref, E = co.weights(c, Q, LSE.cpu().numpy(), off, 1 / math.sqrt(d), np.zeros(W.shape, np.float32))
+    rel = score_error(d, E) + 2.0 ** -23 * (1 + LSE.abs().max().item()) + (2 * rows + 4) * 2.0 ** -24
+    assert (np.abs(W.double().cpu().numpy() - ref) <= rel * ref + 2.0 ** -24).all()
+    cache.lens.copy_(m.bdlm_cache_append(cache, dk, dv, workspace=ws))
+    c["lens"] = co.append(c, K, V, off)
+    lo, wo, kept = m.bdlm_cache_evict(cache, W, dev(dst), 200, 4, 8, workspace=ws)
+    m.bdlm_sync_status(ws)
+    rl, rw, rk = co.evict(c, W.cpu().numpy(), dst, 200, 4, 8)
+    assert np.array_equal(kept.cpu().numpy(), rk) and lo.cpu().tolist() == rl.tolist()
+    assert np.array_equal(wo.cpu().numpy(), rw)
+    for w, p, s in zip("kv", pool, sc):
+        assert np.array_equal(p[shift:].cpu().numpy(), c[w + "8"])
+        assert np.array_equal(s[shift:].cpu().numpy(), c[w + "s"], equal_nan=True)
+
+
 def test_two_streams_with_a_workspace_each(lib):
     m = lib
     c, _ = make_cache([5000, 30], 5000, 2, 64, 64, seed=87)

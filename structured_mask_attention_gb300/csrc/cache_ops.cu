@@ -36,6 +36,18 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float* f) {
   f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
 }
 
+// Four codes times r, rounded to codes again (r: a power of two, nothing above 448 comes out).
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, __half2 r) {
+  uint32_t q[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const uint32_t h = e4m3x2_to_half2(w >> (16 * y));
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h), r);
+    q[y] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+  }
+  return q[0] | q[1] << 16;
+}
+
 // ------------------------------------------------------------------ append
 // A CTA takes TT = max(page, 64) slots of one (sequence, KV head), K and V: 16
 // values per thread and step (two 16-byte loads, HD / 16 lanes to a token),
@@ -403,17 +415,21 @@ __global__ void __launch_bounds__(kMoveThreads) bdlm_evict_move_kernel(const Evi
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int kv = i >= NT / 2, tok = ((i % (NT / 2)) * kMoveThreads + tid) / CH;
-    const uint32_t m4 = __vmaxu4(__vmaxu4(x[i].x & 0x7f7f7f7fu, x[i].y & 0x7f7f7f7fu),
-                                 __vmaxu4(x[i].z & 0x7f7f7f7fu, x[i].w & 0x7f7f7f7fu));
-    uint32_t top = 0;
+    // the largest of 16 magnitudes, two bytes at a time: of a 16-bit maximum the
+    // high byte is the high bytes' maximum
+    uint32_t hb = 0, lb = 0;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) top = umax2(top, (m4 >> (8 * b)) & 0xffu);
+    for (int y = 0; y < 4; ++y) {
+      const uint32_t w = (y == 0 ? x[i].x : y == 1 ? x[i].y : y == 2 ? x[i].z : x[i].w) & 0x7f7f7f7fu;
+      hb = __vmaxu2(hb, w);
+      lb = __vmaxu2(lb, w << 8);
+    }
+    const uint32_t m2 = __vmaxu2(hb, lb), top = umax2(m2 >> 24, (m2 >> 8) & 0xffu);
     const uint32_t hv = e4m3x2_to_half2(top);
     const float val = __half22float2(*reinterpret_cast<const __half2*>(&hv)).x * s_scale[kv][tok];
     uint32_t bits = s_row[tok] >= 0 ? __float_as_uint(val) & 0x7fffffffu : 0u;
     // a warp's rows belong to one destination page
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) bits = umax2(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+    bits = __reduce_max_sync(0xffffffffu, bits);
     if ((tid & 31) == 0) atomicMax(&s_amax[kv][tok >> c.lp], bits);
   }
   __syncthreads();
@@ -425,20 +441,26 @@ __global__ void __launch_bounds__(kMoveThreads) bdlm_evict_move_kernel(const Evi
     const float ns = block_scale(s_amax[kv][j]), sc = s_scale[kv][tok];
     uint4 o = x[i];
     if (sc != ns) {
-      const bool pow2 = is_pow2(ns);
-      const float inv = pow2 ? __uint_as_float(0x7f000000u - __float_as_uint(ns)) : 0.f;
-      float f[8];
-      e4m3x4_to_float(x[i].x, f);
-      e4m3x4_to_float(x[i].y, f + 4);
+      const uint32_t ratio = __float_as_uint(sc) - __float_as_uint(ns) + 0x3f800000u;  // of two powers of two
+      if (is_pow2(sc) && is_pow2(ns) && (int)ratio <= 0x47000000) {
+        // times 2^j, j <= 15, in halves: exact from 2^-14 on, and what is smaller rounds to the code 0 either way
+        const __half2 r = __float2half2_rn((int)ratio > 0x33000000 ? __uint_as_float(ratio) : 0.f);
+        o = make_uint4(rescale4(x[i].x, r), rescale4(x[i].y, r), rescale4(x[i].z, r), rescale4(x[i].w, r));
+      } else {
+        const bool pow2 = is_pow2(ns);
+        const float inv = pow2 ? __uint_as_float(0x7f000000u - __float_as_uint(ns)) : 0.f;
+        uint2 q[2];
 #pragma unroll
-      for (int y = 0; y < 8; ++y) f[y] *= sc;
-      const uint2 lo = quantise8(f, ns, inv, pow2);
-      e4m3x4_to_float(x[i].z, f);
-      e4m3x4_to_float(x[i].w, f + 4);
+        for (int z = 0; z < 2; ++z) {
+          float f[8];
+          e4m3x4_to_float(z ? x[i].z : x[i].x, f);
+          e4m3x4_to_float(z ? x[i].w : x[i].y, f + 4);
 #pragma unroll
-      for (int y = 0; y < 8; ++y) f[y] *= sc;
-      const uint2 hi = quantise8(f, ns, inv, pow2);
-      o = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          for (int y = 0; y < 8; ++y) f[y] *= sc;
+          q[z] = quantise8(f, ns, inv, pow2);
+        }
+        o = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+      }
     }
     const int64_t blk = (int64_t)id * c.Hkv + h;
     *(reinterpret_cast<uint4*>((kv ? c.v8 : c.k8) + (blk * c.page + (tok & (c.page - 1))) * HD) + k % CH) = o;

@@ -226,41 +226,56 @@ __global__ void __launch_bounds__(kSelThreads, 1) bdlm_evict_select_kernel(const
   const CacheDesc& c = p.c;
   const int s = blockIdx.y, h = blockIdx.x / C, tid = threadIdx.x;
   uint32_t bad = 0;
+  launch_dependents();
   const SeqView v = seq_view(c, RowsDesc{nullptr, 0, 0}, s, bad);
   const int64_t cap = (int64_t)c.max_pages << c.lp;
   const float* w = p.W + ((int64_t)s * c.Hkv + h) * cap;
   float* wo = p.W_out + ((int64_t)s * c.Hkv + h) * cap;
   int32_t* kept = p.kept + ((int64_t)s * c.Hkv + h) * p.keep;
   const int len = v.len, left = len < p.keep ? len : p.keep;
-  // this CTA's positions
-  const int run = (len + C - 1) / C, b0 = min(rank * run, len), n = min(run, len - b0);
-  auto weigh = [&](int i) {  // i: position in the run
-    const int at = b0 + i;
-    return at < p.sinks || at >= len - p.recent ? 0xffffffffu : rank_key(w[at]);
+  // this CTA's positions (runs of fours: the row of weights has a multiple of 16)
+  const int run = ((len + C - 1) / C + 3) & ~3, b0 = min(rank * run, len), n = min(run, len - b0);
+  const int top_sink = p.sinks - b0, first_recent = len - p.recent - b0;  // (as places in the run)
+  auto weigh4 = [&](int i, float4 x) {  // keys of the run's places i .. i + 3
+    uint4 k = make_uint4(rank_key(x.x), rank_key(x.y), rank_key(x.z), rank_key(x.w));
+    if (i < top_sink || i + 3 >= first_recent) {
+      if (i < top_sink || i >= first_recent) k.x = 0xffffffffu;
+      if (i + 1 < top_sink || i + 1 >= first_recent) k.y = 0xffffffffu;
+      if (i + 2 < top_sink || i + 2 >= first_recent) k.z = 0xffffffffu;
+      if (i + 3 < top_sink || i + 3 >= first_recent) k.w = 0xffffffffu;
+    }
+    return k;
   };
-  for (int i = tid; i < min(n, held); i += 8 * kSelThreads) {  // (eight loads in flight)
-    uint32_t k[8];
+  auto load4 = [&](int i) { return i < n ? *reinterpret_cast<const float4*>(w + b0 + i) : make_float4(0.f, 0.f, 0.f, 0.f); };
+  constexpr int kRound = 4 * kSelThreads;
+  const int here = min(n, held);
+  for (int i = 4 * tid; i < here; i += 4 * kRound) {  // (four loads in flight)
+    float4 x[4];
 #pragma unroll
-    for (int y = 0; y < 8; ++y) k[y] = i + y * kSelThreads < n ? weigh(i + y * kSelThreads) : 0u;
+    for (int y = 0; y < 4; ++y) x[y] = load4(i + y * kRound);
 #pragma unroll
-    for (int y = 0; y < 8; ++y)
-      if (i + y * kSelThreads < min(n, held)) keys[i + y * kSelThreads] = k[y];
+    for (int y = 0; y < 4; ++y)
+      if (i + y * kRound < here) *reinterpret_cast<uint4*>(keys + i + y * kRound) = weigh4(i + y * kRound, x[y]);
   }
-  auto key_of = [&](int i) { return i < held ? keys[i] : weigh(i); };
+  auto keys_of = [&](int i) { return i < held ? *reinterpret_cast<const uint4*>(keys + i) : weigh4(i, load4(i)); };
   for (int i = tid; i < kSelHist; i += kSelThreads) hist[i] = 0;
   __syncthreads();
   uint32_t thr = 0, mask = 0;
   int need = left;  // tokens still to take among those that match thr under mask
-  if (left < len) {
+  const bool cut = left < len;
+  if (cut) {
     for (int pass = 0; pass < 3; ++pass) {
       const int sh = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, bins = 1 << bits;
       // the first pass counts every key, most of them in a few digits: its
       // warps share out kSelCopies - 1 histograms (the last copy is pass 1's)
       uint32_t* mine = hist + (pass == 1 ? kSelCopies - 1 : 0) * kSelBins;
       uint32_t* count = pass == 0 ? hist + ((tid >> 5) % (kSelCopies - 1)) * kSelBins : mine;
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t k = key_of(i);
-        if ((k & mask) == thr) atomicAdd(&count[(k >> sh) & (bins - 1)], 1u);
+      for (int i = 4 * tid; i < n; i += kRound) {
+        const uint4 k4 = keys_of(i);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if ((k[y] & mask) == thr && i + y < n) atomicAdd(&count[(k[y] >> sh) & (bins - 1)], 1u);
       }
       if (pass == 0) {
         __syncthreads();
@@ -269,14 +284,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) bdlm_evict_select_kernel(const
       }
       cl.sync();
       // two bins per thread, digits from the top: the one where the count reaches need
+      // (all CTAs' counts asked for together, each CTA beginning with its own)
       const int top = bins - 1 - 2 * tid;
       int n0 = 0, n1 = 0;
-      if (top > 0)
-        for (int r = 0; r < C; ++r) {
-          const uint2 x = *reinterpret_cast<const uint2*>(cl.map_shared_rank(mine, r) + top - 1);
-          n0 += (int)x.y;
-          n1 += (int)x.x;
+      if (top > 0) {
+        uint2 x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          x[r] = r < C ? *reinterpret_cast<const uint2*>(cl.map_shared_rank(mine, (rank + r) & (C - 1)) + top - 1)
+                       : make_uint2(0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          n0 += (int)x[r].y;
+          n1 += (int)x[r].x;
         }
+      }
       int total;
       const int above = block_scan(n0 + n1, red, &total);
       if (above < need && above + n0 >= need) {
@@ -296,58 +318,82 @@ __global__ void __launch_bounds__(kSelThreads, 1) bdlm_evict_select_kernel(const
       __syncthreads();
     }
   }
-  // kept tokens in order of position: a warp takes a run of positions, 32 at a time
+  // kept tokens in order of position: a warp takes a run of positions, 4 per
+  // lane at a time; a token's new slot is the number of larger keys before it
+  // plus that of equal ones, of which the first `need` are kept
   const int lane = tid & 31, warp = tid >> 5;
-  const unsigned below = (1u << lane) - 1;
-  const int per = ((n + kSelThreads - 1) / kSelThreads) * 32;
+  const int per = ((n + kRound - 1) / kRound) * 128;
   const int i0 = min(warp * per, n), i1 = min(i0 + per, n);
-  const bool cut = left < len;
-  int gt = 0, eq = 0;
-  if (cut)
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-      const uint32_t k = i < i1 ? key_of(i) : 0u;
-      gt += __popc(__ballot_sync(0xffffffffu, i < i1 && k > thr));
-      eq += __popc(__ballot_sync(0xffffffffu, i < i1 && k == thr));
+  auto sort4 = [&](int i, const uint4& k4, uint32_t& gt, uint32_t& eq) {  // a bit for each of 4 keys
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    gt = eq = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      if (i + y < i1 && (!cut || k[y] > thr)) gt |= 1u << y;
+      if (i + y < i1 && cut && k[y] == thr) eq |= 1u << y;
     }
-  else
-    gt = i1 - i0;
+  };
+  int gts = 0, eqs = 0;
+  for (int i = i0 + 4 * lane; i < i1; i += 128) {
+    uint32_t gt, eq;
+    sort4(i, keys_of(i), gt, eq);
+    gts += __popc(gt);
+    eqs += __popc(eq);
+  }
+  gts = __reduce_add_sync(0xffffffffu, gts);
+  eqs = __reduce_add_sync(0xffffffffu, eqs);
   int gt_all, eq_all;
-  int eq0 = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? eq : 0, red, &eq_all), 0);
-  int at = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? gt : 0, red, &gt_all), 0);
+  int eq0 = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? eqs : 0, red, &eq_all), 0);
+  int gt0 = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? gts : 0, red, &gt_all), 0);
   if (tid == 0) {
     s_count[0] = gt_all;
     s_count[1] = eq_all;
   }
   cl.sync();
-  // what the CTAs before this one keep: all above the key, and of those equal to it the first `need`
   for (int r = 0; r < rank; ++r) {
     const int* o = cl.map_shared_rank(s_count, r);
-    at += o[0];
+    gt0 += o[0];
     eq0 += o[1];
   }
-  if (cut) at += min(need, eq0);
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    bool take = i < i1;
-    const uint32_t k = take ? key_of(i) : 0u;
-    if (cut) {
-      const unsigned same = __ballot_sync(0xffffffffu, take && k == thr);
-      take = take && (k > thr || (k == thr && eq0 + __popc(same & below) < need));
-      eq0 += __popc(same);
+  cl.barrier_arrive();  // (done with the other CTAs' memory)
+  for (int ib = i0; ib < i1; ib += 128) {
+    const int i = ib + 4 * lane;
+    uint32_t gt = 0, eq = 0;
+    uint4 k4 = make_uint4(0, 0, 0, 0);
+    if (i < i1) {
+      k4 = keys_of(i);
+      sort4(i, k4, gt, eq);
     }
-    const unsigned taken = __ballot_sync(0xffffffffu, take);
-    if (take) {
-      const int o = at + __popc(taken & below);
-      kept[o] = b0 + i;
-      wo[o] = k >= 0xfffffffeu ? w[b0 + i] : rank_weight(k);
+    const uint32_t mine = (uint32_t)__popc(gt) | (uint32_t)__popc(eq) << 16;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t z = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += z;
     }
-    at += __popc(taken);
+    const uint32_t before = sum - mine, all = __shfl_sync(0xffffffffu, sum, 31);
+    int g = gt0 + (int)(before & 0xffffu), e = eq0 + (int)(before >> 16);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const bool is_eq = (eq >> y) & 1, take = ((gt >> y) & 1) || (is_eq && e < need);
+      if (take) {
+        const int o = g + min(e, need);
+        kept[o] = b0 + i + y;
+        wo[o] = k[y] >= 0xfffffffeu ? w[b0 + i + y] : rank_weight(k[y]);
+      }
+      g += (gt >> y) & 1;
+      e += is_eq;
+    }
+    gt0 += (int)(all & 0xffffu);
+    eq0 += (int)(all >> 16);
   }
   const int step = C * kSelThreads;
   for (int i = left + rank * kSelThreads + tid; i < p.keep; i += step) kept[i] = -1;
   for (int64_t i = left + rank * kSelThreads + tid; i < cap; i += step) wo[i] = 0.f;
   if (h == 0 && rank == 0 && tid == 0) p.lens_out[s] = left;
   if (bad && tid == 0) atomicOr(p.status, bad);
-  cl.sync();  // no CTA leaves while another may still read its counts
+  cl.barrier_wait();  // no CTA leaves while another may still read its counts
 }
 
 // Moves the kept tokens of TT = max(page, 64) destination slots, K and V: one
@@ -369,6 +415,8 @@ __global__ void __launch_bounds__(kMoveThreads) bdlm_evict_move_kernel(const Evi
   uint32_t bad = 0;
   const SeqView v = seq_view(c, RowsDesc{nullptr, 0, 0}, s, bad);
   const int left = v.len < p.keep ? v.len : p.keep;
+  // (the selection may still run; every thread waits for it, so that this grid's end implies its end)
+  dependency_wait();
   if (t0 >= left) return;
   float a = 0.f, b = 0.f;
   if (tid < TT) {
@@ -500,7 +548,7 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t st, int* launc
   int C = 1;
   while (C < 8 && (int64_t)C * kSelRun < cap) C *= 2;
   while (C < 8 && (int64_t)C * kSelRun / 8 < cap && (int64_t)p.c.n_seqs * p.c.Hkv * C * 2 <= 152) C *= 2;
-  const int64_t run = (cap + C - 1) / C;
+  const int64_t run = ((cap + C - 1) / C + 3) & ~(int64_t)3;
   const int held = (int)(run < kSelHeld ? run : kSelHeld);
   const int bytes = (kSelHist + held) * (int)sizeof(uint32_t);
   static std::atomic<uint64_t> raised{0};
@@ -526,9 +574,14 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t st, int* launc
   const dim3 grid((unsigned)((most + TT - 1) / TT), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
   auto move = p.c.d == 128 ? (TT == 128 ? bdlm_evict_move_kernel<128, 128> : bdlm_evict_move_kernel<128, 64>)
                            : (TT == 128 ? bdlm_evict_move_kernel<64, 128> : bdlm_evict_move_kernel<64, 64>);
-  move<<<grid, kMoveThreads, 0, st>>>(p);
-  ++*launches;
-  return cudaGetLastError();
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // may start before the selection's end
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  e = cudaLaunchKernelEx(&cfg, move, p);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 }  // namespace bdlm

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) bdlm_evict_select_kernel(const
 // (e4m3 magnitudes compare like integers, so the maximum needs no conversion).
 constexpr int kMoveThreads = 256;
 template <int HD, int TT>
-__global__ void __launch_bounds__(kMoveThreads) bdlm_evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads, TT == 128 ? 5 : 1) bdlm_evict_move_kernel(const EvictParams p) {
   constexpr int CH = HD / 16;                            // 16-byte chunks of a row
   constexpr int NT = 2 * TT * CH / kMoveThreads;         // chunks per thread, the first half K's
   __shared__ int64_t s_row[TT];                          // old row ((page, head) block * page + slot), -1: none

@@ -914,13 +914,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 32; ++x)
             o[x] = __float_as_uint(fmaf(__uint_as_float(o1[x]), s1, __uint_as_float(o[x])));
         }
+        if (!live) continue;  // (nobody reads a partial result's rows without a token)
         if (!whole) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             reinterpret_cast<float4*>(slot)[(col / 4 + x) * kTileRows + prow] =
                 make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
                             __uint_as_float(o[4 * x + 3]));
-        } else if (live) {
+        } else {
           if (p.o_f32) {
             float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.O) + oofs + col);
 #pragma unroll

@@ -223,7 +223,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     p.limit_ns = abi_wait_limit_ns();
     p.sp.tile_rows = cached_tile_rows(flat);
     const bool small = p.sp.tile_rows <= kSmallRows;
-    p.sp.extra = small ? kSmallExtra : kTcExtra;
+    p.sp.extra = !small ? kTcExtra : Kn ? kSmallExtraOwn : kSmallExtra;
     p.sp.keyed = 0;
     p.whole = 0;
     p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));

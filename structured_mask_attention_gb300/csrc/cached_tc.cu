@@ -35,6 +35,16 @@
 // convert V.  TMEM: S of sub-tile t at 128 t (P over it), O at 256 + 128 t.
 // The rows' own block (bf16 keys) follows the cached tiles of the last unit or
 // has units of its own; its Q is bf16, its V tile needs no conversion.
+//
+// What bounds it (16 / 8 heads of 128, merge included): a block of 512 over one
+// sequence of 131072 tokens takes 483 us, 1.14 PFLOP/s or 62 % of the measured
+// bf16 rate; a pair's tile period is about 4150 cycles against 2150 of its
+// products alone: the chain S -> softmax (2500) -> P V of each sub-tile, and the
+// issuing thread's waits in between.  Blocks of 128 over 4 sequences, 40 / 8
+// heads: 226 us, 0.76 PFLOP/s (three tiles of 256 for 640 rows: a sixth is
+// padding).  Blocks of 32 over 16 sequences of 8192 at most (split, 64 rows of
+// 128): 87 us, of which 30 are the 28 tiles of a CTA (1.1 us each) and the rest
+// begins and ends its two segments.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -10,8 +10,14 @@
 // threads together, the sum stays in two registers, and no two threads ever
 // add to the same weight (no atomics).  All rows of a (sequence, KV head) are
 // handled by the CTA that owns the key tile, 256 at a time.
-// Bound: for few rows the stream of K's codes; from about 128 rows on the
-// exponentials (one per row and key) and the products.
+// Bound: for few rows the stream of K's codes (32 sequences of 32768 tokens at
+// most, 32 / 8 heads of 128, one token each: 129 us for 0.69 GB, 5.3 TB/s or
+// 78 % of the measured copy rate); from about 128 rows on the exponentials (one per
+// row and key) and the products (blocks of 128 over 4 such sequences, 16 / 8
+// heads: 45 us, 0.76 PFLOP/s; the tensor pipe 31 %, the exponentials' 37 % busy, a
+// third of the time begins and ends the CTAs' two segments).  Not kept: both
+// parts' products side by side as 2 N columns, added by the threads (162 us
+// against 158 when it was tried).
 // Roles (12 warps): warp 0 loads K, one lane of warp 1 issues the MMAs, warp 3
 // walks the CTA's share of the list; warps 4-7 and 8-11 prepare the queries
 // together and then take alternate key tiles (256 TMEM columns each).

@@ -554,7 +554,9 @@ cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* lau
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t st, int* launches) {
   const int64_t cap = (int64_t)p.c.max_pages << p.c.lp;
   // a CTA for each kSelRun positions of the longest sequence, up to the portable
-  // cluster size; more, down to kSelRun / 8 positions, while the GPU has room
+  // cluster size; more, down to kSelRun / 8 positions, while the GPU has room.  One
+  // CTA against eight, 8 KV heads, the move included: 1 sequence of 131072 tokens
+  // 143 / 53 us, of 16384 23 / 21, 2 of 40000 49 / 47; 16 of 8192 43 / 166
   int C = 1;
   while (C < 8 && (int64_t)C * kSelRun < cap) C *= 2;
   while (C < 8 && (int64_t)C * kSelRun / 8 < cap && (int64_t)p.c.n_seqs * p.c.Hkv * C * 2 <= 152) C *= 2;

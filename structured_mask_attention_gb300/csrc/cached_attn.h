@@ -30,18 +30,18 @@ struct CachedParams {
 // side by side), then the rows' reference maxima (log2 units) and sums.
 __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (int64_t)tile_rows * (d + 2); }
 
-// Rows up to which the mma.sync kernel takes a call.  16 sequences of 16384
-// tokens with 20 / 32 rows: 111 / 116 us here, 130 / 130 in the tcgen05
-// kernel; 64 rows (16 sequences of 8192): 118 us here, 88 there.
+// Rows up to which the mma.sync kernel takes a call.  16 sequences of up to 16384
+// tokens with 20 / 32 rows: 107 / 107 us here, 129 / 129 in the tcgen05
+// kernel; 64 rows (16 sequences of up to 8192): 118 us here, 87 there.
 constexpr int kSmallRows = 32;
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
 
 // Row tile of a call whose sequences have at most `flat` rows times heads of
 // a group: 16 or 32 (mma.sync), 128 or 256 (tcgen05, split and pairs).  Split
-// serves any number of rows in tiles of 128; pairs read the keys half as often
-// but hold 256 rows: split against pairs 82 / 83 us at 128 rows, 106 / 111 at
-// 160, 92 / 84 at 256 (8 sequences of 8192), 174 / 177 at 384, 250 / 226 at 640,
-// 537 / 487 at 1024.
+// could serve any number of rows in tiles of 128; pairs read the keys half as
+// often but hold 256 rows.  Split against pairs: 106 / 111 us at 160 rows, 92 / 84
+// at 256 (8 sequences of up to 8192), 174 / 177 at 384, 250 / 226 at 640, 537 / 487
+// at 1024.
 inline int cached_tile_rows(int64_t flat) {
   return flat <= 16 ? 16 : flat <= kSmallRows ? 32 : flat <= 128 ? 128 : 256;
 }
@@ -54,13 +54,18 @@ struct CachedMaps {
 };
 cudaError_t launch_cached_tc(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 // Longest cache, in tokens, up to which the mma.sync kernel gives each segment
-// one CTA: no work list to walk and no merge kernel, whose launch alone is about
-// 4 us, against the four units of 128 keys, 0.7 us each, that it would share out.
+// one CTA, without a list to walk and a merge.  1 / 32 sequences of 8 KV heads:
+// whole against split 7.5 / 8.9 and 10.3 / 16.1 us at 256 tokens, 13.3 / 16.5 and
+// 13.8 / 20.8 at 1000, 21.4 / 27.9 and 19.8 / 29.1 at 2000.
 constexpr int kWholeKeys = 1024;
 // AttnSplit::extra: what a segment costs beside its units, in units.  The
-// tcgen05 kernels spend 16 to 20 thousand cycles to begin and end a segment and
-// 2060 (split) or 4150 (pairs) on a unit; with 0 / 6, blocks of 32 and 128 took
-// 130 / 106 and 293 / 248 us.
+// mma.sync kernel spends about 6000 cycles to begin and end a segment, 5000 more
+// on its own rows' keys and 2300 on a unit: with 1 / 3 / 5, the token batch of
+// cached_small.cu took 220 / 207 / 205 us with own keys and 205 / 204 / 206 without,
+// blocks of 8 over 16 short sequences 70 / 47 / 42 and 48 / 40 / 41.  The tcgen05
+// kernels spend 16 to 20 thousand cycles on a segment and 2060 (split) or 4150
+// (pairs) on a unit: with 0 / 6, blocks of 32 and 128 took 130 / 106 and 293 /
+// 248 us; 4 to 12 are level.
 constexpr int kSmallExtra = 3, kSmallExtraOwn = 5, kTcExtra = 6;
 
 cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);

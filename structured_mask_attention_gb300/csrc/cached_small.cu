@@ -1,14 +1,20 @@
-// cached_small.cu -- attention of up to 64 rows over the 8-bit cache on mma.sync
+// cached_small.cu -- attention of up to 32 rows over the 8-bit cache on mma.sync
 // tiles, and the merge of partial results.
 //
 // One token of a sequence, or a short block, gives Hq / Hkv rows per token and
 // KV head, a handful against thousands of keys: the stream of codes bounds the
 // call, and a tcgen05 tile of 128 rows would be mostly padding.  A CTA of four
-// warps takes 16, 32 or 64 rows (MT 16-row tiles); its warps are MT row tiles by
+// warps takes 16 or 32 rows (MT 16-row tiles); its warps are MT row tiles by
 // 4 / MT groups of keys.  A fifth warp keeps a ring of K and V tiles of 128 keys
 // filled by TMA, codes as they lie, so that 128 KB per SM (two CTAs) are in flight
 // whatever the warps do; they turn codes into fp16 on the way from shared
 // memory to the MMA.
+// Bound by HBM: 32 sequences of up to 32768 tokens (1.30 GB of codes), a token
+// each, 32 / 8 heads of 128, take 209 us with the merge: 6.2 TB/s, 92 % of the
+// measured copy rate.  (With loads issued by the computing warps themselves it
+// was 334 us.)  S from two e4m3 parts of Q by e4m3 m16n8k32 instead, without
+// K's conversion: 259 us against 227 when it was tried.  One sequence of 256
+// tokens: 7.5 us, less than the call takes on the host.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -614,6 +620,9 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
 // 2 c' of the CTAs c' that continue it, and are joined in that order.  A
 // block takes 16 of the tile's rows; neighbouring threads read neighbouring
 // rows (the partials' layout), and the rows leave through shared memory.
+// Bound by latency: it is launched under the attention kernel's tail and takes
+// 9 to 17 us alone with nothing in L2 (15 us for 22 MB of partials of 256-row
+// tiles), where they are as a rule.
 constexpr int kMergeThreads = 128, kMergeRows = 16;
 template <int HD>
 __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const CachedParams p) {

@@ -11,8 +11,10 @@
 // add to the same weight (no atomics).  All rows of a (sequence, KV head) are
 // handled by the CTA that owns the key tile, 256 at a time.
 // Bound: for few rows the stream of K's codes (32 sequences of 32768 tokens at
-// most, 32 / 8 heads of 128, one token each: 129 us for 0.69 GB, 5.3 TB/s or
-// 78 % of the measured copy rate); from about 128 rows on the exponentials (one per
+// most, 32 / 8 heads of 128, one token each: 126 us for 0.69 GB, 5.5 TB/s or
+// 81 % of the measured copy rate; what the issuing thread does for a tile, 700
+// cycles, is the rest of it: more K slots, more score buffers and weights added in
+// L2 instead of read first were all level); from about 128 rows on the exponentials (one per
 // row and key) and the products (blocks of 128 over 4 such sequences, 16 / 8
 // heads: 45 us, 0.76 PFLOP/s; the tensor pipe 31 %, the exponentials' 37 % busy, a
 // third of the time begins and ends the CTAs' two segments).  Not kept: both
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           for (int j = 0; j < n; ++j, ++tc) {
             const uint32_t buf = tc & 1;
-            ok = mbar_wait(BAR(B_SE + buf), ((tc >> 1) & 1) ^ 1, wd, 63) && mbar_wait(BAR(B_KF + slot), kph, wd, 64);
+            ok = mbar_wait(BAR(B_KF + slot), kph, wd, 64) && mbar_wait(BAR(B_SE + buf), ((tc >> 1) & 1) ^ 1, wd, 63);
             if (!ok) break;
             tc_fence_after();
             constexpr uint32_t H = desc_hi(SW, 8 * HD);
@@ -206,7 +208,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < HD / 32; ++kk)
               mma_ss<true>(tmem + buf * 256, k + kk * 2, H, q + (LY::kPart >> 4) + kk * 2, H, id, 1);
             tc_commit(BAR(B_SF + buf));
-            tc_commit(BAR(B_KE + slot));
             if (++slot == NK) slot = 0, kph ^= 1;
           }
           tc_commit(BAR(B_QD));
@@ -327,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           sph ^= 1;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          // (the products are done with K's slot; the issuing thread, which bounds short rows, is spared a commit)
+          if ((tid & 127) == 0) mbar_arrive(BAR(B_KE + tc % NK));
           tc_fence_after();
           const uint64_t ks2 = f2(ks, ks);
           uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};

@@ -13,7 +13,10 @@
 // except where they fall below 2^-6 of the new scale.
 #pragma once
 #include <cuda_fp8.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "geometry.cuh"
 
@@ -43,7 +46,16 @@ struct RowsDesc {
 // workspace's status word): what is bad is left out of the result.
 enum : uint32_t { kStatusBadPage = 0x7201, kStatusBadLen = 0x7202, kStatusBadRows = 0x7204, kStatusCacheMask = 0x7200 };
 
+// Raises a kernel's dynamic shared memory limit on the current device, once per
+// device (`done`: a bit for each).
+cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
+
 #if defined(__CUDACC__)
+
+// Programmatic dependent launch: lets the next kernel of the stream start
+// when it was launched so; waits for the kernel before this one to end.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct SeqView {
   int64_t row0;

@@ -4,7 +4,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
 #include <string>
 
 #include "geometry.cuh"
@@ -120,10 +119,6 @@ cudaError_t launch_watchdog(uint32_t* status, uint64_t limit_ns, cudaStream_t st
 cudaError_t launch_varlen_items(const Geom& all, const int64_t* off, const int64_t* order, const int64_t* beg, int n,
                                 int64_t total, int kind, int tq, int tk, int4* out, cudaStream_t stream,
                                 int* launches);
-
-// Raises a kernel's dynamic shared-memory limit once per device (`done`: one
-// static word per kernel, a bit per device ordinal).
-cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // Records the message bdlm_last_error() returns on this thread.
 void set_last_error(const std::string& msg);

@@ -109,7 +109,7 @@ bdlm_status check_space(void* ws, size_t bytes, size_t need) {
 
 size_t attn_space(int64_t flat, int d) {
   const int tile = cached_tile_rows(flat);
-  return (size_t)cached_ctas(tile, kSmsMax) * 2 * part_floats(tile, d) * sizeof(float);
+  return (size_t)cached_ctas(tile, kSmsMax) * (2 * part_floats(tile, d) + fine_floats(tile, d)) * sizeof(float);
 }
 
 // Codes: boxes of one (page, KV head) block, swizzled by the row's bytes.
@@ -227,6 +227,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     p.sp.keyed = 0;
     p.whole = 0;
     p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
+    p.fine = p.part + (int64_t)p.G * 2 * part_floats(p.sp.tile_rows, p.c.d);
     const int64_t rt = (flat + p.sp.tile_rows - 1) / p.sp.tile_rows;
     if (small && (int64_t)p.c.max_pages * p.c.page <= kWholeKeys && rt * p.c.Hkv * p.c.n_seqs <= 0x7fffffff) {
       p.whole = (int)rt;

@@ -19,6 +19,7 @@ struct CachedParams {
   int o_f32;
   float* LSE;
   float* part;  // two partial results per CTA of G
+  float* fine;  // (fp32 outputs, tcgen05) behind them: two sub-tiles' sums, 128 x d, per CTA
   int G;
   int whole;    // not 0: a CTA per segment, that many row tiles for each (sequence, KV head)
   uint32_t* status;
@@ -35,6 +36,10 @@ __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (i
 // kernel; 64 rows (16 sequences of up to 8192): 118 us here, 87 there.
 constexpr int kSmallRows = 32;
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
+// (fp32 outputs) Weights are kept 2^7 larger than exp2(s - maximum): the smallest
+// step of their second fp16 part, 2^-24, is so much finer against the many small
+// ones of a long row.
+constexpr float kFineShift = 7.0f;
 
 // Row tile of a call whose sequences have at most `flat` rows times heads of
 // a group: 16 or 32 (mma.sync), 128 or 256 (tcgen05, split and pairs).  Split
@@ -45,6 +50,7 @@ constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
 inline int cached_tile_rows(int64_t flat) {
   return flat <= 16 ? 16 : flat <= kSmallRows ? 32 : flat <= 128 ? 128 : 256;
 }
+inline int64_t fine_floats(int tile_rows, int d) { return tile_rows > kSmallRows ? (int64_t)2 * 128 * d : 0; }
 inline int cached_ctas(int tile_rows, int sms) { return tile_rows <= kSmallRows ? sms * kSmallCtasPerSm : sms; }
 
 // Tensor maps: the codes as [n_pages * Hkv, page, d] (V's for the mma.sync

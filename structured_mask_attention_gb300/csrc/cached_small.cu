@@ -90,7 +90,7 @@ struct State {
 // themselves (O = sum p' code, at the fp16 precision of the largest weight
 // whatever the scales), and the row sum takes p' / vs (iv).  In units of
 // exp2(m), O / l is the attention's output and m + log2 l its LSE.
-template <int HD, int N8>
+template <int HD, int N8, bool FINE>
 __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], const float (&iv)[N8 / 2]) {
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -101,7 +101,7 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float mn = fmaxf(st.m[r], mx);
     const float base = mn == -INFINITY ? 0.f : mn;  // no key yet: every p below is 0
-    const float alpha = ex2_approx(st.m[r] - base);
+    const float alpha = ex2_approx(st.m[r] - base), less = FINE ? base - kFineShift : base;
     if (__any_sync(0xffffffffu, mn != st.m[r])) {
 #pragma unroll
       for (int j = 0; j < HD / 8; ++j) {
@@ -114,8 +114,8 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
     float sum[N8 / 2] = {};
 #pragma unroll
     for (int i = 0; i < N8; ++i) {
-      s[i][2 * r] = ex2_approx(s[i][2 * r] - base);
-      s[i][2 * r + 1] = ex2_approx(s[i][2 * r + 1] - base);
+      s[i][2 * r] = ex2_approx(s[i][2 * r] - less);
+      s[i][2 * r + 1] = ex2_approx(s[i][2 * r + 1] - less);
       sum[i / 2] += s[i][2 * r] + s[i][2 * r + 1];
     }
 #pragma unroll
@@ -140,7 +140,9 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
 // P is rounded to fp16 (2^-11) for cached keys and bf16 for own ones, below a
 // bf16 output's own rounding.  FINE, for an fp32 output: P goes in two (three)
 // parts, each what the rounding of the one before left, so that O is off by
-// fp32 sums alone.
+// fp32 sums alone; and the products of 16 keys are added to O by the threads: the
+// tensor cores cut their sums off instead of rounding them, always towards zero,
+// which over 600 products in a row came to 9e-6 of O.
 struct SInfo {  // of each 16 keys of a tile: K's scale, log2 and inverse of V's (1, 0, 1 without a page)
   float s[8], lv[8], iv[8];
   int gone;     // bit x: no page
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           __syncwarp();
           if (lane == 0) mbar_arrive(KE(slot));
         }
-        softmax_step<HD, 4>(st, s, iv);
+        softmax_step<HD, 4, FINE>(st, s, iv);
         uint32_t pa[2][4], pr[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -456,8 +458,16 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const uint32_t b0 = e4m3x2_to_half2(lo >> (16 * y)), b1 = e4m3x2_to_half2(hi >> (16 * y));
-                mma_f16(st.o[4 * w + 2 * hf + y], pa[x][0], pa[x][1], pa[x][2], pa[x][3], b0, b1);
-                if (FINE) mma_f16(st.o[4 * w + 2 * hf + y], pr[x][0], pr[x][1], pr[x][2], pr[x][3], b0, b1);
+                float (&o)[4] = st.o[4 * w + 2 * hf + y];
+                if (FINE) {
+                  float z[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_f16(z, pa[x][0], pa[x][1], pa[x][2], pa[x][3], b0, b1);
+                  mma_f16(z, pr[x][0], pr[x][1], pr[x][2], pr[x][3], b0, b1);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[e] += z[e];
+                } else {
+                  mma_f16(o, pa[x][0], pa[x][1], pa[x][2], pa[x][3], b0, b1);
+                }
               }
             }
         }
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           for (int e = 0; e < 4; ++e)
             s[i][e] = key0 + 8 * i + 2 * t + (e & 1) < seg.v.rows ? s[i][e] * p.sl2 : -INFINITY;
         const float one[1] = {1.f};
-        softmax_step<HD, 2>(st, s, one);
+        softmax_step<HD, 2, FINE>(st, s, one);
         uint32_t pa[4], pr[4], pq[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (t == 0) {
-        red_ml[warp][g + 8 * r][0] = st.m[r];
+        red_ml[warp][g + 8 * r][0] = FINE ? st.m[r] - kFineShift : st.m[r];  // the weights' reference
         red_ml[warp][g + 8 * r][1] = l;
       }
       // tile j, element e: column HD / 8 perm(2 t + e) + j

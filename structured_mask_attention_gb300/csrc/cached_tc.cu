@@ -63,8 +63,11 @@ constexpr int kLaunchRegs = 128;
 static_assert(128 * (kRegsControl + kRegsConvert) + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
               "register split exceeds the block");
 constexpr float kRescale = 8.0f;  // log2 units: the reference maximum moves in steps of at least this
-// (fp32 outputs) weights are kept 2^7 larger, up to 2^15: the second part's smallest step, 2^-24, is so much finer
-constexpr float kFineShift = 7.0f;
+// (fp32 outputs) Key tiles that a sub-tile adds up on the tensor cores.  1 / 2 / 4 /
+// all of about 90: O off by 1.0 / 1.2 / 1.6 / 8.9e-6 of its size over 19357 keys
+// (fp32 products in torch: 2.6e-6); blocks of 128 of the case above as fp32, with 1 /
+// 2 / 4: 972 / 835 / 776 us.
+constexpr int kFineTiles = 4;
 constexpr int NK = 3;             // K slots: 128 keys of codes, or one 64-column panel of own keys
 constexpr int NI = 16;            // tile-info slots (more than any two roles are apart, and a batch of four)
 constexpr int kSlot = 128 * 128;  // bytes of a K slot, of a V slot and of a bf16 panel
@@ -782,6 +785,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!KS || nk > 0) ++qfc;
       }
       float m_ref = -INFINITY, l = 0.f;
+      // FINE: the tensor cores cut their sums off instead of rounding them, always
+      // towards zero (9e-6 of O over 600 products in a row); so every kFineTiles
+      // tiles O moves to sums that this thread keeps, and begins again at 0
+      float m_sum = -INFINITY;
+      int since = 0;
+      bool summed = false;
+      float4* sums = reinterpret_cast<float4*>(p.fine + ((int64_t)blockIdx.x * 2 + t) * 128 * HD) + row;
+      // back: O takes in the sums; else: the sums take in O
+      auto move_o = [&](bool back) {
+        const float f = summed && m_ref != -INFINITY ? ex2_approx(m_sum - m_ref) : 0.f;
+#pragma unroll 1
+        for (int c4 = 0; c4 < HD / 32; ++c4) {
+          uint32_t o[32];
+          tmem_ld32(tO + t * 128 + c4 * 32, o);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            float4* at = sums + (c4 * 8 + x) * 128;
+            float4 v = summed ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+            v.x = fmaf(v.x, f, __uint_as_float(o[4 * x]));
+            v.y = fmaf(v.y, f, __uint_as_float(o[4 * x + 1]));
+            v.z = fmaf(v.z, f, __uint_as_float(o[4 * x + 2]));
+            v.w = fmaf(v.w, f, __uint_as_float(o[4 * x + 3]));
+            if (!back) *at = v;
+            o[4 * x] = back ? __float_as_uint(v.x) : 0u;
+            o[4 * x + 1] = back ? __float_as_uint(v.y) : 0u;
+            o[4 * x + 2] = back ? __float_as_uint(v.z) : 0u;
+            o[4 * x + 3] = back ? __float_as_uint(v.w) : 0u;
+          }
+          tmem_st32(tO + t * 128 + c4 * 32, o);
+        }
+        m_sum = m_ref;
+        summed = true;
+      };
       // keys left from the piece's first cached (own) tile on
       const int left_k = pp->len - pp->k0 * kUnit, left_l = pp->rows - pp->l0 * kUnit;
       for (int j = KS ? t : 0; j < n; j += KS ? 2 : 1, ++sc) {
@@ -798,6 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        // (O is complete up to the tile before: S of this one was issued behind its product)
+        if (FINE && since++ == kFineTiles) {
+          move_o(false);
+          since = 1;
+        }
         const int hi = own ? left_l - (j - nk) * kUnit : left_k - j * kUnit;
         const float rf = own ? p.sl2 : cq;
         float f[4] = {rf * ks4.x, rf * ks4.y, rf * ks4.z, rf * ks4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
@@ -890,8 +931,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tcount += (uint32_t)n;
 
       // ---- the piece's result
-      if (FINE) m_ref -= kFineShift;  // the reference of the weights as they were kept
-      float w0 = 1.f, w1 = 0.f, M = m_ref, L = l;
+      // (the reference of the weights as they were kept)
+      const float m_kept = FINE ? m_ref - kFineShift : m_ref;
+      float w0 = 1.f, w1 = 0.f, M = m_kept, L = l;
       const int n0 = KS ? (n + 1) / 2 : n, n1 = KS ? n / 2 : n;
       if (KS && n > 0) {
         // both sub-tiles' states of this row (O's first product of the piece waited
@@ -900,7 +942,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && n1 > 0) ok = mbar_wait(BAR(B_OD + 1), itn[1] & 1, wd, 45);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        ml[t * 128 + row] = make_float2(m_ref, l);
+        if (FINE && summed) {
+          tc_fence_after();
+          move_o(true);
+          tc_fence_before();
+        }
+        ml[t * 128 + row] = make_float2(m_kept, l);
         mbar_arrive(BAR(B_ML));
         ok = mbar_wait(BAR(B_ML), mlc & 1, wd, 46);
         ok = __all_sync(0xffffffffu, ok);
@@ -919,6 +966,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++itn[0];
+        if (FINE && summed) {
+          tc_fence_after();
+          move_o(true);
+        }
       }
       tc_fence_after();
       const float inv = L != 0.f ? 1.f / L : 0.f;

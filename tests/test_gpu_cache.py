@@ -106,6 +106,30 @@ def test_attn_long_prefix_spans_many_parts(lib, rows):
     run_attn(lib, [6000, 1], [rows, 1], 4, 1, 64, 128, seed=9)
 
 
+@pytest.mark.parametrize("rows,chain", [(1, 2), (10, 2), (40, 64), (150, 64)])
+def test_attn_fp32_output_of_long_rows(lib, rows, chain):
+    """Sequences of many keys of like weight (the same pages, other queries),
+    so that a CTA adds up tens of key tiles.  The tensor cores cut each sum
+    off by up to 2^-23 of it, always towards zero; ``chain`` products of 16 keys
+    follow each other before the threads take over with rounded sums.  A sum of
+    terms unlike in sign grows as the root of their number, 2/3 of its last size
+    in the mean: off by chain * 2^-23 * 2/3 at most, here 2^-22.6 or 2^-17.6 of O.
+    The weights' and scores' own errors, 2^-22 a few times over, are unlike in
+    sign from key to key: 2^-21 of O in the mean."""
+    m = lib
+    d, n, L = 128, 24, 12000
+    c, _ = make_cache([L], L, 2, d, 64, seed=93)
+    c["table"], c["lens"] = np.repeat(c["table"], n, 0), np.repeat(c["lens"], n)
+    Q = make_rows(n * rows, 4, d, 3)
+    O, LSE = m.bdlm_attn_cached(to_dev(Q, torch), None, None, device_cache(m, torch, c), o_dtype=torch.float32)
+    ref = co.attn(c, Q, None, None, offsets_of([rows] * n), 1 / math.sqrt(d))
+    check_attn(O, LSE, ref, d, False)
+    diff = O.double().cpu().numpy() - ref[0]
+    rel = math.sqrt((diff ** 2).sum() / (ref[0] ** 2).sum())
+    print(f"  O off by {rel:.2e} of its size")
+    assert rel <= chain * 2.0 ** -23 * 2 / 3 + 2.0 ** -21
+
+
 def test_attn_many_sequences(lib):
     lens = [(37 * i) % 200 for i in range(70)]
     run_attn(lib, lens, [1 + i % 3 for i in range(70)], 4, 2, 64, 16, seed=11)

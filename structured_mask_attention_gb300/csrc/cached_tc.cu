@@ -66,7 +66,8 @@ constexpr float kRescale = 8.0f;  // log2 units: the reference maximum moves in 
 // (fp32 outputs) Key tiles that a sub-tile adds up on the tensor cores.  1 / 2 / 4 /
 // all of about 90: O off by 1.0 / 1.2 / 1.6 / 8.9e-6 of its size over 19357 keys
 // (fp32 products in torch: 2.6e-6); blocks of 128 of the case above as fp32, with 1 /
-// 2 / 4: 972 / 835 / 776 us.
+// 2 / 4: 972 / 835 / 776 us (624 since the issuing thread's short loop serves fp32
+// outputs too and the third parts stay where they arise).
 constexpr int kFineTiles = 4;
 constexpr int NK = 3;             // K slots: 128 keys of codes, or one 64-column panel of own keys
 constexpr int NI = 16;            // tile-info slots (more than any two roles are apart, and a batch of four)
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = start_s(0) && (n < 2 || start_s(1));
             int j = 0;
             // (as in pairs, below: while the tile after next is a cached one)
-            const bool opened = !FINE && nk > 3;
+            const bool opened = nk > 3;
             if (opened) {
               ok = ok && mbar_wait(BAR(B_OE + 0), oph & 1, wd, 32) && mbar_wait(BAR(B_OE + 1), (oph >> 1) & 1, wd, 32);
               oph ^= 3;
@@ -621,6 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                   mma_ts(tmem + 256 + t * 128, tmem + t * 128 + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+#pragma unroll
+                for (int kk = 0; kk < (FINE ? 8 : 0); ++kk)
+                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 16 + p_col(kk), vt + kk * 128, HV, kIdO16, 1);
                 tc_commit(BAR(B_WE + vs));
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk)
@@ -657,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // cached tiles that a cached tile follows: the waits, products and
             // commits alone (whatever else this thread does idles the tensor
             // cores: their queue holds about one product)
-            if (!FINE && nk > 1) {
+            if (nk > 1) {
               ok = ok && mbar_wait(BAR(B_OE + 0), oph & 1, wd, 32) && mbar_wait(BAR(B_OE + 1), oph & 1, wd, 32);
               oph ^= 1;
               for (; ok && j + 1 < nk; ++j, ++wc) {
@@ -672,6 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kk = 0; kk < 8; ++kk)
                   mma_ts(tmem + 256, tmem + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
 #pragma unroll
+                for (int kk = 0; kk < (FINE ? 8 : 0); ++kk)
+                  mma_ts(tmem + 256, tmem + 16 + p_col(kk), vt + kk * 128, HV, kIdO16, 1);
+#pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                   constexpr int n8 = HD / 32;
                   mma_ss<true>(tmem, q + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ, kt + (kk % n8) * 2, HQ, kId8, kk > 0);
@@ -683,6 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                   mma_ts(tmem + 384, tmem + 128 + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+#pragma unroll
+                for (int kk = 0; kk < (FINE ? 8 : 0); ++kk)
+                  mma_ts(tmem + 384, tmem + 144 + p_col(kk), vt + kk * 128, HV, kIdO16, 1);
                 tc_commit(BAR(B_WE + (wc & 1)));
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
@@ -696,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pph ^= 1;
               }
             }
-            const bool opened = !FINE && nk > 1;
+            const bool opened = nk > 1;
             for (; ok && j < n; ++j, ++wc) {
               const bool last = j == n - 1, swap = j + 1 == nk && !last;
               ok = issue_pv(0, wc, own(j), j == 0, j == 0 && !opened);
@@ -871,7 +881,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float nm = m_ref == -INFINITY ? 0.f : (FINE ? kFineShift : 0.f) - m_ref;
         l *= alpha;
-        uint32_t rest[FINE ? 64 : 1];  // own keys, FINE: the third parts, packed
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           float s0, s1;
@@ -879,13 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = fine ? fmaf(s0, iv[x], fmaf(s1, ki.iv[1][x], l)) : fmaf(s0 + s1, iv[x], l);
           if (own) {
             store_p<true, FINE>(a[x], tS + 32 * x);
-            if (FINE) {
-              store_p<true, true>(a[x], tS + 32 * x + 16);
-#pragma unroll
-              for (int y = 0; y < 16; ++y)
-                rest[(FINE ? 16 * x + y : 0)] =
-                    pack_bf16x2(__uint_as_float(a[x][2 * y]), __uint_as_float(a[x][2 * y + 1]));
-            }
+            if (FINE) store_p<true, true>(a[x], tS + 32 * x + 16);  // (leaves the third part in a)
           } else {
             store_p<false, FINE>(a[x], tS + 32 * x);
             if (FINE) store_p<false, false>(a[x], tS + 32 * x + 16);
@@ -914,7 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 4; ++x) {
             uint32_t pk[16];
 #pragma unroll
-            for (int y = 0; y < 16; ++y) pk[y] = rest[FINE ? 16 * x + y : 0];
+            for (int y = 0; y < 16; ++y)
+              pk[y] = pack_bf16x2(__uint_as_float(a[x][2 * y]), __uint_as_float(a[x][2 * y + 1]));
             tmem_st16(tS + 32 * x, pk);
           }
           tc_fence_before();

@@ -418,7 +418,8 @@ size_t bdlm_workspace_size_cache(int n_seqs, int Hq, int Hkv, int d, int64_t max
  * to the new scale.  A block that takes in a NaN or an infinity gets a NaN
  * scale: every row that sees it reads NaN.  lens_out [n_seqs] (may be null)
  * gets lens + rows; it must not overlap lens, which is left as it is.  Pages
- * written by the call must belong to one sequence only. */
+ * written by the call must belong to one sequence only, at one place of its
+ * table. */
 bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* cache, const int32_t* row_offsets,
                               int64_t rows, int64_t max_rows, int32_t* lens_out, void* workspace, size_t ws_bytes,
                               bdlm_stream stream);
@@ -452,7 +453,7 @@ bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cach
  * those of largest weight (equal weights: the lower position; NaN counts as
  * the largest).  The kept tokens move, in order, to slots 0, 1, ... of the
  * pages of dst_table [n_seqs, max_pages] (pages of the same pool that no
- * sequence reads; entries behind the last page needed are not used), in
+ * sequence reads, each named once; entries behind the last page needed are not used), in
  * blocks that get the scale of bdlm_cache_append for what they hold.
  * lens_out [n_seqs] = min(lens, keep); weights_out gets the kept tokens'
  * weights and zero behind them; kept [n_seqs, Hkv, keep] (may be null) their

@@ -66,9 +66,9 @@ constexpr float kRescale = 8.0f;  // log2 units: the reference maximum moves in 
 // (fp32 outputs) Key tiles that a sub-tile adds up on the tensor cores.  1 / 2 / 4 /
 // all of about 90: O off by 1.0 / 1.2 / 1.6 / 8.9e-6 of its size over 19357 keys
 // (fp32 products in torch: 2.6e-6); blocks of 128 of the case above as fp32, with 1 /
-// 2 / 4: 972 / 835 / 776 us (624 since the issuing thread's short loop serves fp32
-// outputs too and the third parts stay where they arise).
-constexpr int kFineTiles = 4;
+// 2 / 4: 972 / 835 / 776 us (since the issuing thread's short loop serves fp32
+// outputs too and the third parts stay where they arise, 2 / 4: 647 / 624).
+constexpr int kFineTiles = 2;
 constexpr int NK = 3;             // K slots: 128 keys of codes, or one 64-column panel of own keys
 constexpr int NI = 16;            // tile-info slots (more than any two roles are apart, and a batch of four)
 constexpr int kSlot = 128 * 128;  // bytes of a K slot, of a V slot and of a bf16 panel

@@ -55,8 +55,8 @@ struct LayW {
   static constexpr int kQ = 0;                      // two parts of 256 rows
   static constexpr int kPart = kChunk * HD;
   static constexpr int kK = 2 * kPart;
-  static constexpr int kRow = kK + NK * kSlot;      // row pairs {c0, c1, n0, n1}
-  static constexpr int kInfo = kRow + kChunk * 8;
+  static constexpr int kRow = kK + NK * kSlot;      // two buffers of row pairs {c0, c1, n0, n1}
+  static constexpr int kInfo = kRow + 2 * kChunk * 8;
   static constexpr int kPC = kInfo + NI * (int)sizeof(WInfo);
   static constexpr int kBar = (kPC + NP * (int)sizeof(WPiece) + 15) & ~15;
   static constexpr int kBytes = kBar + 8 * B_COUNT + 16;
@@ -262,6 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       done(np);
       for (int r0 = 0; r0 < flat; r0 += kChunk) {
         const int cnt = min(flat - r0, kChunk), N = (cnt + 31) & ~31;
+        // The rows' constants have two buffers, by the chunk's parity: the products'
+        // end (B_QD) frees the query tiles, but one sub-tile may still be reading the
+        // constants for its last key tile while the other writes the next chunk's.  It
+        // comes to chunk c + 2, and chunk c's buffer, behind B_QF of chunk c + 1, where
+        // all 256 threads arrive when they have left chunk c.
+        float* const rows_c = reinterpret_cast<float*>(bp + LY::kRow) + (qd & 1) * 2 * kChunk;
         // ---- HD / 16 lanes take a row, 16 values each
         constexpr int PER = HD / 16;
         constexpr int RB = 4, RS = 256 / PER;  // rows in flight per thread, rows per pass
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
             st_shared_v4(at + LY::kPart, lo[0], lo[1], lo[2], lo[3]);
             if (i == 0) {
-              float* rp = reinterpret_cast<float*>(bp + LY::kRow) + (r >> 1) * 4 + (r & 1);
+              float* rp = rows_c + (r >> 1) * 4 + (r & 1);
               rp[0] = p.sl2 * inv;
               rp[2] = nl;
             }
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(BAR(B_QF), qd & 1, wd, 66);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const float4* rowc = reinterpret_cast<const float4*>(bp + LY::kRow);
+        const float4* rowc = reinterpret_cast<const float4*>(rows_c);
         // (a tile's weights are read a tile ahead)
         auto old = [&](int j) { return j < n && (j0 + j) * kUnit + key < len ? W[(j0 + j) * kUnit + key] : 0.f; };
         float next = old((int)((tc ^ (uint32_t)t) & 1));

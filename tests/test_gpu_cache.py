@@ -335,6 +335,34 @@ def test_weights(lib, lens, rows, Hq, Hkv, d, page):
         assert np.array_equal(W[s, :, L:].cpu().numpy(), W0[s, :, L:])
 
 
+@pytest.mark.parametrize("lens,rows,Hq,Hkv,d,page", [
+    ([4800, 3000], [384, 384], 16, 8, 128, 64),        # three chunks of 256 rows, three key tiles per CTA
+    ([9000, 2000, 5000], [330, 260, 384], 4, 2, 64, 16),
+    ([9000, 20000], [200, 90], 40, 2, 128, 128),       # 16 and 8 chunks
+])
+def test_weights_of_several_chunks_and_tiles(lib, lens, rows, Hq, Hkv, d, page):
+    """A CTA goes through several chunks of rows and several segments: each
+    time with its own rows' constants, whichever sub-tile is ahead."""
+    m = lib
+    c, _ = make_cache(lens, max(lens), Hkv, d, page, seed=sum(rows))
+    off, T = offsets_of(rows), sum(rows)
+    Q = make_rows(T, Hq, d, 3)
+    dQ, doff, cache = to_dev(Q, torch), torch.from_numpy(off).cuda(), device_cache(m, torch, c)
+    ws = m.bdlm_cache_workspace(cache, Hq, max(rows))
+    LSE = m.bdlm_attn_cached(dQ, None, None, cache, doff, max(rows), workspace=ws, o_dtype=torch.float32)[1]
+    def once():
+        W = torch.zeros((len(lens), Hkv, c["table"].shape[1] * page), device="cuda")
+        return m.bdlm_cache_weights(dQ, LSE, cache, W, doff, max(rows), workspace=ws)
+    W = once()
+    for _ in range(50):
+        assert torch.equal(once(), W)
+    m.bdlm_sync_status(ws)
+    L = LSE.cpu().numpy()
+    ref, E = co.weights(c, Q, L, off, 1 / math.sqrt(d), np.zeros(W.shape, np.float32))
+    rel = score_error(d, E) + 2.0 ** -23 * (1 + np.abs(L).max()) + (max(rows) * (Hq // Hkv) + 4) * 2.0 ** -24
+    assert (np.abs(W.double().cpu().numpy() - ref) <= rel * ref + 2.0 ** -24).all()
+
+
 def test_weights_of_rows_without_a_key(lib):
     """LSE = -inf rows (a block whose other keys were not given) add nothing."""
     m = lib

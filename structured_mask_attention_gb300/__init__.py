@@ -676,6 +676,8 @@ def _cache_workspace(cache, ws, made, need):
         made.append(ws)
     elif ws.device != cache.device:
         raise ValueError(f"the workspace is on {ws.device}, the cache on {cache.device}")
+    elif not ws.is_contiguous():  # (a view's elements may be more than its memory)
+        raise ValueError("the workspace must be contiguous")
     return ws
 
 
@@ -699,7 +701,7 @@ def bdlm_cache_append(cache, K, V, row_offsets=None, max_rows: int | None = None
     ws = _cache_workspace(cache, workspace, made, 256)
     _cache_call(load_library().bdlm_cache_append, cache, stream,
                 (K.data_ptr(), V.data_ptr(), cache._ref, off, T, max_rows, lens_out.data_ptr(), ws.data_ptr(),
-                 ws.numel()), made)
+                 ws.nbytes), made)
     return lens_out
 
 
@@ -735,7 +737,7 @@ def bdlm_attn_cached(Qn, Kn, Vn, cache, row_offsets=None, max_rows: int | None =
     _cache_call(load_library().bdlm_attn_cached, cache, stream,
                 (Qn.data_ptr(), None if Kn is None else Kn.data_ptr(), None if Vn is None else Vn.data_ptr(), cache._ref,
                  off, T, max_rows, Hq, 1.0 / math.sqrt(d) if scale is None else scale, O.data_ptr(),
-                 F32 if O.dtype == torch.float32 else BF16, LSE.data_ptr(), ws.data_ptr(), ws.numel()), made)
+                 F32 if O.dtype == torch.float32 else BF16, LSE.data_ptr(), ws.data_ptr(), ws.nbytes), made)
     return O, LSE
 
 
@@ -755,7 +757,7 @@ def bdlm_cache_weights(Qn, LSE, cache, weights, row_offsets=None, max_rows: int 
     ws = _cache_workspace(cache, workspace, made, 256)
     _cache_call(load_library().bdlm_cache_weights, cache, stream,
                 (Qn.data_ptr(), LSE.data_ptr(), cache._ref, off, T, max_rows, Hq,
-                 1.0 / math.sqrt(d) if scale is None else scale, weights.data_ptr(), ws.data_ptr(), ws.numel()), made)
+                 1.0 / math.sqrt(d) if scale is None else scale, weights.data_ptr(), ws.data_ptr(), ws.nbytes), made)
     return weights
 
 
@@ -782,7 +784,7 @@ def bdlm_cache_evict(cache, weights, dst_table, keep: int, sinks: int = 0, recen
     ws = _cache_workspace(cache, workspace, made, 256)
     _cache_call(load_library().bdlm_cache_evict, cache, stream,
                 (cache._ref, weights.data_ptr(), dst_table.data_ptr(), keep, sinks, recent, lens_out.data_ptr(),
-                 weights_out.data_ptr(), kept.data_ptr() or None, ws.data_ptr(), ws.numel()), made)
+                 weights_out.data_ptr(), kept.data_ptr() or None, ws.data_ptr(), ws.nbytes), made)
     return lens_out, weights_out, kept
 
 

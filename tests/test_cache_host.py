@@ -134,6 +134,17 @@ def test_handle_refuses_host_tensors_and_reassignment(lib):
         m.BdlmCache(f8[0], f8, sc, sc, tab, lens)
 
 
+def test_workspace_views_are_refused():
+    """A view with more elements than memory, or with gaps, would be overrun."""
+    import types
+    cache = types.SimpleNamespace(device=torch.device("cpu"))
+    ws = torch.zeros(512, dtype=torch.uint8)
+    assert m._cache_workspace(cache, ws, [], 256) is ws
+    for bad in (ws[:1].expand(512), ws[::2], ws.view(16, 32).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            m._cache_workspace(cache, bad, [], 256)
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="host-only check of the no-device path")
 def test_valid_calls_without_a_device_report_an_error(lib):
     assert _attn(lib) in (5, 6)

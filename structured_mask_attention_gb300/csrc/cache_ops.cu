@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
     if (bad) atomicOr(p.status, bad);
     bad = 0;
   }
-  if (first >= rows) return;
+  if (rows <= 0 || first >= rows) return;  // (without new rows a half-filled page, maybe another sequence's too, stays as it is)
   if (tid < TT / 16) {
     const int f = first + (tid << c.lp);  // new token of the block's first slot
     int id = -1;

@@ -80,7 +80,7 @@ typedef void* bdlm_stream;
 
 /* Workspace bytes a call of kind `op` needs at this shape (P is ignored by
  * every op today and kept for shard-count dependent variants).  The
- * workspace holds a 256-byte header (the status word in its first 4 bytes,
+ * workspace holds a 256-byte header (the status words in its first 8 bytes,
  * then the counters from which the kernels' persistent CTAs claim work
  * items; every call zeroes what it uses before its first kernel) and, for
  * BDLM_OP_BWD, the row statistic D of both streams.  Returns 0 for an
@@ -387,12 +387,13 @@ bdlm_status bdlm_attn_bwd_varlen(const void* Qc, const void* Kc, const void* Vc,
  * row_offsets null, max_rows rows each (rows = n_seqs * max_rows).
  *
  * Workspace: bdlm_workspace_size_cache bytes, whose first 256 the caller
- * zeroes ONCE (these calls do not clear the status word: an error stays until
+ * zeroes ONCE (these calls do not clear the status words: an error stays until
  * bdlm_sync_status reads it).  Contents that only the device can check -- a
  * page id outside the pool, a length that is negative or outside the page
  * table, row offsets that leave the rows or exceed max_rows -- are left out of
  * the result (those keys unseen, that length cut, those rows skipped) and
- * reported by bdlm_sync_status as BDLM_ERR_INVALID_ARG. */
+ * reported by bdlm_sync_status as BDLM_ERR_INVALID_ARG; a wait that expired is
+ * recorded beside them and reported first, as BDLM_ERR_TIMEOUT. */
 typedef struct {
   void* k8;                  /* [n_pages, Hkv, page, d] e4m3 */
   void* v8;
@@ -485,7 +486,7 @@ int64_t bdlm_worklist(int64_t L, int64_t B, int Hq, int Hkv, int tile_q, int til
                       int64_t kv_begin, int64_t kv_end, int include_local,
                       int32_t* out, int64_t cap);
 
-/* Waits for `stream`, then reads and clears the workspace's status word.
+/* Waits for `stream`, then reads and clears the workspace's status words.
  * Returns BDLM_ERR_TIMEOUT if a kernel's bounded wait expired,
  * BDLM_ERR_INVALID_ARG if a cache call met contents out of range,
  * BDLM_ERR_CUDA if the stream reported an error, else BDLM_OK. */

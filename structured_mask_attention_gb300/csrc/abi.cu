@@ -964,18 +964,23 @@ bdlm_status bdlm_sync_status(void* workspace, bdlm_stream stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    uint32_t word = 0;
-    e = cudaMemcpy(&word, workspace, 4, cudaMemcpyDeviceToHost);
+    uint32_t words[kContentsWord + 1] = {};
+    e = cudaMemcpy(words, workspace, sizeof(words), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(status)");
-    e = cudaMemset(workspace, 0, 4);
+    e = cudaMemset(workspace, 0, sizeof(words));
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(status)");
-    if ((word >> 8) == (kStatusCacheMask >> 8))
-      return fail(BDLM_ERR_INVALID_ARG, "cache contents out of range (status 0x%x):%s%s%s", word,
-                  (word & 0xff & kStatusBadPage) ? " a page id outside the pool;" : "",
-                  (word & 0xff & kStatusBadLen) ? " a length outside its page table;" : "",
-                  (word & 0xff & kStatusBadRows) ? " row offsets outside the rows;" : "");
+    const uint32_t word = words[0], bad = words[kContentsWord];
+    char what[160] = "";
+    if (bad)
+      snprintf(what, sizeof(what), "cache contents out of range (0x%x):%s%s%s", bad,
+               (bad & 0xff & kStatusBadPage) ? " a page id outside the pool;" : "",
+               (bad & 0xff & kStatusBadLen) ? " a length outside its page table;" : "",
+               (bad & 0xff & kStatusBadRows) ? " row offsets outside the rows;" : "");
+    // (an expired wait first: after it nothing of the result is good)
     if (word != 0)
-      return fail(BDLM_ERR_TIMEOUT, "device wait limit expired (status 0x%x, wait site %u)", word, word & 0xffu);
+      return fail(BDLM_ERR_TIMEOUT, "device wait limit expired (status 0x%x, wait site %u)%s%s", word, word & 0xffu,
+                  bad ? "; " : "", what);
+    if (bad) return fail(BDLM_ERR_INVALID_ARG, "%s", what);
     return BDLM_OK;
   });
 }

@@ -19,6 +19,7 @@
 #include <atomic>
 
 #include "geometry.cuh"
+#include "kernels.h"
 
 namespace bdlm {
 
@@ -42,9 +43,12 @@ struct RowsDesc {
   int max_rows;
 };
 
-// Status codes of contents that only the device can check (or-ed into the
-// workspace's status word): what is bad is left out of the result.
-enum : uint32_t { kStatusBadPage = 0x7201, kStatusBadLen = 0x7202, kStatusBadRows = 0x7204, kStatusCacheMask = 0x7200 };
+// Findings about contents that only the device can check: what is bad is left
+// out of the result.  They are or-ed into a word of their own in the workspace
+// header, so that the status word stays free for the first expired wait.
+enum : uint32_t { kStatusBadPage = 0x7201, kStatusBadLen = 0x7202, kStatusBadRows = 0x7204 };
+constexpr int kContentsWord = 1;  // (uint32; word 0: the status word)
+static_assert(kContentsWord < kSchedWordFwd && (kContentsWord + 1) * 4 <= kHeaderClearBytes, "a word that training calls clear");
 
 // Raises a kernel's dynamic shared memory limit on the current device, once per
 // device (`done`: a bit for each).

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
   const int first = base - v.len;                               // as a new token (negative: old tokens)
   if (blockIdx.x == 0 && h == 0 && tid == 0) {
     if (p.lens_out) p.lens_out[s] = v.len + rows;
-    if (bad) atomicOr(p.status, bad);
+    if (bad) atomicOr(p.status + kContentsWord, bad);
     bad = 0;
   }
   if (rows <= 0 || first >= rows) return;  // (without new rows a half-filled page, maybe another sequence's too, stays as it is)
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
     s_was[0][tid] = id >= 0 && f < 0 ? c.ks[b] : 0.f;
     s_was[1][tid] = id >= 0 && f < 0 ? c.vs[b] : 0.f;
     s_amax[0][tid] = s_amax[1][tid] = 0;
-    if (bad) atomicOr(p.status, bad);
+    if (bad) atomicOr(p.status + kContentsWord, bad);
   }
   uint4 x[NT][2];
 #pragma unroll
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) bdlm_evict_select_kernel(const
   for (int i = left + rank * kSelThreads + tid; i < p.keep; i += step) kept[i] = -1;
   for (int64_t i = left + rank * kSelThreads + tid; i < cap; i += step) wo[i] = 0.f;
   if (h == 0 && rank == 0 && tid == 0) p.lens_out[s] = left;
-  if (bad && tid == 0) atomicOr(p.status, bad);
+  if (bad && tid == 0) atomicOr(p.status + kContentsWord, bad);
   cl.barrier_wait();  // no CTA leaves while another may still read its counts
 }
 
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kMoveThreads, TT == 128 ? 5 : 1) bdlm_evict_mo
     *(reinterpret_cast<uint4*>((kv ? c.v8 : c.k8) + (blk * c.page + (tok & (c.page - 1))) * HD) + k % CH) = o;
     if (k % CH == 0 && (tok & (c.page - 1)) == 0) (kv ? c.vs : c.ks)[blk] = ns;
   }
-  if (bad) atomicOr(p.status, bad);
+  if (bad) atomicOr(p.status + kContentsWord, bad);
 }
 
 }  // namespace

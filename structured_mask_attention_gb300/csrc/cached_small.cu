@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
       }
       if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
     }
-    if (bad) atomicOr(p.status, bad);
+    if (bad) atomicOr(p.status + kContentsWord, bad);
     // (copies that a timeout left in flight land before the CTA's shared memory is given up)
     if (*abort_flag) drain_after_abort(200);
     return;

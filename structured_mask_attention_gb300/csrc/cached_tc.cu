@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         done(np);
       }
-      if (bad) atomicOr(p.status, bad);
+      if (bad) atomicOr(p.status + kContentsWord, bad);
     };
     if (warp == 0) {
       load(std::false_type{});
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
         }
       }
-      if (bad) atomicOr(p.status, bad);  // (each lane has looked at other sequences)
+      if (bad) atomicOr(p.status + kContentsWord, bad);  // (each lane has looked at other sequences)
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issue
       if (lane == 0) {

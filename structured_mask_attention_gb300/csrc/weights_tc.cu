@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       done(np);
     }
-    if (bad) atomicOr(p.status, bad);
+    if (bad) atomicOr(p.status + kContentsWord, bad);
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issue
     if (lane == 0) {
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q.n < 0) break;
       }
     }
-    if (bad) atomicOr(p.status, bad);  // (each lane has looked at other sequences)
+    if (bad) atomicOr(p.status + kContentsWord, bad);  // (each lane has looked at other sequences)
   } else if (warp >= 4) {
     // ---------------------------------------------- queries, then a key per thread
     const int t = (warp - 4) >> 2, tid = threadIdx.x - 128;

@@ -39,3 +39,33 @@ def test_append_leaves_a_sequence_without_rows_alone(lib, scale, page, d):
     for w in ("k", "v"):
         assert np.array_equal(host_codes(getattr(cache, w + "8")), c[w + "8"])
         assert np.array_equal(getattr(cache, w + "_scale").cpu().numpy(), c[w + "s"], equal_nan=True)
+
+
+def test_a_timeout_is_reported_whatever_the_contents_were(lib):
+    """Contents out of range and an expired wait have a word each: neither hides
+    the other, and a timeout (here: its code, written as a kernel would) is what
+    the report names."""
+    m = lib
+    c, _ = make_cache([60], 64, 1, 64, 16, seed=51)
+    cache = device_cache(m, torch, c)
+    ws = m.bdlm_cache_workspace(cache, 2, 1)
+    words = ws[:64].view(torch.int32)
+    cache.page_table[0, 1] = -5
+    Q = to_dev(make_rows(1, 2, 64, 1), torch)
+    def call():
+        m.bdlm_attn_cached(Q, None, None, cache, workspace=ws)
+        torch.cuda.synchronize()
+    call()
+    assert int(words[0]) == 0                        # free for the first expired wait
+    with pytest.raises(m.BdlmError, match="page id"):
+        m.bdlm_sync_status(ws)
+    for first in (True, False):
+        if not first:
+            call()
+        words[0] = 0x7100 | 33
+        if first:
+            call()
+        with pytest.raises(m.BdlmError, match="wait site 33") as e:
+            m.bdlm_sync_status(ws)
+        assert e.value.status == 7 and "page id" in str(e.value)
+        m.bdlm_sync_status(ws)                       # both are read once

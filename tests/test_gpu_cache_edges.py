@@ -69,3 +69,41 @@ def test_a_timeout_is_reported_whatever_the_contents_were(lib):
             m.bdlm_sync_status(ws)
         assert e.value.status == 7 and "page id" in str(e.value)
         m.bdlm_sync_status(ws)                       # both are read once
+
+
+def test_captured_eviction(lib):
+    """A graph of weigh + evict, replayed on other weights and lengths."""
+    m = lib
+    keep = 40
+    c, (dst,) = make_cache([300, 90], 320, 2, 64, 16, seed=71, sets=2)
+    cache, ddst = device_cache(m, torch, c), torch.from_numpy(dst).cuda()
+    ws = m.bdlm_cache_workspace(cache, 4, 1, keep)
+    W = torch.zeros((2, 2, c["table"].shape[1] * 16), device="cuda")
+    out = (torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros_like(W),
+           torch.zeros((2, 2, keep), dtype=torch.int32, device="cuda"))
+    call = lambda: m.bdlm_cache_evict(cache, W, ddst, keep, 2, 8, *out, workspace=ws)
+    codes = lambda: [t.clone() for t in (cache.k8.view(torch.uint8), cache.v8.view(torch.uint8), cache.k_scale,
+                                         cache.v_scale)]
+    saved = codes()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for k in range(4):
+        rng = np.random.default_rng(k)
+        Wn = rng.random(W.shape, dtype=np.float32)
+        lens = np.array([300 - 61 * k, 90 - 20 * k], np.int32)
+        W.copy_(torch.from_numpy(Wn))
+        cache.lens.copy_(torch.from_numpy(lens))
+        for t, s in zip((cache.k8.view(torch.uint8), cache.v8.view(torch.uint8), cache.k_scale, cache.v_scale), saved):
+            t.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        h = {x: v.copy() for x, v in c.items()}
+        h["lens"] = lens
+        rl, rw, rk = co.evict(h, Wn, dst, keep, 2, 8)
+        assert out[0].tolist() == rl.tolist() and np.array_equal(out[1].cpu().numpy(), rw)
+        assert np.array_equal(out[2].cpu().numpy(), rk)
+        for w in ("k", "v"):
+            assert np.array_equal(host_codes(getattr(cache, w + "8")), h[w + "8"])
+    m.bdlm_sync_status(ws)

@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "cached_attn.h"
@@ -866,7 +867,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (hi < kUnit) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mask32(a[x], hi - 32 * x);
+          for (int x = 0; x < 4; ++x) {
+            // (tiny queries on a block of tiny scale: 0 times -inf would be NaN)
+            if (f[x] == 0.f) f[x] = FLT_MIN;
+            mask32(a[x], hi - 32 * x);
+          }
         }
         const float mx = fmaxf(fmaxf(fmaf(max32(a[0]), f[0], lv[0]), fmaf(max32(a[1]), f[1], lv[1])),
                                fmaxf(fmaf(max32(a[2]), f[2], lv[2]), fmaf(max32(a[3]), f[3], lv[3])));

@@ -10,12 +10,28 @@ import numpy as np
 import pytest
 
 import oracle.cache_oracle as co
-from tests.cache_util import device_cache, host_codes, make_cache, make_rows
+from structured_mask_attention_gb300.inputs import bf16_round
+from tests.cache_util import device_cache, host_codes, make_cache, make_rows, offsets_of
 from tests.parity_util import to_dev
-from tests.test_gpu_cache import lib  # noqa: F401
+from tests.test_gpu_cache import check_attn, lib  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [1, 20, 40, 150])
+@pytest.mark.parametrize("page,L", [(128, 168), (32, 128 + 32 + 7)])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+def test_attn_tiny_queries_on_a_block_of_zeros(lib, rows, page, L, o_dtype):
+    """A key block of zeros has the scale 2^-64; with a query of 2^-90 the product
+    of both scales is below the smallest fp32 number, in a tile that ends inside."""
+    m = lib
+    c, _ = make_cache([L], L, 1, 64, page, seed=3)
+    last = c["table"][0, 128 // page:]
+    c["k8"][last], c["ks"][last] = 0, 2.0 ** -64
+    Q = bf16_round(make_rows(rows, 2, 64, 1) * np.float32(2.0 ** -90))
+    O, LSE = m.bdlm_attn_cached(to_dev(Q, torch), None, None, device_cache(m, torch, c), o_dtype=o_dtype)
+    check_attn(O, LSE, co.attn(c, Q, None, None, offsets_of([rows]), 0.125), 64, o_dtype == torch.bfloat16)
 
 
 @pytest.mark.parametrize("scale", [2.0 ** -70, math.nan])

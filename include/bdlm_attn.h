@@ -429,9 +429,11 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
  * and Vn are null, to the rows of their own sequence:
  *   O_i = sum_j exp(s_ij - LSE_i) v_j,  s_ij = scale q_i . k_j,  LSE natural log.
  * Qn [rows, Hq, d], Kn, Vn [rows, Hkv, d] bf16; O [rows, Hq, d] in o_dtype;
- * LSE [Hq, rows] fp32.  A row without a key gets O = 0, LSE = -inf.  For a
- * bf16 output the probabilities are rounded to 16 bits; for an fp32 one they
- * enter the product with V in several 16-bit parts (off by 2^-22 at most).
+ * LSE [Hq, rows] fp32.  A row without a key gets O = 0, LSE = -inf.  A
+ * cached key's weight times value scale meets its codes off by at most 2^-11 of
+ * itself and 2^-34 of the row's largest; an own key's weight off by 2^-8 of itself;
+ * for an fp32 output, in several 16-bit parts, both by 2^-22 of themselves and
+ * 2^-34 of the largest.  The row sum and LSE take the weights in fp32.  (The value scales that a row sees may differ by 2^100.)
  * O must not overlap Qn, Kn or Vn.
  * Deterministic: the keys are split over the GPU by their number, and the
  * parts are joined in a fixed order. */

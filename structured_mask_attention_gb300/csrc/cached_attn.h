@@ -36,10 +36,19 @@ __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (i
 // kernel; 64 rows (16 sequences of up to 8192): 118 us here, 87 there.
 constexpr int kSmallRows = 32;
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
-// (fp32 outputs) Weights are kept 2^7 larger than exp2(s - maximum): the smallest
-// step of their second fp16 part, 2^-24, is so much finer against the many small
-// ones of a long row.
-constexpr float kFineShift = 7.0f;
+// Weights are kept in fp16, 2^shift larger than exp2(s - reference): the largest
+// come near 2^16, its end, and its range lies below them.  The mma.sync kernel has
+// the exact running maximum for a reference: a weight keeps 11 bits down to 2^-29
+// of the row's largest and counts down to 2^-40.  The tcgen05 kernels' reference
+// may lie kRescale behind the maximum (and a tenth of a bit for rounding): 11
+// bits down to 2^-23 of the reference, something down to 2^-34.  Such weights make up O
+// where one key dominates a row and has a small value, an attention sink.  The
+// rarer the rescaling, the less range: steps of 8 / 7 / 6 / 5 / 4 took 87.0 / 87.3 / 88.2 /
+// 89.6 / 90.5 us for blocks of 32 and 225 / 228 / 229 / 231 / 232 for blocks of 128; 512
+// were level.  The row sum takes p' 2^-shift.
+constexpr float kRescale = 6.9f;  // log2 units: the tcgen05 kernels' reference moves in steps of at least this
+constexpr float kSmallShift = 15.0f, kTcShift = 9.0f;
+constexpr float kSmallUnshift = 1.0f / (1 << (int)kSmallShift), kTcUnshift = 1.0f / (1 << (int)kTcShift);
 
 // Row tile of a call whose sequences have at most `flat` rows times heads of
 // a group: 16 or 32 (mma.sync), 128 or 256 (tcgen05, split and pairs).  Split

@@ -87,10 +87,10 @@ struct State {
 //
 // Value scales.  A cached key's score comes with log2 of its value block's
 // scale added: p' = exp2(s + log2 vs - m) is then the weight of the codes
-// themselves (O = sum p' code, at the fp16 precision of the largest weight
-// whatever the scales), and the row sum takes p' / vs (iv).  In units of
-// exp2(m), O / l is the attention's output and m + log2 l its LSE.
-template <int HD, int N8, bool FINE>
+// themselves (O = sum p' code, whatever the scales), and the row sum takes
+// p' / vs (iv).  In units of exp2(m), O / l is the attention's output and
+// m + log2 l its LSE.  The weights carry 2^kSmallShift (iv its inverse).
+template <int HD, int N8>
 __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], const float (&iv)[N8 / 2]) {
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -101,7 +101,7 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float mn = fmaxf(st.m[r], mx);
     const float base = mn == -INFINITY ? 0.f : mn;  // no key yet: every p below is 0
-    const float alpha = ex2_approx(st.m[r] - base), less = FINE ? base - kFineShift : base;
+    const float alpha = ex2_approx(st.m[r] - base), less = base - kSmallShift;
     if (__any_sync(0xffffffffu, mn != st.m[r])) {
 #pragma unroll
       for (int j = 0; j < HD / 8; ++j) {
@@ -137,13 +137,13 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
 // and thread g's piece of V is chunk perm(g): the eight lanes of a load phase
 // then touch all 32 banks.  (HD = 64, 64-byte swizzle: perm is the identity.)
 //
-// P is rounded to fp16 (2^-11) for cached keys and bf16 for own ones, below a
-// bf16 output's own rounding.  FINE, for an fp32 output: P goes in two (three)
+// P is rounded to fp16 for cached keys (2^-11, of weights down to 2^-29 of the
+// largest) and bf16 for own ones (2^-8).  FINE, for an fp32 output: P goes in two (three)
 // parts, each what the rounding of the one before left, so that O is off by
 // fp32 sums alone; and the products of 16 keys are added to O by the threads: the
 // tensor cores cut their sums off instead of rounding them, always towards zero,
 // which over 600 products in a row came to 9e-6 of O.
-struct SInfo {  // of each 16 keys of a tile: K's scale, log2 and inverse of V's (1, 0, 1 without a page)
+struct SInfo {  // of each 16 keys of a tile: K's scale, log2 and 2^-shift times the inverse of V's (scale 1 without a page)
   float s[8], lv[8], iv[8];
   int gone;     // bit x: no page
 };
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
         if (4 * b + grp < n) {
           si.s[x] = sk;
           si.lv[x] = log2f(sv);
-          si.iv[x] = 1.f / sv;
+          si.iv[x] = kSmallUnshift / sv;
           if (x == 0) si.gone = (int)((none >> lane) & 0xffu);
         }
         __syncwarp();  // (before the arrivals that tell of them)
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           __syncwarp();
           if (lane == 0) mbar_arrive(KE(slot));
         }
-        softmax_step<HD, 4, FINE>(st, s, iv);
+        softmax_step<HD, 4>(st, s, iv);
         uint32_t pa[2][4], pr[2][4];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             s[i][e] = key0 + 8 * i + 2 * t + (e & 1) < seg.v.rows ? s[i][e] * p.sl2 : -INFINITY;
-        const float one[1] = {1.f};
-        softmax_step<HD, 2, FINE>(st, s, one);
+        const float one[1] = {kSmallUnshift};
+        softmax_step<HD, 2>(st, s, one);
         uint32_t pa[4], pr[4], pq[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (t == 0) {
-        red_ml[warp][g + 8 * r][0] = FINE ? st.m[r] - kFineShift : st.m[r];  // the weights' reference
+        red_ml[warp][g + 8 * r][0] = st.m[r];
         red_ml[warp][g + 8 * r][1] = l;
       }
       // tile j, element e: column HD / 8 perm(2 t + e) + j
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
       if (tok >= seg.v.rows) continue;
       const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
       const int64_t o0 = ((seg.v.row0 + tok) * p.Hq + head) * HD;
-      const float inv = whole ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
+      const float inv = whole ? (L != 0.f ? kSmallUnshift / L : 0.f) : kSmallUnshift;
 #pragma unroll
       for (int k = 0; k < HD / 32; ++k) {
         const int col = c0 + 32 * k;

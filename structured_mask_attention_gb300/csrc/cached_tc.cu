@@ -14,8 +14,8 @@
 // two, so a warpgroup converts V's codes, without their scales, while the tensor
 // cores work on the tile before.  The scales join the scores: with log2 of its
 // value block's scale added to a key's score, p' = exp2(s + log2 vs - m) is the
-// weight of the codes themselves, at fp16's precision of the largest weight
-// whatever the scales, and the row sum takes p' / vs: a few operations per
+// weight of the codes themselves, whatever the scales (in fp16 with a shift that
+// cached_attn.h explains), and the row sum takes p' / vs: a few operations per
 // block of keys and row.  (In bf16, V's values code * scale cost five
 // instructions for two, as much issue as the softmax; P in two e4m3 parts
 // would triple the exponentials' cost.)  For an fp32 output P goes in two
@@ -63,7 +63,6 @@ constexpr int kRegsControl = 72, kRegsConvert = 40, kRegsSoftmax = 200;
 constexpr int kLaunchRegs = 128;
 static_assert(128 * (kRegsControl + kRegsConvert) + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
               "register split exceeds the block");
-constexpr float kRescale = 8.0f;  // log2 units: the reference maximum moves in steps of at least this
 // (fp32 outputs) Key tiles that a sub-tile adds up on the tensor cores.  1 / 2 / 4 /
 // all of about 90: O off by 1.0 / 1.2 / 1.6 / 8.9e-6 of its size over 19357 keys
 // (fp32 products in torch: 2.6e-6); blocks of 128 of the case above as fp32, with 1 /
@@ -79,7 +78,7 @@ enum { B_QF = 0, B_KF = 2, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + 2, 
        B_ML = B_P2 + 2, B_KI = B_ML + 1, B_PCF = B_KI + NI, B_PCE = B_PCF + 4, B_COUNT = B_PCE + 4 };
 
 // What the softmax and the conversion need of a tile.  s, lv, iv: K's scale, log2
-// and inverse of V's (1, 0, 1 where there is no page), [0][x] of keys 32 x ..
+// and 2^-shift times the inverse of V's (scale 1 where there is no page), [0][x] of keys 32 x ..
 // 32 x + 15 and [1][x] of the 16 behind them.
 struct alignas(16) KInfo {
   float s[2][4], lv[2][4], iv[2][4];
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (on) {
               ki.s[x & 1][x >> 1] = sk;
               ki.lv[x & 1][x >> 1] = log2f(sv);
-              ki.iv[x & 1][x >> 1] = 1.f / sv;
+              ki.iv[x & 1][x >> 1] = kTcUnshift / sv;
             }
             if (on && x == 0) {
               ki.fine = (((gone | odd) >> lane) & 0xffu) != 0;
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = (int)(pp->row0 + (int64_t)(pp->l0 + l) * kUnit);
           if (!isV) {
             KInfo& ki = kinfo[tc % NI];
-            if (lane < 4) ki.s[0][lane] = ki.iv[0][lane] = 1.f, ki.lv[0][lane] = 0.f;
+            if (lane < 4) ki.s[0][lane] = 1.f, ki.iv[0][lane] = kTcUnshift, ki.lv[0][lane] = 0.f;
             if (lane == 0) ki.fine = ki.gone = 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(B_KI + tc % NI));
@@ -884,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_ref = mx;
           rescale = true;
         }
-        const float nm = m_ref == -INFINITY ? 0.f : (FINE ? kFineShift : 0.f) - m_ref;
+        const float nm = m_ref == -INFINITY ? 0.f : kTcShift - m_ref;
         l *= alpha;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -940,9 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tcount += (uint32_t)n;
 
       // ---- the piece's result
-      // (the reference of the weights as they were kept)
-      const float m_kept = FINE ? m_ref - kFineShift : m_ref;
-      float w0 = 1.f, w1 = 0.f, M = m_kept, L = l;
+      float w0 = 1.f, w1 = 0.f, M = m_ref, L = l;
       const int n0 = KS ? (n + 1) / 2 : n, n1 = KS ? n / 2 : n;
       if (KS && n > 0) {
         // both sub-tiles' states of this row (O's first product of the piece waited
@@ -956,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           move_o(true);
           tc_fence_before();
         }
-        ml[t * 128 + row] = make_float2(m_kept, l);
+        ml[t * 128 + row] = make_float2(m_ref, l);
         mbar_arrive(BAR(B_ML));
         ok = mbar_wait(BAR(B_ML), mlc & 1, wd, 46);
         ok = __all_sync(0xffffffffu, ok);
@@ -981,11 +978,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_after();
-      const float inv = L != 0.f ? 1.f / L : 0.f;
       const bool whole = pp->whole;
+      const float inv = whole ? (L != 0.f ? kTcUnshift / L : 0.f) : kTcUnshift;
       const Row r = my_row();
       const bool live = r.live;
-      const float s0 = whole ? w0 * inv : w0, s1 = whole ? w1 * inv : w1;
+      const float s0 = w0 * inv, s1 = w1 * inv;
       float* slot = p.part + (2 * (int64_t)blockIdx.x + (pp->first ? 1 : 0)) * part_floats(kTileRows, HD);
       const int prow = (KS ? 0 : t * 128) + row;
       const int64_t oofs = (r.at * p.Hq + r.head) * HD;

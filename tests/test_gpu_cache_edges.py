@@ -13,10 +13,80 @@ import oracle.cache_oracle as co
 from structured_mask_attention_gb300.inputs import bf16_round
 from tests.cache_util import device_cache, host_codes, make_cache, make_rows, offsets_of
 from tests.parity_util import to_dev
-from tests.test_gpu_cache import check_attn, lib  # noqa: F401
+from tests.test_gpu_cache import check_attn, lib, score_error  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
+
+
+def sink_case(L, d, rows, nats, seed, at=0, value=0.0):
+    """One key of ``nats`` more than the others' mean score for every query, its value ``value`` times
+    the others'; 2 heads on one KV head, pages of 64."""
+    c, _ = make_cache([L], L, 1, d, 64, seed)
+    Q = make_rows(rows, 2, d, seed + 1)
+    pages = c["table"][0, : -(-L // 64)]
+    c["k8"][pages, :, :, :8] = 0                     # channels 0 to 7 are the sink's alone
+    pg, slot = c["table"][0, at // 64], at % 64
+    Q[:, :, :8] = bf16_round(np.float32(nats * math.sqrt(d) / (8 * 1.25)))
+    c["k8"][pg, 0, slot] = 0
+    c["k8"][pg, 0, slot, :8] = co.encode(1.25 / c["ks"][pg, 0])
+    c["v8"][pg, 0, slot] = co.encode(co.E4M3[c["v8"][pg, 0, slot]] * value)
+    return c, Q
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40, 150])   # mma.sync in tiles of 16 and 32, tcgen05 split and in pairs
+@pytest.mark.parametrize("nats,at", [(14, 0), (18, 0), (20, 0), (18, 3900)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_sink_without_a_value(lib, rows, nats, at, d):
+    """The others' weights, 2^-20 to 2^-29 of the largest one, are all of O.  (The
+    row's 4096 keys are in one CTA's piece.)"""
+    m = lib
+    n = 152 * (2 if 2 * rows <= 32 else 1)           # sequences on the same pages: one or two for each CTA
+    c, Q = sink_case(4096, d, rows, nats, seed=nats + rows, at=at)
+    c["table"], c["lens"] = np.repeat(c["table"], n, 0), np.repeat(c["lens"], n)
+    O, LSE = m.bdlm_attn_cached(to_dev(np.concatenate([Q] * n), torch), None, None, device_cache(m, torch, c))
+    one = {**c, "table": c["table"][:1], "lens": c["lens"][:1]}
+    ref = co.attn(one, Q, None, None, offsets_of([rows]), 1 / math.sqrt(d))
+    # of O: bf16's rounding, 2^-9 at most in the mean, and each weight's in fp16, evenly spread and unlike in sign, 2^-11
+    # of it and at least 2^-25 of the row's largest weight 1 times 2^9 (pages' scales: at most 4 times that): its root
+    # mean square, by that of the weights
+    z = Q[0, 0].astype(np.float64) @ co.tokens(one, "k", 0, 0).T / math.sqrt(d)
+    p = np.delete(np.exp(z - z.max()), at)
+    limit = math.sqrt(2.0 ** -18 + 2.0 ** -22 + (4 * 2.0 ** -34 / math.sqrt(3) / math.sqrt((p ** 2).mean())) ** 2)
+    for s in (0, n // 2, n - 1):
+        o = O[s * rows:(s + 1) * rows]
+        check_attn(o, LSE[:, s * rows:(s + 1) * rows], ref, d, True)
+        rel = np.linalg.norm(o.double().cpu().numpy() - ref[0]) / np.linalg.norm(ref[0])
+        print(f"  O off by {rel:.2e} of its size")
+        assert rel <= 1.25 * limit
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40, 150])
+@pytest.mark.parametrize("value", [0.0, 0.02, 1.0])
+def test_attn_fp32_of_weights_far_apart(lib, rows, value):
+    """fp32 outputs: a weight enters to 2^-22 of itself and 2^-34 of the row's
+    largest weight times its value block's scale."""
+    m = lib
+    d, L = 128, 4096
+    n = 152 * (2 if 2 * rows <= 32 else 1)
+    c, Q = sink_case(L, d, rows, 16, seed=7 + rows, value=value)
+    c["table"], c["lens"] = np.repeat(c["table"], n, 0), np.repeat(c["lens"], n)
+    O, LSE = m.bdlm_attn_cached(to_dev(np.concatenate([Q] * n), torch), None, None, device_cache(m, torch, c),
+                                o_dtype=torch.float32)
+    one = {**c, "table": c["table"][:1], "lens": c["lens"][:1]}
+    Or, Lr, A, E = co.attn(one, Q, None, None, offsets_of([rows]), 1 / math.sqrt(d))
+    # the floor: 2^-34 (largest p vs) |code_j| summed over j; scales differ by 4 at most, p <= 1
+    floor = 4 * 2.0 ** -34 * np.abs(co.tokens(one, "v", 0, 0)).sum(0)
+    ds = score_error(d, E)
+    for s in (0, n - 1):
+        o = O[s * rows:(s + 1) * rows].double().cpu().numpy()
+        tol = (2.0 ** -22 + 2 * ds.T[:, :, None]) * A + floor
+        worst = (np.abs(o - Or) / tol).max()
+        rel = np.linalg.norm(o - Or) / np.linalg.norm(Or)
+        print(f"  O {worst:.3f} of its tolerance, off by {rel:.2e} of its size")
+        assert worst <= 1
+        lse = LSE[:, s * rows:(s + 1) * rows].double().cpu().numpy()
+        assert (np.abs(lse - Lr) <= ds + 2.0 ** -22 * (1 + np.abs(Lr))).all()
 
 
 @pytest.mark.parametrize("rows", [1, 20, 40, 150])

@@ -433,7 +433,10 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
  * cached key's weight times value scale meets its codes off by at most 2^-11 of
  * itself and 2^-34 of the row's largest; an own key's weight off by 2^-8 of itself;
  * for an fp32 output, in several 16-bit parts, both by 2^-22 of themselves and
- * 2^-34 of the largest.  The row sum and LSE take the weights in fp32.  (The value scales that a row sees may differ by 2^100.)
+ * 2^-34 of the largest.  The row sum and LSE take the weights in fp32.
+ * Scores are fp32 sums of products with the queries as they are, or, for more
+ * than 32 rows times heads of a group and in bdlm_cache_weights, with queries
+ * whose elements below 2^-13 of the row's largest are off by up to 2^-21 of it.  (The value scales that a row sees may differ by 2^100.)
  * O must not overlap Qn, Kn or Vn.
  * Deterministic: the keys are split over the GPU by their number, and the
  * parts are joined in a fixed order. */

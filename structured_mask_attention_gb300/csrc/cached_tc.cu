@@ -2,12 +2,12 @@
 // sm_103a tensor cores.
 //
 // S = Q K^T without touching K's codes: a bf16 query has 8 significant bits, so
-// it is the exact sum of two e4m3 values of 4 bits each, and
+// it is the sum of an e4m3 value of 4 bits and an e5m2 value of 3, and
 // S = Qhi K^T + Qlo K^T are two kind::f8f6f4 products that cost together what
-// one bf16 product would (e4m3 runs at twice its rate), with K's tiles taken
+// one bf16 product would (8-bit types run at twice its rate), with K's tiles taken
 // as TMA leaves them.  (Each row of Q is first scaled by a power of two that
 // puts its largest magnitude into [128, 256): exact for elements down to
-// 2^-10 of it, off by at most 2^-18 of it below.)  Scores meet the key
+// 2^-13 of it, off by at most 2^-21 of it below; split_f8.)  Scores meet the key
 // blocks' scales in the softmax, one multiplication per block that the
 // exponent's fma absorbs.
 // P V runs in fp16: an e4m3 code is exact in fp16 and one instruction turns
@@ -88,7 +88,7 @@ struct alignas(16) KInfo {
 
 template <int HD>
 struct Lay {
-  static constexpr int kQ = 0;                    // two regions of 128 rows x HD bf16 (or two e4m3 parts)
+  static constexpr int kQ = 0;                    // two regions of 128 rows x HD bf16 (or its two 8-bit parts)
   static constexpr int kQBytes = 128 * HD * 2;
   static constexpr int kK = 2 * kQBytes;
   static constexpr int kV = kK + NK * kSlot;      // codes of V, 2 slots
@@ -120,7 +120,7 @@ constexpr int NP = 4;  // ring slots
 
 // A tile's 128 query rows (first: the first as token * group + head of the
 // group), by the TEAM threads of one or both sub-tiles: 16-byte copies, all in
-// flight at once, then, for the e4m3 parts, each thread turns the 32 bytes that it
+// flight at once, then, for the 8-bit parts, each thread turns the 32 bytes that it
 // copied to where their 16 + 16 codes go.  Loops that are not unrolled: this
 // runs once or twice in a CTA's life, and instructions that no CTA has fetched
 // yet cost more (about 25 cycles each) than the loops' own.
@@ -158,7 +158,7 @@ __device__ __forceinline__ void put_rows(const CachedParams& p, const Piece* pp,
       for (int o = PER / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       float inv;
       const float f = row_factor(amax, inv);
-      split_e4m3(w, f, hi, lo);
+      split_f8(w, f, hi, lo);
       st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
       st_shared_v4(at + 128 * HD, lo[0], lo[1], lo[2], lo[3]);
       if (i == 0) factor[r] = p.sl2 * inv;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ---------------------------------------------- MMA issue
       if (lane == 0) {
-        constexpr uint32_t kId8 = idesc_e4m3(128, 128);
+        constexpr uint32_t kId8[2] = {idesc_f8(128, 128, kE4m3, kE4m3), idesc_f8(128, 128, kE5m2, kE4m3)};  // Q's parts
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true);    // own keys
         constexpr uint32_t kIdO16 = kIdO & ~((1u << 7) | (1u << 10));  // cached keys: fp16 P and V
@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t q = desc_lo(base + LY::kQ + (KS ? 0 : t) * LY::kQBytes, 16);
             const uint32_t k = desc_lo(base + LY::kK + k0 * kSlot, 16);
 #pragma unroll
-            for (int kk = 0; kk < HD / 32; ++kk) mma_ss<true>(d, q + kk * 2, H, k + kk * 2, H, kId8, kk > 0);
+            for (int kk = 0; kk < HD / 32; ++kk) mma_ss<true>(d, q + kk * 2, H, k + kk * 2, H, kId8[0], kk > 0);
 #pragma unroll
-            for (int kk = 0; kk < HD / 32; ++kk) mma_ss<true>(d, q + 8 * HD + kk * 2, H, k + kk * 2, H, kId8, 1);
+            for (int kk = 0; kk < HD / 32; ++kk) mma_ss<true>(d, q + 8 * HD + kk * 2, H, k + kk * 2, H, kId8[1], 1);
           } else {
             constexpr uint32_t H = desc_hi(2, 1024);
 #pragma unroll
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_commit(BAR(B_WE + vs));
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk)
-                  mma_ss<true>(tmem + t * 128, q + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ, kt + (kk % n8) * 2, HQ, kId8,
+                  mma_ss<true>(tmem + t * 128, q + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ, kt + (kk % n8) * 2, HQ, kId8[kk / n8],
                                kk > 0);
                 tc_commit(BAR(B_SF + t));
                 tc_commit(BAR(B_KE + ks));
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                   constexpr int n8 = HD / 32;
-                  mma_ss<true>(tmem, q + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ, kt + (kk % n8) * 2, HQ, kId8, kk > 0);
+                  mma_ss<true>(tmem, q + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ, kt + (kk % n8) * 2, HQ, kId8[kk / n8], kk > 0);
                 }
                 tc_commit(BAR(B_SF + 0));
                 ok = mbar_wait(BAR(B_PF + 1), pph & 1, wd, 31);
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kk = 0; kk < HD / 16; ++kk) {
                   constexpr int n8 = HD / 32;
                   mma_ss<true>(tmem + 128, q + (LY::kQBytes >> 4) + (kk / n8) * 8 * HD + (kk % n8) * 2, HQ,
-                               kt + (kk % n8) * 2, HQ, kId8, kk > 0);
+                               kt + (kk % n8) * 2, HQ, kId8[kk / n8], kk > 0);
                 }
                 tc_commit(BAR(B_SF + 1));
                 tc_commit(BAR(B_KE + ks));
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.at = pp->row0 + (r.live ? tok : 0);
         return r;
       };
-      // Q's rows to shared memory, HD / 16 (HD / 8) lanes to a row: e4m3 in two
+      // Q's rows to shared memory, HD / 16 (HD / 8) lanes to a row: 8 bits in two
       // parts with the rows' factors, or bf16.  Pairs: the sub-tile's 128 rows by its
       // threads; split: the tile's 128 rows by both sub-tiles' threads.
       constexpr int kTeam = KS ? 256 : 128;

@@ -1,5 +1,5 @@
 // cached_tc.cuh -- what the cache's tcgen05 kernels share: operand descriptors,
-// e4m3 products, bulk copies, a query row as two e4m3 parts.
+// 8-bit products, bulk copies, a query row as two 8-bit parts.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -20,7 +20,7 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, int lbo) {
   return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(lbo >> 4) << 16);
 }
 
-// D[tmem] (+)= A[smem] B[smem]: e4m3, K = 32 (F8), or bf16, K = 16.
+// D[tmem] (+)= A[smem] B[smem]: 8-bit types, K = 32 (F8), or bf16, K = 16.
 template <bool F8>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi,
                                        uint32_t idesc, uint32_t acc) {
@@ -46,9 +46,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uin
       "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(acc)
       : "memory");
 }
-// fp32 accumulator, e4m3 A and B (format 0), both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// kind::f8f6f4, fp32 accumulator, both operands K-major, each of its own format:
+// e4m3 (0) or e5m2 (1).
+constexpr int kE4m3 = 0, kE5m2 = 1;
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a, int b) {
+  return (1u << 4) | ((uint32_t)a << 7) | ((uint32_t)b << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Contiguous copy into shared memory (16-byte aligned, a multiple of 16 bytes).
@@ -69,9 +71,15 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Sixteen values of a bf16 query row, times f, as the 16-byte chunks of its two
-// e4m3 parts: hi the nearest e4m3 values, lo what that left.  (In fp16 the scaled
-// values are exact down to 2^-24, below e4m3's smallest step.)
-__device__ __forceinline__ void split_e4m3(const uint32_t* w, float f, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+// parts: hi the nearest e4m3 values, lo what that left, in e5m2.  A bf16 value has
+// 8 significant bits, hi rounds to 4: the rest is at most 8 units of the 8th bit,
+// which e5m2's 3 bits hold.  So the parts are exact for values from 2^-6 on, e4m3's
+// smallest normal one; below, hi's step is 2^-9, the rest at most 2^-10, and its
+// 3 bits leave 2^-14 at most.  Of a row's largest value, 2^7 to 2^8, that is: exact
+// down to 2^-13, off by 2^-21 below.  (lo in e4m3, whose smallest step is 2^-9:
+// exact down to 2^-9, off by 2^-17.  In fp16 the scaled values are exact down to
+// 2^-17 and off by 2^-25 below.)
+__device__ __forceinline__ void split_f8(const uint32_t* w, float f, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const __half2 v =
@@ -79,7 +87,7 @@ __device__ __forceinline__ void split_e4m3(const uint32_t* w, float f, uint32_t 
     const uint32_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
     const uint32_t back = e4m3x2_to_half2(h);
     const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
-    const uint32_t l = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(d), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t l = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(d), __NV_SATFINITE, __NV_E5M2);
     hi[k >> 1] = k & 1 ? hi[k >> 1] | h << 16 : h;
     lo[k >> 1] = k & 1 ? lo[k >> 1] | l << 16 : l;
   }
@@ -96,7 +104,7 @@ __device__ __forceinline__ float row_factor(uint32_t amax, float& inv) {
   return amax >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Byte offset of 16-byte chunk i of row r in a K-major e4m3 tile of HD columns
+// Byte offset of 16-byte chunk i of row r in a K-major 8-bit tile of HD columns
 // (128-byte swizzle; 64-byte for HD = 64).
 template <int HD>
 __device__ __forceinline__ uint32_t e4m3_chunk(int r, int i) {

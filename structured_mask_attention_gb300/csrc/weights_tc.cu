@@ -4,7 +4,7 @@
 //   W[j] += sum over rows i of exp(s_ij - LSE_i)
 // needs the sum of each *key* over all rows, so the scores are computed
 // transposed: K's tile of 128 keys is the first operand (its e4m3 codes as TMA
-// left them), the rows' queries the second (two e4m3 parts, cached_tc.cu), and
+// left them), the rows' queries the second (two 8-bit parts, cached_tc.cu), and
 // S^T has a key per TMEM lane.  A thread then owns a key: its block's scale is
 // a constant, the rows' factors and LSEs are read from shared memory by all
 // threads together, the sum stays in two registers, and no two threads ever
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         done(np);
         for (int r0 = 0; ok && r0 < flat; r0 += kChunk) {
           const int N = (min(flat - r0, kChunk) + 31) & ~31;
-          const uint32_t id = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);  // e4m3, M = 128
+          const uint32_t id = idesc_f8(128, N, kE4m3, kE4m3), id_lo = idesc_f8(128, N, kE4m3, kE5m2);
           ok = mbar_wait(BAR(B_QF), qph, wd, 62);
           qph ^= 1;
           if (!ok) break;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < HD / 32; ++kk) mma_ss<true>(tmem + buf * 256, k + kk * 2, H, q + kk * 2, H, id, kk > 0);
 #pragma unroll
             for (int kk = 0; kk < HD / 32; ++kk)
-              mma_ss<true>(tmem + buf * 256, k + kk * 2, H, q + (LY::kPart >> 4) + kk * 2, H, id, 1);
+              mma_ss<true>(tmem + buf * 256, k + kk * 2, H, q + (LY::kPart >> 4) + kk * 2, H, id_lo, 1);
             tc_commit(BAR(B_SF + buf));
             if (++slot == NK) slot = 0, kph ^= 1;
           }
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float inv;
             const float f = row_factor(amax, inv);
             uint32_t hi[4], lo[4];
-            split_e4m3(w, f, hi, lo);
+            split_f8(w, f, hi, lo);
             const uint32_t at = base + LY::kQ + e4m3_chunk<HD>(r, i);
             st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
             st_shared_v4(at + LY::kPart, lo[0], lo[1], lo[2], lo[3]);

@@ -90,3 +90,26 @@ def test_evict_keeps_sinks_recent_and_the_heaviest():
     assert Wout[0, 0, :7].tolist() == [0, 5, 1, 7, 9, 0, 0]
     c["table"], c["lens"] = dst, lens
     assert np.abs(co.tokens(c, "k", 0, 0) - x[[0, 1, 2, 3, 6, 9]]).max() <= 2.0 ** -10 * c["ks"][dst[0, 0], 0]
+
+
+def test_a_query_is_the_sum_of_its_two_8_bit_parts():
+    """What the tensor-core kernels multiply for a query row: its values, scaled
+    by a power of two into [128, 256), as the nearest e4m3 values plus the e5m2
+    values of what those left.  Exact down to 2^-13 of the largest, off by 2^-21 below."""
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn((20000, 64), generator=g) * torch.exp2(torch.rand((20000, 64), generator=g) * -30)
+    x[:, 0] = torch.randn(20000, generator=g) * 4
+    x = x.bfloat16().float()
+    top = x.abs().amax(1, keepdim=True)
+    v = (x * torch.exp2(7 - torch.floor(torch.log2(top)))).half().float()
+    hi = v.to(torch.float8_e4m3fn).float()
+    lo = (v - hi).half().to(torch.float8_e5m2).float()
+    off = (v.double() - hi.double() - lo.double()).abs()
+    largest = v.abs().amax(1, keepdim=True).double()
+    assert (largest >= 128).all() and (largest < 256).all()
+    assert (off[v.abs() >= 2.0 ** -13 * largest] == 0).all() and (off <= 2.0 ** -21 * largest).all()
+    # every significand of 8 bits, signs and all exponents from e4m3's smallest normal one on
+    v = (torch.arange(128, 256).float()[None] * torch.exp2(torch.arange(-13, 1).float())[:, None]).reshape(-1)
+    v = torch.cat([v, -v])
+    hi = v.to(torch.float8_e4m3fn).float()
+    assert torch.equal(hi + (v - hi).to(torch.float8_e5m2).float(), v)

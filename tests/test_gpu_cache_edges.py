@@ -104,6 +104,30 @@ def test_attn_tiny_queries_on_a_block_of_zeros(lib, rows, page, L, o_dtype):
     check_attn(O, LSE, co.attn(c, Q, None, None, offsets_of([rows]), 0.125), 64, o_dtype == torch.bfloat16)
 
 
+@pytest.mark.parametrize("rows", [1, 20, 40, 150])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("factor", [30.0, 100.0, 1000.0])
+def test_attn_and_weights_of_a_channel_of_another_size(lib, rows, d, factor):
+    """One channel of the queries is ``factor`` times the others."""
+    m = lib
+    L = 700
+    c, _ = make_cache([L], L, 1, d, 32, seed=5)
+    Q = make_rows(rows, 2, d, 1)
+    Q[:, :, 5] = bf16_round(Q[:, :, 5] * np.float32(factor))
+    sc, cache = 1 / math.sqrt(d), device_cache(m, torch, c)
+    sc *= 0.25 if factor < 200 else 0.025
+    O, LSE = m.bdlm_attn_cached(to_dev(Q, torch), None, None, cache, scale=sc, o_dtype=torch.float32)
+    ref = co.attn(c, Q, None, None, offsets_of([rows]), sc)
+    check_attn(O, LSE, ref, d, False)
+    W = torch.zeros((1, 1, c["table"].shape[1] * 32), device="cuda")
+    m.bdlm_cache_weights(to_dev(Q, torch), torch.from_numpy(ref[1].astype(np.float32)).cuda(), cache, W, scale=sc)
+    Wr, E = co.weights(c, Q, ref[1].astype(np.float32), offsets_of([rows]), sc, np.zeros(W.shape, np.float32))
+    rel = score_error(d, E) + 2.0 ** -23 * (1 + np.abs(ref[1]).max()) + (2 * rows + 4) * 2.0 ** -24
+    worst = (np.abs(W.double().cpu().numpy() - Wr) / (rel * Wr + 2.0 ** -24)).max()
+    print(f"  weights {worst:.3f} of their tolerance")
+    assert worst <= 1
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -70, math.nan])
 @pytest.mark.parametrize("page,d", [(16, 64), (64, 128), (128, 128)])
 def test_append_leaves_a_sequence_without_rows_alone(lib, scale, page, d):

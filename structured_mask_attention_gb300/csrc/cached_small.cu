@@ -544,10 +544,16 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
             for (int y = 0; y < 2; ++y) {
               const uint32_t sel = y ? 0x7632 : 0x5410;
               const uint32_t b0 = __byte_perm(x0[k], x1[k], sel), b1 = __byte_perm(y0[k], y1[k], sel);
-              mma_bf16(st.o[8 * w + 2 * k + y], pa[0], pa[1], pa[2], pa[3], b0, b1);
+              float (&o)[4] = st.o[8 * w + 2 * k + y];
               if (FINE) {
-                mma_bf16(st.o[8 * w + 2 * k + y], pr[0], pr[1], pr[2], pr[3], b0, b1);
-                mma_bf16(st.o[8 * w + 2 * k + y], pq[0], pq[1], pq[2], pq[3], b0, b1);
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_bf16(z, pa[0], pa[1], pa[2], pa[3], b0, b1);
+                mma_bf16(z, pr[0], pr[1], pr[2], pr[3], b0, b1);
+                mma_bf16(z, pq[0], pq[1], pq[2], pq[3], b0, b1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] += z[e];
+              } else {
+                mma_bf16(o, pa[0], pa[1], pa[2], pa[3], b0, b1);
               }
             }
           }

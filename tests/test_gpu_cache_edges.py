@@ -128,6 +128,31 @@ def test_attn_and_weights_of_a_channel_of_another_size(lib, rows, d, factor):
     assert worst <= 1
 
 
+@pytest.mark.parametrize("rows,Hq,local,chain", [(32, 1, True, 3), (16, 2, True, 3), (32, 1, False, 2)])
+@pytest.mark.parametrize("L", [0, 3000])
+def test_attn_fp32_output_with_own_keys(lib, rows, Hq, local, chain, L):
+    """mma.sync tiles, fp32 O: the tensor cores cut a sum off by up to 2^-23 of
+    it, always towards zero, 2/3 of its last size in the mean; the products of 16
+    keys, two (own keys: three) of their weights' parts, are added to O by the
+    threads, rounded.  2^-21 for the weights' and scores' own errors."""
+    m = lib
+    d, n = 128, 40
+    c, _ = make_cache([L], max(L, 1), 1, d, 64, seed=93)
+    c["table"], c["lens"] = np.repeat(c["table"], n, 0), np.repeat(c["lens"], n)
+    if not local and not L:
+        return
+    Q, K, V = (make_rows(n * rows, H, d, 3 + i) for i, H in enumerate((Hq, 1, 1)))
+    kv = (K, V) if local else (None, None)
+    dkv = [None if x is None else to_dev(x, torch) for x in kv]
+    O, LSE = m.bdlm_attn_cached(to_dev(Q, torch), *dkv, device_cache(m, torch, c), o_dtype=torch.float32)
+    ref = co.attn(c, Q, *kv, offsets_of([rows] * n), 1 / math.sqrt(d))
+    check_attn(O, LSE, ref, d, False)
+    diff = O.double().cpu().numpy() - ref[0]
+    rel = math.sqrt((diff ** 2).sum() / (ref[0] ** 2).sum())
+    print(f"  O off by {rel:.2e} of its size")
+    assert rel <= chain * 2.0 ** -23 * 2 / 3 + 2.0 ** -21
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -70, math.nan])
 @pytest.mark.parametrize("page,d", [(16, 64), (64, 128), (128, 128)])
 def test_append_leaves_a_sequence_without_rows_alone(lib, scale, page, d):

@@ -430,13 +430,13 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
  *   O_i = sum_j exp(s_ij - LSE_i) v_j,  s_ij = scale q_i . k_j,  LSE natural log.
  * Qn [rows, Hq, d], Kn, Vn [rows, Hkv, d] bf16; O [rows, Hq, d] in o_dtype;
  * LSE [Hq, rows] fp32.  A row without a key gets O = 0, LSE = -inf.  A
- * cached key's weight times value scale meets its codes off by at most 2^-11 of
- * itself and 2^-34 of the row's largest; an own key's weight off by 2^-8 of itself;
- * for an fp32 output, in several 16-bit parts, both by 2^-22 of themselves and
- * 2^-34 of the largest.  The row sum and LSE take the weights in fp32.
+ * key's weight times value scale meets its codes off by at most 2^-11 of itself
+ * and 2^-34 of the row's largest (an fp32 output: 2^-22 and 2^-34), own values
+ * counting as codes of up to 448 with a scale for each 128 rows; the row sum and
+ * LSE take the weights in fp32.  (Value scales that a row sees may differ by 2^100.)
  * Scores are fp32 sums of products with the queries as they are, or, for more
  * than 32 rows times heads of a group and in bdlm_cache_weights, with queries
- * whose elements below 2^-13 of the row's largest are off by up to 2^-21 of it.  (The value scales that a row sees may differ by 2^100.)
+ * whose elements below 2^-13 of the row's largest are off by up to 2^-21 of it.
  * O must not overlap Qn, Kn or Vn.
  * Deterministic: the keys are split over the GPU by their number, and the
  * parts are joined in a fixed order. */

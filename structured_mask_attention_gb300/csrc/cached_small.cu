@@ -70,6 +70,9 @@ __device__ __forceinline__ uint32_t rest_bf16x2(uint32_t hi, float a, float b) {
   return pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
 }
 
+// Two bf16 values, those that are not finite as 0.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) { return w & __vcmpltu2(w & 0x7fff7fffu, 0x7f807f80u); }
+
 // Barrier of the computing warps.
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
@@ -138,8 +141,9 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
 // then touch all 32 banks.  (HD = 64, 64-byte swizzle: perm is the identity.)
 //
 // P is rounded to fp16 for cached keys (2^-11, of weights down to 2^-29 of the
-// largest) and bf16 for own ones (2^-8).  FINE, for an fp32 output: P goes in two (three)
-// parts, each what the rounding of the one before left, so that O is off by
+// largest); own keys, whose bf16 values would not fit fp16, take it in two bf16
+// parts (2^-16), the second what the first's rounding left.  FINE, for an fp32
+// output: P goes in two (own keys: three) parts, so that O is off by
 // fp32 sums alone; and the products of 16 keys are added to O by the threads: the
 // tensor cores cut their sums off instead of rounding them, always towards zero,
 // which over 600 products in a row came to 9e-6 of O.
@@ -520,10 +524,8 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
         for (int i = 0; i < 4; ++i) {
           const float a = s[i >> 1][2 * (i & 1)], b = s[i >> 1][2 * (i & 1) + 1];
           pa[i] = pack_bf16x2(a, b);
-          if (FINE) {
-            pr[i] = rest_bf16x2(pa[i], a, b);
-            pq[i] = rest_bf16x2(pr[i], a - bf_lo(pa[i]), b - bf_hi(pa[i]));
-          }
+          pr[i] = rest_bf16x2(pa[i], a, b);
+          if (FINE) pq[i] = rest_bf16x2(pr[i], a - bf_lo(pa[i]), b - bf_hi(pa[i]));
         }
 #pragma unroll
         for (int w = 0; w < HD / 64; ++w) {  // 8 columns of the thread's HD / 8 (16 bytes) at a time
@@ -544,16 +546,19 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
             for (int y = 0; y < 2; ++y) {
               const uint32_t sel = y ? 0x7632 : 0x5410;
               const uint32_t b0 = __byte_perm(x0[k], x1[k], sel), b1 = __byte_perm(y0[k], y1[k], sel);
+              // (the weights' rests may be 0 or negative: infinite values meet the first part alone)
+              const uint32_t c0 = finite2(b0), c1 = finite2(b1);
               float (&o)[4] = st.o[8 * w + 2 * k + y];
               if (FINE) {
                 float z[4] = {0.f, 0.f, 0.f, 0.f};
                 mma_bf16(z, pa[0], pa[1], pa[2], pa[3], b0, b1);
-                mma_bf16(z, pr[0], pr[1], pr[2], pr[3], b0, b1);
-                mma_bf16(z, pq[0], pq[1], pq[2], pq[3], b0, b1);
+                mma_bf16(z, pr[0], pr[1], pr[2], pr[3], c0, c1);
+                mma_bf16(z, pq[0], pq[1], pq[2], pq[3], c0, c1);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] += z[e];
               } else {
                 mma_bf16(o, pa[0], pa[1], pa[2], pa[3], b0, b1);
+                mma_bf16(o, pr[0], pr[1], pr[2], pr[3], c0, c1);
               }
             }
           }

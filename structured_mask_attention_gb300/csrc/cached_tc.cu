@@ -19,7 +19,7 @@
 // block of keys and row.  (In bf16, V's values code * scale cost five
 // instructions for two, as much issue as the softmax; P in two e4m3 parts
 // would triple the exponentials' cost.)  For an fp32 output P goes in two
-// parts, the second what the first's rounding left (own keys: bf16, three).
+// parts, the second what the first's rounding left.
 //
 // A CTA per SM takes its share of the units of 128 keys (cache.cuh).  Two
 // arrangements of the same roles:
@@ -34,7 +34,10 @@
 // 8-11 are the softmax of sub-tiles 0 and 1 (one row per thread), warps 12-15
 // convert V.  TMEM: S of sub-tile t at 128 t (P over it), O at 256 + 128 t.
 // The rows' own block (bf16 keys) follows the cached tiles of the last unit or
-// has units of its own; its Q is bf16, its V tile needs no conversion.
+// has units of its own; its Q is bf16, its V is converted in place, over a scale
+// that the K loader finds (P in bf16 beside bf16 values would be off by 2^-8: O of
+// blocks of 32 / 128 was off by 1.95 / 2.14e-3 of its size, of which bf16 outputs
+// alone are 1.66).
 //
 // What bounds it (16 / 8 heads of 128, merge included): a block of 512 over one
 // sequence of 131072 tokens takes 483 us, 1.14 PFLOP/s or 62 % of the measured
@@ -74,8 +77,8 @@ constexpr int NI = 16;            // tile-info slots (more than any two roles ar
 constexpr int kSlot = 128 * 128;  // bytes of a K slot, of a V slot and of a bf16 panel
 
 enum { B_QF = 0, B_KF = 2, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + 2, B_WF = B_VE + 2, B_WE = B_WF + 2,
-       B_SF = B_WE + 2, B_PF = B_SF + 2, B_OD = B_PF + 2, B_OE = B_OD + 2, B_FD = B_OE + 2, B_P2 = B_FD + 2,
-       B_ML = B_P2 + 2, B_KI = B_ML + 1, B_PCF = B_KI + NI, B_PCE = B_PCF + 4, B_COUNT = B_PCE + 4 };
+       B_SF = B_WE + 2, B_PF = B_SF + 2, B_OD = B_PF + 2, B_OE = B_OD + 2, B_ML = B_OE + 2,
+       B_KI = B_ML + 1, B_PCF = B_KI + NI, B_PCE = B_PCF + 4, B_COUNT = B_PCE + 4 };
 
 // What the softmax and the conversion need of a tile.  s, lv, iv: K's scale, log2
 // and 2^-shift times the inverse of V's (scale 1 where there is no page), [0][x] of keys 32 x ..
@@ -92,7 +95,7 @@ struct Lay {
   static constexpr int kQBytes = 128 * HD * 2;
   static constexpr int kK = 2 * kQBytes;
   static constexpr int kV = kK + NK * kSlot;      // codes of V, 2 slots
-  static constexpr int kW = kV + 2 * kSlot;       // fp16 (own keys: bf16) V, 2 slots of HD / 64 panels
+  static constexpr int kW = kV + 2 * kSlot;       // fp16 V, 2 slots of HD / 64 panels
   static constexpr int kWBytes = kSlot * (HD / 64);
   static constexpr int kBar = kW + 2 * kWBytes;
   static constexpr int kKI = kBar + ((8 * B_COUNT + 8 + 15) & ~15);
@@ -175,6 +178,46 @@ __device__ __noinline__ void put_rows_call(const CachedParams& p, const Piece* p
   put_rows<HD, TEAM, E4M3>(p, pp, tid, first, dst, factor);
 }
 
+// 2^x of a whole x in fp32's normal range.
+__device__ __forceinline__ float exp2_int(float x) { return __uint_as_float((uint32_t)((int)x + 127) << 23); }
+
+// log2 of the scale that own tile l's values get: V / scale is fp16, exact for
+// bf16 values down to 2^-25 of the tile's largest magnitude, which comes to
+// [2^8, 2^9) as in a cached block.  Only the sequence's own rows count, and of
+// them finite values (others stay what they are in fp16).  By the K loader's warp,
+// which would come late to the next tile's keys if each round of loads took its way
+// to L2: the lines are asked for first (block of 512: 501 -> 487 us).
+template <int HD>
+__device__ __forceinline__ float own_scale(const CachedParams& p, const Piece* pp, int l, int lane) {
+  constexpr int PER = HD / 8, STEP = 32 / PER;  // lanes to a row, rows at a time
+  const int first = (pp->l0 + l) * kUnit, n = min(pp->rows - first, kUnit);
+  const __nv_bfloat16* V =
+      static_cast<const __nv_bfloat16*>(p.V) + ((pp->row0 + first) * p.c.Hkv + pp->h) * HD + (lane % PER) * 8;
+  if (n > 16 * STEP)
+    for (int r = lane; r < n; r += 32)
+#pragma unroll
+      for (int x = 0; x < HD / 64; ++x)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(V - (lane % PER) * 8 + (int64_t)r * p.c.Hkv * HD + x * 64));
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int r0 = lane / PER; r0 < n; r0 += 8 * STEP) {  // (eight loads in flight)
+    uint4 w[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int r = r0 + x * STEP;
+      w[x] = r < n ? __ldg(reinterpret_cast<const uint4*>(V + (int64_t)r * p.c.Hkv * HD)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const uint32_t v[4] = {w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu, w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) m = __vmaxu2(m, v[y] & __vcmpltu2(v[y], 0x7f807f80u));
+    }
+  }
+  m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  return (float)max((int)(m >> 7) - 127 - 8, -96);
+}
+
 __device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
   float u[10];
 #pragma unroll
@@ -229,25 +272,28 @@ __device__ __forceinline__ void exp32(uint32_t (&a)[32], float f, float n, float
   s1 = x + y;
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
 // P lies over the S columns that it replaces, 32 keys by 32 keys: 16 packed
 // columns, then 16 of the second part (FINE).  Column of the 16 keys of PV
 // k-step kk:
 __device__ __forceinline__ uint32_t p_col(int kk) { return (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8); }
 
-// Packs 32 values to fp16 (bf16) at 16 columns of TMEM; REST: the values become what the rounding left.
-template <bool BF, bool REST>
+// Packs 32 values to fp16 at 16 columns of TMEM; REST: the values become what the rounding left.
+template <bool REST>
 __device__ __forceinline__ void store_p(uint32_t (&a)[32], uint32_t taddr) {
   uint32_t pk[16];
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     const float x = __uint_as_float(a[c]), y = __uint_as_float(a[c + 1]);
-    uint32_t w;
-    if (BF) w = pack_bf16x2(x, y);
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+    const uint32_t w = pack_f16x2(x, y);
     pk[c / 2] = w;
     if (REST) {
-      const float2 z = BF ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
-                          : __half22float2(*reinterpret_cast<const __half2*>(&w));
+      const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&w));
       a[c] = __float_as_uint(x - z.x);
       a[c + 1] = __float_as_uint(y - z.y);
     }
@@ -293,8 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(B_PF + i), 128);
       mbar_init(BAR(B_OD + i), 1);
       mbar_init(BAR(B_OE + i), KS ? 256 : 128);
-      mbar_init(BAR(B_FD + i), 1);
-      mbar_init(BAR(B_P2 + i), 128);
     }
     mbar_init(BAR(B_ML), 256);
     for (int i = 0; i < NP; ++i) {
@@ -406,13 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           id = id1; raw1 = raw2; sk = sk1; sv = sv1;
         }
-        // own tiles: K by panels through the K slots; V straight into the bf16 slot that its tile has
+        // own tiles: K by panels through the K slots; V straight into the fp16 slot that its tile has
         const int nl = pp->nl;
         for (int l = 0; ok && l < nl; ++l, ++tc) {
           const int row = (int)(pp->row0 + (int64_t)(pp->l0 + l) * kUnit);
           if (!isV) {
             KInfo& ki = kinfo[tc % NI];
-            if (lane < 4) ki.s[0][lane] = 1.f, ki.iv[0][lane] = kTcUnshift, ki.lv[0][lane] = 0.f;
+            const float lv = own_scale<HD>(p, pp, l, lane);
+            if (lane < 4) ki.s[0][lane] = 1.f, ki.iv[0][lane] = exp2_int(-lv) * kTcUnshift, ki.lv[0][lane] = lv;
             if (lane == 0) ki.fine = ki.gone = 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(B_KI + tc % NI));
@@ -495,14 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         constexpr uint32_t kId8[2] = {idesc_f8(128, 128, kE4m3, kE4m3), idesc_f8(128, 128, kE5m2, kE4m3)};  // Q's parts
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
-        constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true);    // own keys
-        constexpr uint32_t kIdO16 = kIdO & ~((1u << 7) | (1u << 10));  // cached keys: fp16 P and V
+        constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true) & ~((1u << 7) | (1u << 10));  // fp16 P and V
         uint32_t ks = 0, kph = 0;            // next K slot and its full parity
         // bit t of a mask: the parity of sub-tile t's next phase (in pairs both bits are equal, bit 0 alone is kept)
         uint32_t qph = 0;                    // Q (split: bit 0 of Q8, bit 1 of bf16 Q)
         uint32_t pph = 0;                    // P
         uint32_t oph = 3;                    // O left by the last piece (first wait passes)
-        uint32_t p2 = 0;                     // third part of P
         uint32_t wc = 0;                     // V tiles multiplied so far
         auto bit = [](uint32_t m, int t) { return (m >> (KS ? t : 0)) & 1; };
         auto flip = [](uint32_t& m, int t) {
@@ -551,16 +594,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // O_t += P_t V of V tile w
         // (col: 0 the first part of P, 16 the second)
-        auto pv = [&](int t, uint32_t w, uint32_t col, bool own, bool first) {
+        auto pv = [&](int t, uint32_t w, uint32_t col, bool first) {
           const uint32_t v = desc_lo(base + LY::kW + (w & 1) * LY::kWBytes, kSlot);
-          const uint32_t id = own ? kIdO : kIdO16;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + col + p_col(kk), v + kk * 128, desc_hi(2, 1024), id,
+            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + col + p_col(kk), v + kk * 128, desc_hi(2, 1024), kIdO,
                    (kk > 0 || !first) ? 1u : 0u);
         };
         // (first: the piece's first product; fresh: the last piece's O may still be read)
-        auto issue_pv = [&](int t, uint32_t w, bool own, bool first, bool fresh) {
+        auto issue_pv = [&](int t, uint32_t w, bool first, bool fresh) {
           if (!mbar_wait(BAR(B_PF + t), bit(pph, t), wd, 31)) return false;
           flip(pph, t);
           if (fresh) {
@@ -569,15 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if ((KS || t == 0) && !mbar_wait(BAR(B_WF + (w & 1)), (w >> 1) & 1, wd, 33)) return false;
           tc_fence_after();
-          pv(t, w, 0, own, first);
-          if (FINE) pv(t, w, 16, own, false);
-          if (FINE && own) {
-            tc_commit(BAR(B_FD + t));
-            if (!mbar_wait(BAR(B_P2 + t), bit(p2, t), wd, 34)) return false;
-            flip(p2, t);
-            tc_fence_after();
-            pv(t, w, 0, true, false);
-          }
+          pv(t, w, 0, first);
+          if (FINE) pv(t, w, 16, false);
           return true;
         };
         for (uint32_t np = 0; ok; ++np) {
@@ -621,10 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + p_col(kk), vt + kk * 128, HV, kIdO, kk > 0 ? 1u : acc);
 #pragma unroll
                 for (int kk = 0; kk < (FINE ? 8 : 0); ++kk)
-                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 16 + p_col(kk), vt + kk * 128, HV, kIdO16, 1);
+                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 16 + p_col(kk), vt + kk * 128, HV, kIdO, 1);
                 tc_commit(BAR(B_WE + vs));
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk)
@@ -643,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (; ok && j < n; ++j, ++wc) {
               const int t = j & 1;
-              ok = issue_pv(t, wc, own(j), j < 2, j < 2 && !opened);
+              ok = issue_pv(t, wc, j < 2, j < 2 && !opened);
               if (!ok) break;
               tc_commit(BAR(B_WE + (wc & 1)));
               if (j + 2 >= n) tc_commit(BAR(B_OD + t));
@@ -674,10 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                  mma_ts(tmem + 256, tmem + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+                  mma_ts(tmem + 256, tmem + p_col(kk), vt + kk * 128, HV, kIdO, kk > 0 ? 1u : acc);
 #pragma unroll
                 for (int kk = 0; kk < (FINE ? 8 : 0); ++kk)
-                  mma_ts(tmem + 256, tmem + 16 + p_col(kk), vt + kk * 128, HV, kIdO16, 1);
+                  mma_ts(tmem + 256, tmem + 16 + p_col(kk), vt + kk * 128, HV, kIdO, 1);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                   constexpr int n8 = HD / 32;
@@ -689,10 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                  mma_ts(tmem + 384, tmem + 128 + p_col(kk), vt + kk * 128, HV, kIdO16, kk > 0 ? 1u : acc);
+                  mma_ts(tmem + 384, tmem + 128 + p_col(kk), vt + kk * 128, HV, kIdO, kk > 0 ? 1u : acc);
 #pragma unroll
                 for (int kk = 0; kk < (FINE ? 8 : 0); ++kk)
-                  mma_ts(tmem + 384, tmem + 144 + p_col(kk), vt + kk * 128, HV, kIdO16, 1);
+                  mma_ts(tmem + 384, tmem + 144 + p_col(kk), vt + kk * 128, HV, kIdO, 1);
                 tc_commit(BAR(B_WE + (wc & 1)));
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
@@ -709,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool opened = nk > 1;
             for (; ok && j < n; ++j, ++wc) {
               const bool last = j == n - 1, swap = j + 1 == nk && !last;
-              ok = issue_pv(0, wc, own(j), j == 0, j == 0 && !opened);
+              ok = issue_pv(0, wc, j == 0, j == 0 && !opened);
               if (!ok) break;
               if (last) tc_commit(BAR(B_OD + 0));
               if (!last) {
@@ -717,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 issue_s(0, own(j + 1));
               }
-              ok = issue_pv(1, wc, own(j), j == 0, j == 0 && !opened);
+              ok = issue_pv(1, wc, j == 0, j == 0 && !opened);
               if (!ok) break;
               tc_commit(BAR(B_WE + (wc & 1)));
               if (last) {
@@ -740,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + tl + t * 128, tO = tmem + tl + 256;
-    uint32_t sc = 0, tcount = 0, itn[2] = {0, 0}, mlc = 0, qfc = 0, p2 = 0;
+    uint32_t sc = 0, tcount = 0, itn[2] = {0, 0}, mlc = 0, qfc = 0;
     bool ok = true;
     for (uint32_t np = 0; ok; ++np) {
       const Piece* pp = piece(np);
@@ -890,13 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s0, s1;
           exp32(a[x], f[x], nm + lv[x], s0, s1);
           l = fine ? fmaf(s0, iv[x], fmaf(s1, ki.iv[1][x], l)) : fmaf(s0 + s1, iv[x], l);
-          if (own) {
-            store_p<true, FINE>(a[x], tS + 32 * x);
-            if (FINE) store_p<true, true>(a[x], tS + 32 * x + 16);  // (leaves the third part in a)
-          } else {
-            store_p<false, FINE>(a[x], tS + 32 * x);
-            if (FINE) store_p<false, false>(a[x], tS + 32 * x + 16);
-          }
+          store_p<FINE>(a[x], tS + 32 * x);
+          if (FINE) store_p<false>(a[x], tS + 32 * x + 16);
         }
         // O is complete up to the tile before (S of this one was issued behind its product)
         if (__any_sync(0xffffffffu, rescale)) {
@@ -911,23 +941,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(BAR(B_PF + t));
-        if (FINE && own) {  // the third part, once the first two are multiplied
-          ok = mbar_wait(BAR(B_FD + t), p2 & 1, wd, 43);
-          ++p2;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int y = 0; y < 16; ++y)
-              pk[y] = pack_bf16x2(__uint_as_float(a[x][2 * y]), __uint_as_float(a[x][2 * y + 1]));
-            tmem_st16(tS + 32 * x, pk);
-          }
-          tc_fence_before();
-          mbar_arrive(BAR(B_P2 + t));
-        }
         if (!KS && j == nk - 1 && nl > 0) {  // the cached keys are through with Q's codes
           put_q16();
           fence_proxy_async_smem();
@@ -1048,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------ V's codes -> fp16
+    // ------------------------------------------------ V's codes, own keys' values -> fp16
     setmaxnreg_dec<kRegsConvert>();
     const int i = threadIdx.x - 384;
     constexpr int CH = HD / 16;             // 16-code chunks of a key
@@ -1096,10 +1109,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          // own tile, loaded as bf16: rows behind the sequence's belong to others
-          const int left = left_l - (j - nk) * kUnit;
-          if (i >= left)
-            for (int x = 0; x < HD / 8; ++x) st_shared_v4(dst + (x >> 3) * kSlot + i * 128 + (x & 7) * 16, 0, 0, 0, 0);
+          // own tile, loaded as bf16: key i's values over the tile's scale, in place (rows behind the sequence's
+          // belong to others: zero)
+          const bool mine = i < left_l - (j - nk) * kUnit;
+          const float f = exp2_int(-kinfo[w % NI].lv[0][0]);
+#pragma unroll 2
+          for (int x = 0; x < HD / 8; ++x) {
+            const uint32_t at = dst + (x >> 3) * kSlot + i * 128 + (((x ^ i) & 7) << 4);
+            const uint4 v = ld_shared_v4(at);
+            const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              h[y] = mine ? pack_f16x2(__uint_as_float(b[y] << 16) * f, __uint_as_float(b[y] & 0xffff0000u) * f) : 0u;
+            st_shared_v4(at, h[0], h[1], h[2], h[3]);
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(BAR(B_WF + slot));

@@ -13,7 +13,7 @@ import oracle.cache_oracle as co
 from structured_mask_attention_gb300.inputs import bf16_round
 from tests.cache_util import device_cache, host_codes, make_cache, make_rows, offsets_of
 from tests.parity_util import to_dev
-from tests.test_gpu_cache import check_attn, lib, score_error  # noqa: F401
+from tests.test_gpu_cache import HALF, check_attn, lib, score_error  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -151,6 +151,62 @@ def test_attn_fp32_output_with_own_keys(lib, rows, Hq, local, chain, L):
     rel = math.sqrt((diff ** 2).sum() / (ref[0] ** 2).sum())
     print(f"  O off by {rel:.2e} of its size")
     assert rel <= chain * 2.0 ** -23 * 2 / 3 + 2.0 ** -21
+
+
+@pytest.mark.parametrize("rows", [5, 20, 33, 60, 150, 300])  # (60 and more: own tiles of their own; 150, 300: several)
+@pytest.mark.parametrize("factor", [1.0, 2.0 ** -40, 2.0 ** 40])
+@pytest.mark.parametrize("L", [0, 200])
+def test_attn_own_keys_count_as_near_as_cached_ones(lib, rows, factor, L):
+    """bf16 outputs: an own key's weight is off by 2^-11 at most, its values, of
+    any size and unlike within a tile, by 2^-34 of the tile's largest."""
+    m = lib
+    d, Hq, n = 64, 2, 3
+    c, _ = make_cache([L] * n, max(L, 1), 1, d, 64, seed=17)
+    T = n * rows
+    Q, K = (make_rows(T, H, d, i) for i, H in ((1, Hq), (2, 1)))
+    V = make_rows(T, 1, d, 3) * np.exp2(np.random.default_rng(4).integers(-20, 1, (T, 1, d))).astype(np.float32)
+    V = bf16_round(V * np.float32(factor))
+    if L:
+        c["vs"] *= np.float32(factor)
+    O, LSE = m.bdlm_attn_cached(*(to_dev(x, torch) for x in (Q, K, V)), device_cache(m, torch, c))
+    Or, Lr, A, E = co.attn(c, Q, K, V, offsets_of([rows] * n), 1 / math.sqrt(d))
+    ds = score_error(d, E)
+    assert (np.abs(LSE.double().cpu().numpy() - Lr) <= ds + 2.0 ** -22 * (1 + np.abs(Lr))).all()
+    big = max(np.abs(V).max(), 448 * float(np.nanmax(c["vs"])) if L else 0.0)
+    tol = (2.0 ** -11 + 2 * ds.T[:, :, None]) * A + HALF * np.abs(Or) + 2.0 ** -33 * big * (L + rows)
+    worst = (np.abs(O.double().cpu().numpy() - Or) / tol).max()
+    print(f"  O {worst:.3f} of its tolerance")
+    assert worst <= 1
+
+
+@pytest.mark.parametrize("rows", [10, 20, 40, 150])
+def test_attn_own_values_that_are_not_finite_or_zero(lib, rows):
+    """An infinite value reaches its column of its own sequence's rows; zeros are zeros."""
+    m = lib
+    d = 64
+    c, _ = make_cache([70, 70, 0], 128, 1, d, 64, seed=19)
+    Q, K, V = (make_rows(3 * rows, H, d, 1 + i) for i, H in enumerate((2, 1, 1)))
+    V[3, 0, 7], V[5, 0, 9] = math.inf, math.nan
+    V[2 * rows:] = 0.0
+    cache = device_cache(m, torch, c)
+    for o_dtype in (torch.bfloat16, torch.float32):
+        O, LSE = m.bdlm_attn_cached(*(to_dev(x, torch) for x in (Q, K, V)), cache, o_dtype=o_dtype)
+        assert torch.isfinite(LSE).all()
+        if o_dtype == torch.bfloat16:
+            assert (O[:rows, :, 7] == math.inf).all()
+        else:  # (on tcgen05 the second part of a weight meets it too, and may be 0)
+            assert not torch.isfinite(O[:rows, :, 7]).any()
+        assert torch.isnan(O[:rows, :, 9]).all()
+        fine = np.setdiff1d(np.arange(d), [7, 9])
+        W = V.copy()
+        W[3, 0, 7] = W[5, 0, 9] = 0.0
+        ref = co.attn(c, Q, K, W, offsets_of([rows] * 3), 0.125)
+        check_attn(O[rows:], LSE[:, rows:], (ref[0][rows:], ref[1][:, rows:], ref[2][rows:], ref[3][:, rows:]), d,
+                   o_dtype == torch.bfloat16)
+        check_attn(O[:rows][:, :, fine], LSE[:, :rows], (ref[0][:rows][:, :, fine], ref[1][:, :rows],
+                                                         ref[2][:rows][:, :, fine], ref[3][:, :rows]), d,
+                   o_dtype == torch.bfloat16)
+        assert (O[2 * rows:] == 0).all()
 
 
 @pytest.mark.parametrize("scale", [2.0 ** -70, math.nan])

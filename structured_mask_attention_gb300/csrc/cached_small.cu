@@ -482,15 +482,9 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
     }
 
     // ---- the rows' own block (bf16), in groups of 16 keys
-    if (p.sp.local) {
-      int k0 = 0, k1 = 0;  // own keys of this piece
-      if (seg.ltiles == 0) {
-        if (je == seg.units) k1 = seg.v.rows;
-      } else {
-        k0 = max(jb - seg.ktiles, 0) * kUnit;
-        k1 = min(max(je - seg.ktiles, 0) * kUnit, seg.v.rows);
-      }
-      for (int key0 = k0 + 16 * kg; key0 < k1; key0 += 16 * KG) {
+    static_assert(kSmallRows <= kFoldRows, "the own block follows the last cached unit");
+    if (p.sp.local && je == seg.units) {
+      for (int key0 = 16 * kg; key0 < seg.v.rows; key0 += 16 * KG) {
         float s[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;

@@ -418,9 +418,9 @@ size_t bdlm_workspace_size_cache(int n_seqs, int Hq, int Hkv, int d, int64_t max
  * tokens keeps its scale if that is larger; else its old codes are rounded
  * to the new scale.  A block that takes in a NaN or an infinity gets a NaN
  * scale: every row that sees it reads NaN.  lens_out [n_seqs] (may be null)
- * gets lens + rows; it must not overlap lens, which is left as it is.  Pages
- * written by the call must belong to one sequence only, at one place of its
- * table. */
+ * gets lens + rows; it must not overlap lens, which is left as it is, row_offsets
+ * or page_table.  Pages written by the call must belong to one sequence only, at
+ * one place of its table; a sequence without new rows writes none. */
 bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* cache, const int32_t* row_offsets,
                               int64_t rows, int64_t max_rows, int32_t* lens_out, void* workspace, size_t ws_bytes,
                               bdlm_stream stream);
@@ -437,7 +437,7 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
  * Scores are fp32 sums of products with the queries as they are, or, for more
  * than 32 rows times heads of a group and in bdlm_cache_weights, with queries
  * whose elements below 2^-13 of the row's largest are off by up to 2^-21 of it.
- * O must not overlap Qn, Kn or Vn.
+ * O and LSE must not overlap each other, Qn, Kn or Vn.
  * Deterministic: the keys are split over the GPU by their number, and the
  * parts are joined in a fixed order. */
 bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, const bdlm_cache* cache,
@@ -449,7 +449,7 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
  *   weights[s, h, j] += sum_{i in rows of s} sum_{heads of h's group} exp(s_ij - LSE_i),
  * with the LSE of bdlm_attn_cached on the same rows.  Rows whose LSE is -inf
  * add nothing.  Deterministic.  max_rows * Hq / Hkv by max_pages * page, both in
- * tiles of 128, may be at most 2^30. */
+ * tiles of 128, may be at most 2^30.  weights must not overlap Qn or LSE. */
 bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cache* cache, const int32_t* row_offsets,
                                int64_t rows, int64_t max_rows, int Hq, float scale, float* weights, void* workspace,
                                size_t ws_bytes, bdlm_stream stream);
@@ -464,7 +464,8 @@ bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cach
  * lens_out [n_seqs] = min(lens, keep); weights_out gets the kept tokens'
  * weights and zero behind them; kept [n_seqs, Hkv, keep] (may be null) their
  * old positions and -1 behind them.  The old pages, page_table, lens and
- * weights are left as they are.  sinks + recent <= keep. */
+ * weights are left as they are; the outputs overlap none of them, dst_table or
+ * each other.  sinks + recent <= keep. */
 bdlm_status bdlm_cache_evict(const bdlm_cache* cache, const float* weights, const int32_t* dst_table, int64_t keep,
                              int64_t sinks, int64_t recent, int32_t* lens_out, float* weights_out, int32_t* kept,
                              void* workspace, size_t ws_bytes, bdlm_stream stream);

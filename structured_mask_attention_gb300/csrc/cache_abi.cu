@@ -100,6 +100,12 @@ bdlm_status check_apart(const char* out, const void* a, int64_t na, const char* 
   return BDLM_OK;
 }
 
+bdlm_status check_lens_out(const int32_t* lens_out, const bdlm_cache* c) {
+  const int64_t ns = 4 * (int64_t)c->n_seqs;
+  CACHE_CHECK(check_apart("lens_out", lens_out, ns, "the cache's lens (read throughout the call)", c->lens, ns));
+  return check_apart("lens_out", lens_out, ns, "page_table", c->page_table, ns * c->max_pages);
+}
+
 bdlm_status check_space(void* ws, size_t bytes, size_t need) {
   if (!ws) return abi_fail(BDLM_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
   CACHE_CHECK(check_ptr("workspace", ws, 16));
@@ -163,8 +169,9 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
       CACHE_CHECK(check_ptr("V", V, 16));
     }
     if (lens_out) CACHE_CHECK(check_ptr("lens_out", lens_out, 4));
-    if (lens_out && lens_out < cache->lens + cache->n_seqs && cache->lens < lens_out + cache->n_seqs)
-      return abi_fail(BDLM_ERR_INVALID_ARG, "lens_out overlaps the cache's lens, which the call reads throughout");
+    CACHE_CHECK(check_lens_out(lens_out, cache));
+    CACHE_CHECK(check_apart("lens_out", lens_out, 4 * (int64_t)cache->n_seqs, "row_offsets", row_offsets,
+                            4 * ((int64_t)cache->n_seqs + 1)));
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
     int sms;
     CACHE_CHECK(abi_device(&sms));
@@ -203,7 +210,11 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
     CACHE_CHECK(check_apart("O", O, no, "Qn", Qn, 2 * nq));
     CACHE_CHECK(check_apart("O", O, no, "Kn", Kn, 2 * nkv));
     CACHE_CHECK(check_apart("O", O, no, "Vn", Vn, 2 * nkv));
-    CACHE_CHECK(check_apart("LSE", LSE, 4 * rows * Hq, "O", O, no));
+    const int64_t nl = 4 * rows * Hq;
+    CACHE_CHECK(check_apart("LSE", LSE, nl, "O", O, no));
+    CACHE_CHECK(check_apart("LSE", LSE, nl, "Qn", Qn, 2 * nq));
+    CACHE_CHECK(check_apart("LSE", LSE, nl, "Kn", Kn, 2 * nkv));
+    CACHE_CHECK(check_apart("LSE", LSE, nl, "Vn", Vn, 2 * nkv));
     const int64_t flat = max_rows * (Hq / p.c.Hkv);
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(flat, p.c.d)));
     int sms;
@@ -270,6 +281,9 @@ bdlm_status bdlm_cache_weights(const void* Qn, const float* LSE, const bdlm_cach
     CACHE_CHECK(check_ptr("Qn", Qn, 16));
     CACHE_CHECK(check_ptr("LSE", LSE, 4));
     CACHE_CHECK(check_ptr("weights", weights, 16));
+    const int64_t nw = 4 * (int64_t)cache->n_seqs * cache->Hkv * cache->max_pages * cache->page;
+    CACHE_CHECK(check_apart("weights", weights, nw, "Qn", Qn, 2 * rows * Hq * p.c.d));
+    CACHE_CHECK(check_apart("weights", weights, nw, "LSE", LSE, 4 * rows * Hq));
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
     // a sequence's units are counted in 32 bits
     const int64_t tiles = (max_rows * (Hq / p.c.Hkv) + 127) / 128, units = ((int64_t)p.c.max_pages * p.c.page + 127) / 128;
@@ -315,14 +329,14 @@ bdlm_status bdlm_cache_evict(const bdlm_cache* cache, const float* weights, cons
     CACHE_CHECK(check_ptr("dst_table", dst_table, 4));
     CACHE_CHECK(check_ptr("lens_out", lens_out, 4));
     if (kept) CACHE_CHECK(check_ptr("kept", kept, 4));
-    const int64_t n = (int64_t)cache->n_seqs * cache->Hkv * cache->max_pages * cache->page;
-    if (weights_out < weights + n && weights < weights_out + n)
-      return abi_fail(BDLM_ERR_INVALID_ARG, "weights_out overlaps weights");
-    if (lens_out < cache->lens + cache->n_seqs && cache->lens < lens_out + cache->n_seqs)
-      return abi_fail(BDLM_ERR_INVALID_ARG, "lens_out overlaps the cache's lens, which the call reads throughout");
-    const int64_t tn = (int64_t)cache->n_seqs * cache->max_pages;
-    if (dst_table < cache->page_table + tn && cache->page_table < dst_table + tn)
-      return abi_fail(BDLM_ERR_INVALID_ARG, "dst_table overlaps the cache's page_table: tokens move to other pages");
+    const int64_t heads = (int64_t)cache->n_seqs * cache->Hkv, nw = 4 * heads * cache->max_pages * cache->page;
+    const int64_t nt = 4 * (int64_t)cache->n_seqs * cache->max_pages, ns = 4 * (int64_t)cache->n_seqs;
+    CACHE_CHECK(check_apart("weights_out", weights_out, nw, "weights", weights, nw));
+    CACHE_CHECK(check_lens_out(lens_out, cache));
+    CACHE_CHECK(check_apart("lens_out", lens_out, ns, "dst_table", dst_table, nt));
+    CACHE_CHECK(check_apart("dst_table (tokens move to other pages)", dst_table, nt, "page_table", cache->page_table, nt));
+    CACHE_CHECK(check_apart("kept", kept, 4 * heads * keep, "weights", weights, nw));
+    CACHE_CHECK(check_apart("kept", kept, 4 * heads * keep, "weights_out", weights_out, nw));
     CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + (kept ? 0 : kept_space(cache->n_seqs, cache->Hkv, keep))));
     int sms;
     CACHE_CHECK(abi_device(&sms));

@@ -71,6 +71,33 @@ def test_weights_units_fit_32_bits(lib):
         assert call(1) in (5, 6)                           # 2^30 pass (and there is no device)
 
 
+@pytest.mark.parametrize("kw", [dict(LSE=0x400000), dict(LSE=0x500000 - 60), dict(LSE=0x600000 + 1020)])
+def test_attn_lse_lies_apart_from_inputs(lib, kw):
+    """4 rows of 4 heads: 64 bytes of LSE; Q, K, V of 2048, 1024 and 1024."""
+    assert _attn(lib, **kw) == 1 and "LSE overlaps" in m.bdlm_last_error(), m.bdlm_last_error()
+
+
+@pytest.mark.parametrize("call,kw", [
+    ("append", dict(off=0x340000, lens_out=0x340010)), ("append", dict(lens_out=0x320000 + 4 * 31)),
+    ("weights", dict(W=0x400000 + 2032)), ("weights", dict(W=0x500000 - 4080)),
+    ("evict", dict(lens=0x350000 + 4 * 31)), ("evict", dict(kept=0x700000 + 4092)), ("evict", dict(kept=0x800000 - 2044)),
+    ("evict", dict(dst=0x320000 + 4 * 31)),
+])
+def test_outputs_lie_apart_from_inputs(lib, call, kw):
+    """4 sequences, 2 KV heads, 8 pages of 16: tables of 128 bytes, weights of 4096, kept (64) of 2048."""
+    c = _cache()
+    ref = ctypes.cast(ctypes.pointer(c), ctypes.c_void_p)
+    a = dict(off=None, lens_out=0x348000, Q=0x400000, LSE=0x500000, W=0x700000, dst=0x350000, lens=0x340000, kept=None)
+    a.update(kw)
+    if call == "append":
+        s = lib.bdlm_cache_append(0x400000, 0x500000, ref, a["off"], 4, 1, a["lens_out"], 0x900000, 256, None)
+    elif call == "weights":
+        s = lib.bdlm_cache_weights(a["Q"], a["LSE"], ref, None, 4, 1, 4, 0.125, a["W"], 0x900000, 256, None)
+    else:
+        s = lib.bdlm_cache_evict(ref, a["W"], a["dst"], 64, 4, 8, a["lens"], 0x800000, a["kept"], 0x900000, 1 << 20, None)
+    assert s == 1 and "overlaps" in m.bdlm_last_error(), (s, m.bdlm_last_error())
+
+
 def test_no_rows_is_no_work(lib):
     assert _attn(lib, off=0x340000, rows=0, Q=None, K=None, V=None) == 0
 

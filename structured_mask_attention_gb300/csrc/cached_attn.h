@@ -32,8 +32,9 @@ struct CachedParams {
 __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (int64_t)tile_rows * (d + 2); }
 
 // Rows up to which the mma.sync kernel takes a call.  16 sequences of up to 16384
-// tokens with 20 / 32 rows: 107 / 107 us here, 129 / 129 in the tcgen05
-// kernel; 64 rows (16 sequences of up to 8192): 118 us here, 87 there.
+// tokens with 20 / 32 rows: 108 / 108 us here, 128 / 127 in the tcgen05 kernel (in a
+// graph, warm); 64 rows (16 sequences of up to 8192): 118 us with tiles of 64 rows
+// here, when it was tried, 83 there.
 constexpr int kSmallRows = 32;
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
 // Weights are kept in fp16, 2^shift larger than exp2(s - reference): the largest
@@ -53,9 +54,9 @@ constexpr float kSmallUnshift = 1.0f / (1 << (int)kSmallShift), kTcUnshift = 1.0
 // Row tile of a call whose sequences have at most `flat` rows times heads of
 // a group: 16 or 32 (mma.sync), 128 or 256 (tcgen05, split and pairs).  Split
 // could serve any number of rows in tiles of 128; pairs read the keys half as
-// often but hold 256 rows.  Split against pairs: 106 / 111 us at 160 rows, 92 / 84
-// at 256 (8 sequences of up to 8192), 174 / 177 at 384, 250 / 226 at 640, 537 / 487
-// at 1024.
+// often but hold 256 rows.  Split against pairs (8 sequences of up to 8192, in a
+// graph, warm): 69 / 73 us at 160 rows, 79 / 78 at 256, 123 / 117 at 384, 213 / 188 at
+// 640, 374 / 260 at 1024.
 inline int cached_tile_rows(int64_t flat) {
   return flat <= 16 ? 16 : flat <= kSmallRows ? 32 : flat <= 128 ? 128 : 256;
 }
@@ -69,17 +70,17 @@ struct CachedMaps {
 };
 cudaError_t launch_cached_tc(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 // Longest cache, in tokens, up to which the mma.sync kernel gives each segment
-// one CTA, without a list to walk and a merge.  1 / 32 sequences of 8 KV heads:
-// whole against split 7.5 / 8.9 and 10.3 / 16.1 us at 256 tokens, 13.3 / 16.5 and
-// 13.8 / 20.8 at 1000, 21.4 / 27.9 and 19.8 / 29.1 at 2000.
+// one CTA, without a list to walk and a merge.  1 / 32 sequences of 8 KV heads (in a
+// graph, warm): whole against split 8.0 / 8.9 and 10.1 / 13.3 us at 256 tokens, 14.1 /
+// 16.4 and 14.7 / 20.3 at 1000, 21.7 / 27.0 and 20.5 / 27.8 at 2000.
 constexpr int kWholeKeys = 1024;
 // AttnSplit::extra: what a segment costs beside its units, in units.  The
 // mma.sync kernel spends about 6000 cycles to begin and end a segment, 5000 more
 // on its own rows' keys and 2300 on a unit: with 1 / 3 / 5, the token batch of
 // cached_small.cu took 220 / 207 / 205 us with own keys and 205 / 204 / 206 without,
 // blocks of 8 over 16 short sequences 70 / 47 / 42 and 48 / 40 / 41.  The tcgen05
-// kernels spend 16 to 20 thousand cycles on a segment and 2060 (split) or 4150
-// (pairs) on a unit: with 0 / 6, blocks of 32 and 128 took 130 / 106 and 293 /
+// kernels spend 10 to 20 thousand cycles to end a segment and begin the next, and
+// 2000 (split) or 4000 (pairs) on a unit: with 0 / 6, when it was tried, blocks of 32 and 128 took 130 / 106 and 293 /
 // 248 us; 4 to 12 are level.
 constexpr int kSmallExtra = 3, kSmallExtraOwn = 5, kTcExtra = 6;
 

@@ -10,11 +10,12 @@
 // whatever the warps do; they turn codes into fp16 on the way from shared
 // memory to the MMA.
 // Bound by HBM: 32 sequences of up to 32768 tokens (1.30 GB of codes), a token
-// each, 32 / 8 heads of 128, take 209 us with the merge: 6.2 TB/s, 92 % of the
+// each, 32 / 8 heads of 128, take 208 us with the merge: 6.2 TB/s, 92 % of the
 // measured copy rate.  (With loads issued by the computing warps themselves it
-// was 334 us.)  S from two e4m3 parts of Q by e4m3 m16n8k32 instead, without
+// was 334 us.)  With fp32 outputs, whose weights go in two parts: 247 us (ptxas
+// reports 60 bytes of spills, 332 with tiles of 32 rows).  S from two e4m3 parts of Q by e4m3 m16n8k32 instead, without
 // K's conversion: 259 us against 227 when it was tried.  One sequence of 256
-// tokens: 7.5 us, less than the call takes on the host.
+// tokens: 8 us, less than the call takes on the host.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

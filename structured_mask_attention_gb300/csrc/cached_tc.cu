@@ -40,14 +40,20 @@
 // alone are 1.66).
 //
 // What bounds it (16 / 8 heads of 128, merge included): a block of 512 over one
-// sequence of 131072 tokens takes 483 us, 1.14 PFLOP/s or 62 % of the measured
-// bf16 rate; a pair's tile period is about 4150 cycles against 2150 of its
+// sequence of 131072 tokens takes 487 us, 1.13 PFLOP/s or 61 % of the measured
+// bf16 rate; a pair's tile period is about 4000 cycles against 2150 of its
 // products alone: the chain S -> softmax (2500) -> P V of each sub-tile, and the
 // issuing thread's waits in between.  Blocks of 128 over 4 sequences, 40 / 8
-// heads: 226 us, 0.76 PFLOP/s (three tiles of 256 for 640 rows: a sixth is
+// heads: 224 us, 0.77 PFLOP/s (three tiles of 256 for 640 rows: a sixth is
 // padding).  Blocks of 32 over 16 sequences of 8192 at most (split, 64 rows of
-// 128): 87 us, of which 30 are the 28 tiles of a CTA (1.1 us each) and the rest
-// begins and ends its two segments.
+// 128): 86 us.  There, by the CTAs' clocks with cold caches, 21 thousand cycles
+// pass before the first scores (2 to start, 9 until the walk has read lengths and
+// offsets, 7 to place the queries, 3 until K is there), 10 more in the first tile
+// (instructions that no CTA has run yet), 2 for each of 33 units, and 10 to 16 for
+// the end of a segment and the beginning of the next (1 to 2 of them): 102 to 156 in
+// all, 132 in the mean, 69 us.
+// Registers: ptxas reports 60 to 176 bytes of spills in the bf16 instances and 208
+// to 420 in the fp32 ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -69,8 +75,7 @@ static_assert(128 * (kRegsControl + kRegsConvert) + 256 * kRegsSoftmax <= kThrea
 // (fp32 outputs) Key tiles that a sub-tile adds up on the tensor cores.  1 / 2 / 4 /
 // all of about 90: O off by 1.0 / 1.2 / 1.6 / 8.9e-6 of its size over 19357 keys
 // (fp32 products in torch: 2.6e-6); blocks of 128 of the case above as fp32, with 1 /
-// 2 / 4: 972 / 835 / 776 us (since the issuing thread's short loop serves fp32
-// outputs too and the third parts stay where they arise, 2 / 4: 647 / 624).
+// 2 / 4: 670 / 596 / 564 us.
 constexpr int kFineTiles = 2;
 constexpr int NK = 3;             // K slots: 128 keys of codes, or one 64-column panel of own keys
 constexpr int NI = 16;            // tile-info slots (more than any two roles are apart, and a batch of four)

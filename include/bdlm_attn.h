@@ -391,7 +391,8 @@ bdlm_status bdlm_attn_bwd_varlen(const void* Qc, const void* Kc, const void* Vc,
  * bdlm_sync_status reads it).  Contents that only the device can check -- a
  * page id outside the pool, a length that is negative or outside the page
  * table, row offsets that leave the rows or exceed max_rows -- are left out of
- * the result (those keys unseen, that length cut, those rows skipped) and
+ * the result (those keys unseen, that length cut, those rows skipped; a token
+ * that an eviction keeps from such a page moves as zeros) and
  * reported by bdlm_sync_status as BDLM_ERR_INVALID_ARG; a wait that expired is
  * recorded beside them and reported first, as BDLM_ERR_TIMEOUT. */
 typedef struct {

@@ -578,7 +578,21 @@ class BdlmCache:
     ``page_table`` [n_seqs, max_pages] int32; ``lens`` [n_seqs] int32.
 
     The handle keeps the tensors; update ``page_table`` and ``lens`` in place
-    (``copy_``), or make a new handle for other tensors."""
+    (``copy_``), or make a new handle for other tensors.
+
+    The calls on it share these arguments:
+
+    ``row_offsets`` [n_seqs + 1] int32 on the device (sequence s owns rows
+    ``row_offsets[s]`` to ``row_offsets[s + 1]``), or None: equally many rows each.
+    ``max_rows``: the most rows of any sequence.  Give it with ``row_offsets``: the
+    host does not read them and would take all rows for it, which is right but
+    slow (64 single tokens then run in the kernels for long blocks).
+    ``workspace`` from ``bdlm_cache_workspace``; without one the call makes its own
+    and drops it, and with it what ``bdlm_sync_status`` would report: expired waits
+    and page ids, lengths or offsets out of range.
+    ``stream`` (default: the current one of the cache's device): tensors that the
+    call makes are ordered behind the current stream; inputs, given outputs and a
+    given workspace are the caller's to order and to keep alive."""
     __slots__ = ("k8", "v8", "k_scale", "v_scale", "page_table", "lens", "device", "n_pages", "n_seqs", "max_pages",
                  "page", "Hkv", "d", "_struct", "_ref")
 

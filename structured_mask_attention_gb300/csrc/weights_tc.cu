@@ -16,7 +16,7 @@
 // cycles, is the rest of it: more K slots, more score buffers and weights added in
 // L2 instead of read first were all level); from about 128 rows on the exponentials (one per
 // row and key) and the products (blocks of 128 over 4 such sequences, 16 / 8
-// heads: 45 us, 0.76 PFLOP/s; the tensor pipe 31 %, the exponentials' 37 % busy, a
+// heads: 45 us, 0.76 PFLOP/s; the tensor pipe 30 %, the exponentials' 36 % busy, a
 // third of the time begins and ends the CTAs' two segments).  Not kept: both
 // parts' products side by side as 2 N columns, added by the threads (162 us
 // against 158 when it was tried).

@@ -438,6 +438,7 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
  * Scores are fp32 sums of products with the queries as they are, or, for more
  * than 32 rows times heads of a group and in bdlm_cache_weights, with queries
  * whose elements below 2^-13 of the row's largest are off by up to 2^-21 of it.
+ * |s_ij| may be up to 2^30 (fp32 leaves it no fraction from 2^23 on).
  * O and LSE must not overlap each other, Qn, Kn or Vn.
  * Deterministic: the keys are split over the GPU by their number, and the
  * parts are joined in a fixed order. */

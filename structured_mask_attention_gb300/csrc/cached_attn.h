@@ -46,7 +46,8 @@ constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
 // where one key dominates a row and has a small value, an attention sink.  The
 // rarer the rescaling, the less range: steps of 8 / 7 / 6 / 5 / 4 took 87.0 / 87.3 / 88.2 /
 // 89.6 / 90.5 us for blocks of 32 and 225 / 228 / 229 / 231 / 232 for blocks of 128; 512
-// were level.  The row sum takes p' 2^-shift.
+// were level.  The row sum takes p' 2^-shift.  (Scores so large that their rounding
+// exceeds the margin: the exact maximum's shift is rounded up, p' saturates.)
 constexpr float kRescale = 6.9f;  // log2 units: the tcgen05 kernels' reference moves in steps of at least this
 constexpr float kSmallShift = 15.0f, kTcShift = 9.0f;
 constexpr float kSmallUnshift = 1.0f / (1 << (int)kSmallShift), kTcUnshift = 1.0f / (1 << (int)kTcShift);

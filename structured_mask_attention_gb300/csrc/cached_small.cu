@@ -13,9 +13,9 @@
 // each, 32 / 8 heads of 128, take 208 us with the merge: 6.2 TB/s, 92 % of the
 // measured copy rate.  (With loads issued by the computing warps themselves it
 // was 334 us.)  With fp32 outputs, whose weights go in two parts: 247 us (ptxas
-// reports 60 bytes of spills, 332 with tiles of 32 rows).  S from two e4m3 parts of Q by e4m3 m16n8k32 instead, without
-// K's conversion: 259 us against 227 when it was tried.  One sequence of 256
-// tokens: 8 us, less than the call takes on the host.
+// reports 60 bytes of spills, 332 with tiles of 32 rows).  S from two e4m3 parts of Q
+// by e4m3 m16n8k32 instead, without K's conversion: 259 us against 227 when it was
+// tried.  One sequence of 256 tokens: 8 us, less than the call takes on the host.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -105,7 +105,7 @@ __device__ __forceinline__ void softmax_step(State<HD>& st, float (&s)[N8][4], c
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float mn = fmaxf(st.m[r], mx);
     const float base = mn == -INFINITY ? 0.f : mn;  // no key yet: every p below is 0
-    const float alpha = ex2_approx(st.m[r] - base), less = base - kSmallShift;
+    const float alpha = ex2_approx(st.m[r] - base), less = __fadd_ru(base, -kSmallShift);
     if (__any_sync(0xffffffffu, mn != st.m[r])) {
 #pragma unroll
       for (int j = 0; j < HD / 8; ++j) {

@@ -295,7 +295,8 @@ __device__ __forceinline__ void store_p(uint32_t (&a)[32], uint32_t taddr) {
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     const float x = __uint_as_float(a[c]), y = __uint_as_float(a[c + 1]);
-    const uint32_t w = pack_f16x2(x, y);
+    uint32_t w;  // (saturating: from scores of 2^20 on their rounding may exceed the margin below 2^16)
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
     pk[c / 2] = w;
     if (REST) {
       const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&w));

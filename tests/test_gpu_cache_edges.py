@@ -153,6 +153,28 @@ def test_attn_fp32_output_with_own_keys(lib, rows, Hq, local, chain, L):
     assert rel <= chain * 2.0 ** -23 * 2 / 3 + 2.0 ** -21
 
 
+@pytest.mark.parametrize("rows", [1, 16, 40, 150])
+@pytest.mark.parametrize("size", [2.0 ** 16, 2.0 ** 22, 2.0 ** 26])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+def test_attn_scores_beyond_fp32s_fractions(lib, rows, size, o_dtype):
+    """Scores of 2^20 and more, whose roundings are of a binary order or more: a row
+    is a mean of values still (which keys share it is below fp32's resolution)."""
+    m = lib
+    c, _ = make_cache([700], 700, 1, 64, 16, seed=23)
+    Q, K, V = (make_rows(rows, H, 64, 1 + i) for i, H in enumerate((2, 1, 1)))
+    Q = bf16_round(Q * np.float32(size))
+    cache, dev = device_cache(m, torch, c), lambda x: to_dev(x, torch)
+    for kv in ((None, None), (dev(K), dev(V))):
+        O, LSE = m.bdlm_attn_cached(dev(Q), *kv, cache, o_dtype=o_dtype)
+        assert torch.isfinite(O).all() and torch.isfinite(LSE).all()
+        ref = co.attn(c, Q, *((K, V) if kv[0] is not None else (None, None)), offsets_of([rows]), 0.125)
+        # the row's largest score, in natural units
+        assert (np.abs(LSE.double().cpu().numpy() - ref[1]) <= score_error(64, ref[3]) + 2.0 ** -22 * np.abs(ref[1])).all()
+        v = np.concatenate([co.tokens(c, "v", 0, 0)] + ([V[:, 0]] if kv[0] is not None else []))
+        assert (O.double().cpu().numpy() <= v.max(0) * (1 + HALF) + 1e-3).all()
+        assert (O.double().cpu().numpy() >= v.min(0) * (1 + HALF) - 1e-3).all()
+
+
 @pytest.mark.parametrize("rows", [5, 20, 33, 60, 150, 300])  # (60 and more: own tiles of their own; 150, 300: several)
 @pytest.mark.parametrize("factor", [1.0, 2.0 ** -40, 2.0 ** 40])
 @pytest.mark.parametrize("L", [0, 200])

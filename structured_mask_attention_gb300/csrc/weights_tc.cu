@@ -289,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < RB; ++k) {
             const int r = rb + k * RS;
             if (r >= N) break;  // (N and RS are such that a warp's lanes agree)
-            const uint32_t w[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
-            // a row without a key, or none at all, adds nothing
+            // a row without a key, or none at all, adds nothing, whatever its query holds
+            const uint32_t on = __shfl_sync(0xffffffffu, lse[k], lane & ~(PER - 1)) == -INFINITY ? 0u : 0xffffffffu;
+            const uint32_t w[8] = {x[k].x & on, x[k].y & on, x[k].z & on, x[k].w & on,
+                                   y[k].x & on, y[k].y & on, y[k].z & on, y[k].w & on};
             const float nl = lse[k] == -INFINITY ? -INFINITY : lse[k] * -1.4426950408889634f;
             uint32_t amax = 0;
 #pragma unroll

@@ -175,6 +175,26 @@ def test_attn_scores_beyond_fp32s_fractions(lib, rows, size, o_dtype):
         assert (O.double().cpu().numpy() >= v.min(0) * (1 + HALF) - 1e-3).all()
 
 
+@pytest.mark.parametrize("rows", [4, 300])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_weights_leave_rows_of_lse_minus_infinity_out(lib, rows, d, value):
+    """A padded batch: rows marked by LSE = -inf, whose queries hold anything."""
+    m = lib
+    c, _ = make_cache([300], 300, 2, d, 64, seed=27)
+    Q = make_rows(rows, 4, d, 1)
+    off = offsets_of([rows])
+    LSE = co.attn(c, Q, None, None, off, 0.1)[1].astype(np.float32)
+    pad = np.arange(rows) % 3 == 1
+    LSE[:, pad] = -np.inf
+    Wr, E = co.weights(c, Q, LSE, off, 0.1, np.zeros((1, 2, 320), np.float32))
+    Q[pad] = value
+    W = torch.zeros((1, 2, 320), device="cuda")
+    m.bdlm_cache_weights(to_dev(Q, torch), torch.from_numpy(LSE).cuda(), device_cache(m, torch, c), W, scale=0.1)
+    rel = score_error(d, E) + 2.0 ** -23 * (1 + np.abs(LSE[:, ~pad]).max()) + (2 * rows + 4) * 2.0 ** -24
+    assert (np.abs(W.double().cpu().numpy() - Wr) <= rel * Wr + 2.0 ** -24).all()
+
+
 @pytest.mark.parametrize("rows", [5, 20, 33, 60, 150, 300])  # (60 and more: own tiles of their own; 150, 300: several)
 @pytest.mark.parametrize("factor", [1.0, 2.0 ** -40, 2.0 ** 40])
 @pytest.mark.parametrize("L", [0, 200])

@@ -472,6 +472,95 @@ bdlm_status bdlm_cache_evict(const bdlm_cache* cache, const float* weights, cons
                              int64_t sinks, int64_t recent, int32_t* lens_out, float* weights_out, int32_t* kept,
                              void* workspace, size_t ws_bytes, bdlm_stream stream);
 
+/* ---- Drafted tokens over the cache ----------------------------------------
+ * A drafter proposes tokens behind each sequence's last one; one step of the
+ * target model runs them all and its probabilities decide which of them stand.
+ * The drafts of a sequence form a tree (a chain is one): row 0 is the sequence's
+ * last token itself, whose key and value are not cached yet, and parents [rows]
+ * holds for every row the row of its own sequence that it follows, a row before
+ * it, or -1 for one that follows the cached tokens.  Rows are packed and laid out
+ * by row_offsets as in the other calls.  A step:
+ *   bdlm_tree_mask    once for the tree;
+ *   bdlm_attn_tree    in every layer;
+ *   bdlm_tree_verify  on the probabilities;
+ *   bdlm_cache_commit in every layer, the accepted rows.
+ * All of it stays on the device: a step can be captured and replayed on other
+ * trees.  A tree has at most 4096 rows.  The workspace is the cache calls' (256
+ * bytes, the header, do for all but bdlm_attn_tree); what only the device can check
+ * (a parent that does not come before its row, a token outside the vocabulary, a
+ * path that leaves the sequence's rows) is reported by bdlm_sync_status as
+ * BDLM_ERR_INVALID_ARG. */
+
+/* What every row of a tree sees: visible [rows, words], bit j % 32 of word j / 32 of
+ * a row says that it sees row j of its sequence: its ancestors and itself.  positions
+ * [rows]: the row's place in the sequence, lens plus the number of its ancestors (for a
+ * rotary embedding).  words * 32 >= max_rows; all words of a row are written.  A row
+ * whose parent is out of range counts as one that follows the cached tokens. */
+bdlm_status bdlm_tree_mask(const int32_t* parents, const bdlm_cache* cache, const int32_t* row_offsets, int64_t rows,
+                           int64_t max_rows, int32_t* visible, int64_t words, int32_t* positions, void* workspace,
+                           size_t ws_bytes, bdlm_stream stream);
+
+/* bdlm_attn_cached with own rows that see only those of their sequence whose bit is
+ * set in visible [rows, words] (any bits: bdlm_tree_mask's, or another pattern; those
+ * of rows that the sequence does not have count for nothing), and all its cached tokens.
+ * A row that sees no key gets O = 0, LSE = -inf.  Keys and values that a row does not
+ * see may hold anything, NaN and infinities too; where a value that it sees is not
+ * finite, its output is not.  Everything else, bounds on O and LSE among it, as in
+ * bdlm_attn_cached; the outputs must not overlap visible either. */
+bdlm_status bdlm_attn_tree(const void* Qn, const void* Kn, const void* Vn, const int32_t* visible, int64_t words,
+                           const bdlm_cache* cache, const int32_t* row_offsets, int64_t rows, int64_t max_rows, int Hq,
+                           float scale, void* O, bdlm_dtype o_dtype, float* LSE, void* workspace, size_t ws_bytes,
+                           bdlm_stream stream);
+
+/* Bytes of workspace for bdlm_tree_verify (0 for an invalid shape); its first 256
+ * are zeroed once by the caller, as the cache calls' are. */
+size_t bdlm_workspace_size_verify(int n_seqs, int64_t max_rows, int64_t V);
+
+/* Which drafts the target accepts.  target [rows, V]: row i the target's
+ * probabilities of the token behind row i; draft, of the same type and shape, the
+ * drafter's from which the tokens of row i's children were drawn, each on its own; or
+ * null, when the drafts were chosen and not drawn.  p_dtype: both in fp32 or bf16; rows
+ * lie target_stride (draft_stride) values apart, at least V.  tokens [rows], in [0, V);
+ * uniforms [rows] and sample [n_seqs]: random numbers in [0, 1) (NaN and below: 0).  Row
+ * 0 of a sequence is accepted.  From the last accepted row, with p and q its rows of target
+ * and draft, its children x_1, x_2, ... are tested in the order of their rows:
+ *   drawn:   x_{k+1} is accepted if u q(x) Z_k < max(p(x) - c_k q(x), 0), where
+ *            c_0 = 0, Z_0 = 1, c_{k+1} = c_k + Z_k, Z_k = sum_x max(p(x) - c_k q(x), 0)
+ *            (max(r / Z - q, 0) over its total replaces r / Z, from r = p on);
+ *   chosen:  x_{k+1} is accepted if u Z_k < p(x) and x has not been rejected here
+ *            before, Z_k = 1 - the p of the tokens rejected here;
+ * u being the child's uniform.  The first one accepted is the next row of the path.
+ * When there is none, or the path has max_path rows, it is complete, and the token
+ * behind it is the first x whose running sum of r passes sample times its total, r
+ * being max(p - c_k q, 0) after k rejected drafts, p without the rejected tokens, or p
+ * itself where there are no children, where the path was cut, or where that total is 0.
+ * Tokens so follow the target's distribution, whatever the drafter's.
+ * path [n_seqs, max_path]: the accepted rows of each sequence, -1 behind them;
+ * accepted [n_seqs]: how many they are; next_token [n_seqs].  A sequence without rows
+ * gets 0 and -1; one whose p is 0 everywhere the token -1 (reported).  Rows whose
+ * parent or token is out of range, and those other than row 0 whose parent is -1, are not
+ * accepted.
+ * Probabilities below 0 (above 1) and NaN count as 0 (as 1 and 0), and are summed as
+ * whole numbers of 2^-62; a row's sum must stay below 4.  Tests are made in 64 bits.
+ * Deterministic; outputs overlap neither inputs nor each other. */
+bdlm_status bdlm_tree_verify(const int32_t* parents, const int32_t* tokens, const void* target, const void* draft,
+                             bdlm_dtype p_dtype, int64_t V, int64_t target_stride, int64_t draft_stride,
+                             const float* uniforms, const float* sample, int n_seqs, const int32_t* row_offsets,
+                             int64_t rows, int64_t max_rows, int32_t* path, int64_t max_path, int32_t* accepted,
+                             int32_t* next_token, void* workspace, size_t ws_bytes, bdlm_stream stream);
+
+/* bdlm_cache_append of the rows path[s, 0], path[s, 1], ... of each sequence, the first
+ * accepted[s] of them, in this order: what bdlm_tree_verify leaves of a step.  path
+ * [n_seqs, max_path]: rows of the sequence, counted from its first; entries behind
+ * the accepted ones are not read.  lens_out = lens + accepted.  A row that is not one of
+ * the sequence's is written as zeros, and an accepted[s] outside [0, max_path] counts as 0;
+ * both are reported.  Everything else as in bdlm_cache_append; lens_out overlaps
+ * neither path nor accepted. */
+bdlm_status bdlm_cache_commit(const void* K, const void* V, const bdlm_cache* cache, const int32_t* path,
+                              int64_t max_path, const int32_t* accepted, const int32_t* row_offsets, int64_t rows,
+                              int64_t max_rows, int32_t* lens_out, void* workspace, size_t ws_bytes,
+                              bdlm_stream stream);
+
 /* Host-only: the forward work list in the order the persistent CTAs claim
  * its items, for inspection and tests.
  * One item per (query tile of tile_q rows, query head, stream), longest

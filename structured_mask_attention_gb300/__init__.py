@@ -25,6 +25,8 @@ __all__ = [
     "bdlm_sync_status", "bdlm_watchdog_selftest", "bdlm_sync_status_noalloc", "bdlm_watchdog_selftest_noalloc",
     "BdlmCache", "bdlm_cache_workspace", "bdlm_workspace_size_cache", "bdlm_cache_append", "bdlm_attn_cached",
     "bdlm_cache_weights", "bdlm_cache_evict",
+    "bdlm_tree_mask", "bdlm_attn_tree", "bdlm_tree_verify", "bdlm_verify_workspace", "bdlm_workspace_size_verify",
+    "bdlm_cache_commit",
     "bdlm_kernel_launches", "bdlm_last_error",
     "bdlm_version", "bdlm_timing_enable", "bdlm_timing_report", "header_functions", "LIB_PATH",
     "HEADER_PATH",
@@ -84,6 +86,12 @@ _SIGS = {
     "bdlm_attn_cached": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _P, _I, _P, _P, _SZ, _P]),
     "bdlm_cache_weights": (_I, [_P, _P, _P, _P, _I64, _I64, _I, _F, _P, _P, _SZ, _P]),
     "bdlm_cache_evict": (_I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "bdlm_tree_mask": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "bdlm_attn_tree": (_I, [_P, _P, _P, _P, _I64, _P, _P, _I64, _I64, _I, _F, _P, _I, _P, _P, _SZ, _P]),
+    "bdlm_workspace_size_verify": (_SZ, [_I, _I64, _I64]),
+    "bdlm_tree_verify": (_I, [_P, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _I, _P, _I64, _I64, _P, _I64, _P, _P, _P,
+                              _SZ, _P]),
+    "bdlm_cache_commit": (_I, [_P, _P, _P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "bdlm_sync_status": (_I, [_P, _P]),
     "bdlm_sync_status_noalloc": (_I, [_P]),
     "bdlm_watchdog_selftest_noalloc": (_I, [ctypes.c_uint32, _P]),
@@ -724,11 +732,17 @@ def bdlm_attn_cached(Qn, Kn, Vn, cache, row_offsets=None, max_rows: int | None =
     """Attention of packed new rows (Qn [rows, Hq, d]; Kn, Vn [rows, Hkv, d],
     or both None for the cached tokens alone) to their sequence's cached
     tokens and their own block.  Returns (O [rows, Hq, d], LSE [Hq, rows])."""
+    if (Kn is None) != (Vn is None):
+        raise ValueError("Kn and Vn: give both or neither")
+    return _cached_attention(load_library().bdlm_attn_cached, Qn, Kn, Vn, (), cache, row_offsets, max_rows, scale, o_dtype,
+                             out, workspace, stream)
+
+
+def _cached_attention(fn, Qn, Kn, Vn, mask, cache, row_offsets, max_rows, scale, o_dtype, out, workspace, stream):
+    """What bdlm_attn_cached and bdlm_attn_tree share; ``mask``: what the call takes behind Vn."""
     torch = _torch()
     T, Hq, d = Qn.shape
     _check_tensor("Qn", Qn, torch.bfloat16, (T, Hq, cache.d), cache.device)
-    if (Kn is None) != (Vn is None):
-        raise ValueError("Kn and Vn: give both or neither")
     if Kn is not None:
         _check_tensor("Kn", Kn, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
         _check_tensor("Vn", Vn, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
@@ -748,8 +762,8 @@ def bdlm_attn_cached(Qn, Kn, Vn, cache, row_offsets=None, max_rows: int | None =
     ws = _cache_workspace(cache, workspace, made,
                           max(bdlm_workspace_size_cache(cache.n_seqs, Hq, cache.Hkv, d, max_rows), 256)
                           if workspace is None else 0)
-    _cache_call(load_library().bdlm_attn_cached, cache, stream,
-                (Qn.data_ptr(), None if Kn is None else Kn.data_ptr(), None if Vn is None else Vn.data_ptr(), cache._ref,
+    _cache_call(fn, cache, stream,
+                (Qn.data_ptr(), None if Kn is None else Kn.data_ptr(), None if Vn is None else Vn.data_ptr(), *mask, cache._ref,
                  off, T, max_rows, Hq, 1.0 / math.sqrt(d) if scale is None else scale, O.data_ptr(),
                  F32 if O.dtype == torch.float32 else BF16, LSE.data_ptr(), ws.data_ptr(), ws.nbytes), made)
     return O, LSE
@@ -800,6 +814,162 @@ def bdlm_cache_evict(cache, weights, dst_table, keep: int, sinks: int = 0, recen
                 (cache._ref, weights.data_ptr(), dst_table.data_ptr(), keep, sinks, recent, lens_out.data_ptr(),
                  weights_out.data_ptr(), kept.data_ptr() or None, ws.data_ptr(), ws.nbytes), made)
     return lens_out, weights_out, kept
+
+
+# --------------------------------------------------------- drafted tokens
+def _tree_words(visible, T, device):
+    if visible.dim() != 2:
+        raise ValueError(f"visible must be [rows, words], not {list(visible.shape)}")
+    _check_tensor("visible", visible, _torch().int32, (T, visible.shape[1]), device)
+    return visible.shape[1]
+
+
+def bdlm_tree_mask(cache, parents, row_offsets=None, max_rows: int | None = None, out=None, workspace=None, stream=None):
+    """What the rows of drafted trees see.  ``parents`` [rows] int32: the row of
+    its own sequence that a row follows, one before it, or -1.  Returns (visible
+    [rows, ceil(max_rows / 32)] int32, bit j % 32 of word j / 32: the row sees row j
+    of its sequence, an ancestor or itself; positions [rows] int32, ``cache.lens`` plus
+    the number of ancestors).  A tree has at most 4096 rows: give ``max_rows`` where
+    there are more in all (and to keep the words few)."""
+    torch = _torch()
+    T = parents.shape[0]
+    _check_tensor("parents", parents, torch.int32, (T,), cache.device)
+    off, max_rows = _cache_rows(cache, row_offsets, max_rows, T)
+    made = []
+    if out is None:
+        visible = torch.empty((T, max(1, (max_rows + 31) // 32)), dtype=torch.int32, device=cache.device)
+        positions = torch.empty(T, dtype=torch.int32, device=cache.device)
+        made += [visible, positions]
+    else:
+        visible, positions = out
+        _check_tensor("positions", positions, torch.int32, (T,), cache.device)
+    words = _tree_words(visible, T, cache.device)
+    ws = _cache_workspace(cache, workspace, made, 256)
+    _cache_call(load_library().bdlm_tree_mask, cache, stream,
+                (parents.data_ptr(), cache._ref, off, T, max_rows, visible.data_ptr(), words, positions.data_ptr(),
+                 ws.data_ptr(), ws.nbytes), made)
+    return visible, positions
+
+
+def bdlm_attn_tree(Qn, Kn, Vn, visible, cache, row_offsets=None, max_rows: int | None = None,
+                   scale: float | None = None, o_dtype=None, out=None, workspace=None, stream=None):
+    """``bdlm_attn_cached`` with own rows that see only those of their sequence whose
+    bit is set in ``visible`` [rows, words] int32 (from ``bdlm_tree_mask``, or any other
+    pattern), and all its cached tokens.  Returns (O [rows, Hq, d], LSE [Hq, rows])."""
+    if Kn is None or Vn is None:
+        raise ValueError("Kn and Vn: a tree's rows see themselves, give both")
+    words = _tree_words(visible, Qn.shape[0], cache.device)
+    return _cached_attention(load_library().bdlm_attn_tree, Qn, Kn, Vn, (visible.data_ptr(), words), cache, row_offsets,
+                             max_rows, scale, o_dtype, out, workspace, stream)
+
+
+def bdlm_workspace_size_verify(n_seqs: int, max_rows: int, V: int) -> int:
+    return int(load_library().bdlm_workspace_size_verify(n_seqs, max_rows, V))
+
+
+def bdlm_verify_workspace(n_seqs: int, max_rows: int, V: int, device="cuda"):
+    """A zeroed workspace for ``bdlm_tree_verify``; one call at a time uses it."""
+    n = bdlm_workspace_size_verify(n_seqs, max_rows, V)
+    if not n:
+        raise ValueError(f"no workspace for n_seqs={n_seqs}, max_rows={max_rows}, V={V}")
+    return _torch().zeros(n, dtype=_torch().uint8, device=device)
+
+
+def _check_probs(name, t, dtype, T, device):
+    if t.dim() != 2 or t.shape[0] != T or t.dtype is not dtype or t.device != device or not t.is_cuda or \
+            (t.shape[1] > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be [{T}, V] {dtype} on {device} (a CUDA device) with rows that lie apart and values "
+                         f"side by side, not {t.dtype} {list(t.shape)} of strides {list(t.stride())} on {t.device}")
+    return t.stride(0) if T > 1 else t.shape[1]
+
+
+def bdlm_tree_verify(parents, tokens, target, draft, uniforms, sample, row_offsets=None, max_rows: int | None = None,
+                     max_path: int | None = None, out=None, workspace=None, stream=None):
+    """Tests drafted trees against the target's probabilities, from given random numbers.
+
+    ``parents``, ``tokens`` [rows] int32; ``target`` [rows, V] float32 or bfloat16: row i
+    the target's probabilities of the token behind row i (a row's values side by side, rows
+    any stride apart); ``draft`` of the same type and shape: the drafter's probabilities
+    that the children of row i were drawn from, or None: they were chosen, not drawn;
+    ``uniforms`` [rows] and ``sample`` [n_seqs] float32 in [0, 1).  Row 0 of a sequence is
+    its last token.  ``max_path``: the most rows of a path (default: max_rows).
+
+    Returns (path [n_seqs, max_path] int32, the accepted rows of each sequence and -1
+    behind them; accepted [n_seqs] int32, how many; next_token [n_seqs] int32, drawn so
+    that the tokens follow the target's distribution).  ``row_offsets``, ``max_rows``,
+    ``workspace`` (from ``bdlm_verify_workspace``) and ``stream`` as in the calls on a cache."""
+    torch = _torch()
+    T, n, device = parents.shape[0], sample.shape[0], target.device
+    if target.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"target must be float32 or bfloat16, not {target.dtype}")
+    strides = [_check_probs("target", target, target.dtype, T, device)]
+    V = target.shape[1]
+    if draft is not None:
+        strides.append(_check_probs("draft", draft, target.dtype, T, device))
+        if draft.shape != target.shape:
+            raise ValueError(f"draft is {list(draft.shape)}, target {list(target.shape)}")
+    _check_tensor("parents", parents, torch.int32, (T,), device)
+    _check_tensor("tokens", tokens, torch.int32, (T,), device)
+    _check_tensor("uniforms", uniforms, torch.float32, (T,), device)
+    _check_tensor("sample", sample, torch.float32, (n,), device)
+    like = _Batch(n, device)
+    off, max_rows = _cache_rows(like, row_offsets, max_rows, T)
+    made = []
+    if out is None:
+        path = torch.empty((n, max_rows if max_path is None else max_path), dtype=torch.int32, device=device)
+        accepted = torch.empty(n, dtype=torch.int32, device=device)
+        token = torch.empty(n, dtype=torch.int32, device=device)
+        made += [path, accepted, token]
+    else:
+        path, accepted, token = out
+        if max_path is not None and path.shape[-1] != max_path:
+            raise ValueError(f"path has {path.shape[-1]} columns, max_path is {max_path}")
+        _check_tensor("path", path, torch.int32, (n, path.shape[-1]), device)
+        _check_tensor("accepted", accepted, torch.int32, (n,), device)
+        _check_tensor("next_token", token, torch.int32, (n,), device)
+    ws = _cache_workspace(like, workspace, made, 256)
+    _cache_call(load_library().bdlm_tree_verify, like, stream,
+                (parents.data_ptr(), tokens.data_ptr(), target.data_ptr(), None if draft is None else draft.data_ptr(),
+                 F32 if target.dtype is torch.float32 else BF16, V, strides[0], strides[-1], uniforms.data_ptr(),
+                 sample.data_ptr(), n, off, T, max_rows, path.data_ptr(), path.shape[1], accepted.data_ptr(),
+                 token.data_ptr(), ws.data_ptr(), ws.nbytes), made)
+    return path, accepted, token
+
+
+class _Batch:
+    """What the shared checks of the calls on a cache need of one that has none."""
+    __slots__ = ("n_seqs", "device")
+
+    def __init__(self, n_seqs, device):
+        self.n_seqs, self.device = n_seqs, device
+
+
+def bdlm_cache_commit(cache, K, V, path, accepted, row_offsets=None, max_rows: int | None = None, lens_out=None,
+                      workspace=None, stream=None):
+    """``bdlm_cache_append`` of the rows that ``bdlm_tree_verify`` accepted: of each
+    sequence rows ``path[s, :accepted[s]]`` (counted from its first row), in this order.
+    Returns ``lens_out`` [n_seqs] int32 = lens + accepted; copy it into ``cache.lens`` once
+    every layer's cache has them."""
+    torch = _torch()
+    if path.dim() != 2:
+        raise ValueError(f"path must be [n_seqs, max_path], not {list(path.shape)}")
+    T = K.shape[0]
+    _check_tensor("K", K, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
+    _check_tensor("V", V, torch.bfloat16, (T, cache.Hkv, cache.d), cache.device)
+    _check_tensor("path", path, torch.int32, (cache.n_seqs, path.shape[1]), cache.device)
+    _check_tensor("accepted", accepted, torch.int32, (cache.n_seqs,), cache.device)
+    off, max_rows = _cache_rows(cache, row_offsets, max_rows, T)
+    made = []
+    if lens_out is None:
+        lens_out = torch.empty(cache.n_seqs, dtype=torch.int32, device=cache.device)
+        made.append(lens_out)
+    else:
+        _check_tensor("lens_out", lens_out, torch.int32, (cache.n_seqs,), cache.device)
+    ws = _cache_workspace(cache, workspace, made, 256)
+    _cache_call(load_library().bdlm_cache_commit, cache, stream,
+                (K.data_ptr(), V.data_ptr(), cache._ref, path.data_ptr(), path.shape[1], accepted.data_ptr(), off, T,
+                 max_rows, lens_out.data_ptr(), ws.data_ptr(), ws.nbytes), made)
+    return lens_out
 
 
 def bdlm_sync_status(workspace, stream=None):

@@ -22,7 +22,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbdlm_attn.so")
 SOURCES = ["abi.cu", "fwd_tc.cu", "bwd_dq.cu", "bwd_dkv.cu", "small_kernels.cu", "noalloc.cu",
            "cache_abi.cu", "cache_ops.cu", "cached_small.cu", "cached_tc.cu",
-           "weights_tc.cu"]
+           "weights_tc.cu", "tree_small.cu", "tree_tc.cu", "tree_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

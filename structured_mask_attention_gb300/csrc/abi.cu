@@ -33,12 +33,13 @@ thread_local std::string g_last_error;
 std::atomic<uint64_t> g_launches{0};
 
 // ---------------------------------------------------------------- timing
-enum KernelKind { K_FWD = 0, K_DKV, K_DQ, K_PREP, K_MERGE, K_WATCHDOG, K_CACHE0, K_COUNT = K_CACHE0 + 5 };
+enum KernelKind { K_FWD = 0, K_DKV, K_DQ, K_PREP, K_MERGE, K_WATCHDOG, K_CACHE0, K_COUNT = K_CACHE0 + 8 };
 const char* const kKindNames[K_COUNT] = {"bdlm_fwd_tc", "bdlm_bwd_dkv", "bdlm_bwd_dq",
                                          "bdlm_preprocess", "bdlm_merge", "bdlm_watchdog",
                                          // in the order of AbiTimer
                                          "bdlm_cache_append", "bdlm_attn_cached", "bdlm_cached_merge",
-                                         "bdlm_cache_weights", "bdlm_cache_evict"};
+                                         "bdlm_cache_weights", "bdlm_cache_evict", "bdlm_tree_mask", "bdlm_tree_verify",
+                                         "bdlm_cache_commit"};
 
 struct Timing {
   std::mutex mu;
@@ -970,12 +971,13 @@ bdlm_status bdlm_sync_status(void* workspace, bdlm_stream stream) {
     e = cudaMemset(workspace, 0, sizeof(words));
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(status)");
     const uint32_t word = words[0], bad = words[kContentsWord];
-    char what[160] = "";
+    char what[224] = "";
     if (bad)
-      snprintf(what, sizeof(what), "cache contents out of range (0x%x):%s%s%s", bad,
+      snprintf(what, sizeof(what), "cache contents out of range (0x%x):%s%s%s%s", bad,
                (bad & 0xff & kStatusBadPage) ? " a page id outside the pool;" : "",
                (bad & 0xff & kStatusBadLen) ? " a length outside its page table;" : "",
-               (bad & 0xff & kStatusBadRows) ? " row offsets outside the rows;" : "");
+               (bad & 0xff & kStatusBadRows) ? " row offsets outside the rows;" : "",
+               (bad & 0xff & kStatusBadTree) ? " a tree's parents, tokens, path or accepted rows;" : "");
     // (an expired wait first: after it nothing of the result is good)
     if (word != 0)
       return fail(BDLM_ERR_TIMEOUT, "device wait limit expired (status 0x%x, wait site %u)%s%s", word, word & 0xffu,

@@ -20,7 +20,8 @@ bdlm_status abi_device(int* sms);
 bdlm_status abi_encoder(EncodeTiledFn* fn);
 uint64_t abi_wait_limit_ns();
 
-enum AbiTimer { ABI_T_APPEND, ABI_T_ATTN_CACHED, ABI_T_CACHED_MERGE, ABI_T_WEIGHTS, ABI_T_EVICT };
+enum AbiTimer { ABI_T_APPEND, ABI_T_ATTN_CACHED, ABI_T_CACHED_MERGE, ABI_T_WEIGHTS, ABI_T_EVICT,
+                ABI_T_TREE_MASK, ABI_T_VERIFY, ABI_T_COMMIT };
 // Brackets a launch for bdlm_timing_report (nothing when timing is off).
 void* abi_timer_begin(AbiTimer kind, cudaStream_t st);
 void abi_timer_end(void* timer);

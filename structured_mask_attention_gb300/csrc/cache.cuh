@@ -46,7 +46,7 @@ struct RowsDesc {
 // Findings about contents that only the device can check: what is bad is left
 // out of the result.  They are or-ed into a word of their own in the workspace
 // header, so that the status word stays free for the first expired wait.
-enum : uint32_t { kStatusBadPage = 0x7201, kStatusBadLen = 0x7202, kStatusBadRows = 0x7204 };
+enum : uint32_t { kStatusBadPage = 0x7201, kStatusBadLen = 0x7202, kStatusBadRows = 0x7204, kStatusBadTree = 0x7208 };
 constexpr int kContentsWord = 1;  // (uint32; word 0: the status word)
 static_assert(kContentsWord < kSchedWordFwd && (kContentsWord + 1) * 4 <= kHeaderClearBytes, "a word that training calls clear");
 
@@ -66,19 +66,25 @@ struct SeqView {
   int rows, len;
 };
 
+// Rows of sequence s, held inside the tensors' bounds.
+struct RowsView {
+  int64_t row0;
+  int rows;
+};
+__device__ __forceinline__ RowsView rows_view(const RowsDesc& r, int s, uint32_t& bad) {
+  if (!r.off) return RowsView{(int64_t)s * r.max_rows, r.max_rows};
+  const int a = r.off[s], b = r.off[s + 1];
+  const bool ok = a >= 0 && b >= a && b <= r.T && b - a <= r.max_rows;
+  if (!ok) bad |= kStatusBadRows;
+  return RowsView{ok ? a : 0, ok ? b - a : 0};
+}
+
 // Rows and cached length of sequence s, held inside the tensors' bounds.
 __device__ __forceinline__ SeqView seq_view(const CacheDesc& c, const RowsDesc& r, int s, uint32_t& bad) {
+  const RowsView rv = rows_view(r, s, bad);
   SeqView v;
-  if (r.off) {
-    const int a = r.off[s], b = r.off[s + 1];
-    const bool ok = a >= 0 && b >= a && b <= r.T && b - a <= r.max_rows;
-    if (!ok) bad |= kStatusBadRows;
-    v.row0 = ok ? a : 0;
-    v.rows = ok ? b - a : 0;
-  } else {
-    v.row0 = (int64_t)s * r.max_rows;
-    v.rows = r.max_rows;
-  }
+  v.row0 = rv.row0;
+  v.rows = rv.rows;
   const int64_t cap = (int64_t)c.max_pages << c.lp;
   const int len = c.lens[s];
   v.len = len < 0 ? 0 : len > cap ? (int)cap : len;

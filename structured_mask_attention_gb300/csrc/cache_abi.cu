@@ -13,6 +13,7 @@
 #include "cache_ops.h"
 #include "cached_attn.h"
 #include "kernels.h"
+#include "tree_ops.h"
 
 using namespace bdlm;
 
@@ -145,6 +146,144 @@ bdlm_status encode_rows(EncodeTiledFn fn, CUtensorMap* m, const void* p, int64_t
 }
 size_t kept_space(int n_seqs, int Hkv, int64_t keep) { return (size_t)n_seqs * Hkv * keep * sizeof(int32_t); }
 
+// bdlm_cache_append, and with a path bdlm_cache_commit.
+bdlm_status append_call(const void* K, const void* V, const bdlm_cache* cache, const int32_t* path, int64_t max_path,
+                        const int32_t* accepted, const int32_t* row_offsets, int64_t rows, int64_t max_rows,
+                        int32_t* lens_out, void* workspace, size_t ws_bytes, bdlm_stream stream) {
+  AppendParams p;
+  CACHE_CHECK(check_cache(cache, &p.c));
+  CACHE_CHECK(check_rows(p.c, row_offsets, rows, max_rows, &p.r));
+  const int64_t ns = 4 * (int64_t)cache->n_seqs;
+  if (path && (max_path <= 0 || max_path > (int64_t)1 << 24))
+    return abi_fail(BDLM_ERR_SHAPE, "max_path=%lld must be in [1, 2^24]", (long long)max_path);
+  if (rows > 0) {
+    CACHE_CHECK(check_ptr("K", K, 16));
+    CACHE_CHECK(check_ptr("V", V, 16));
+  }
+  if (lens_out) CACHE_CHECK(check_ptr("lens_out", lens_out, 4));
+  CACHE_CHECK(check_lens_out(lens_out, cache));
+  CACHE_CHECK(check_apart("lens_out", lens_out, ns, "row_offsets", row_offsets, ns + 4));
+  CACHE_CHECK(check_apart("lens_out", lens_out, ns, "path", path, ns * max_path));
+  CACHE_CHECK(check_apart("lens_out", lens_out, ns, "accepted", accepted, ns));
+  CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
+  int sms;
+  CACHE_CHECK(abi_device(&sms));
+  p.K = K;
+  p.V = V;
+  p.path = path;
+  p.accepted = accepted;
+  p.max_path = (int)max_path;
+  p.lens_out = lens_out;
+  p.status = static_cast<uint32_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  void* tm = abi_timer_begin(path ? ABI_T_COMMIT : ABI_T_APPEND, st);
+  cudaError_t e = launch_cache_append(p, st, &launches);
+  abi_timer_end(tm);
+  return abi_finish(e, launches, path ? "cache commit launch" : "cache append launch");
+}
+
+// bdlm_attn_cached, and with visibility words bdlm_attn_tree.
+bdlm_status attn_call(const void* Qn, const void* Kn, const void* Vn, const int32_t* visible, int64_t words,
+                      const bdlm_cache* cache, const int32_t* row_offsets, int64_t rows, int64_t max_rows, int Hq,
+                      float scale, void* O, bdlm_dtype o_dtype, float* LSE, void* workspace, size_t ws_bytes,
+                      bdlm_stream stream) {
+  CachedParams p;
+  CACHE_CHECK(check_cache(cache, &p.c));
+  CACHE_CHECK(check_rows(p.c, row_offsets, rows, max_rows, &p.r));
+  CACHE_CHECK(check_heads(p.c, p.r, Hq, scale));
+  if (o_dtype != BDLM_BF16 && o_dtype != BDLM_F32) return abi_fail(BDLM_ERR_INVALID_ARG, "bad o_dtype %d", (int)o_dtype);
+  if (!Kn != !Vn) return abi_fail(BDLM_ERR_INVALID_ARG, "Kn and Vn: give both or neither");
+  if (visible && max_rows > 32 * words)
+    return abi_fail(BDLM_ERR_SHAPE, "%lld words hold the bits of fewer rows than max_rows=%lld", (long long)words,
+                    (long long)max_rows);
+  if (rows == 0) return BDLM_OK;
+  CACHE_CHECK(check_ptr("Qn", Qn, 16));
+  if (Kn) {
+    CACHE_CHECK(check_ptr("Kn", Kn, 16));
+    CACHE_CHECK(check_ptr("Vn", Vn, 16));
+  }
+  CACHE_CHECK(check_ptr("O", O, 16));
+  CACHE_CHECK(check_ptr("LSE", LSE, 4));
+  const int64_t nq = rows * Hq * p.c.d, nkv = rows * p.c.Hkv * p.c.d, no = nq * (o_dtype == BDLM_F32 ? 4 : 2);
+  CACHE_CHECK(check_apart("O", O, no, "Qn", Qn, 2 * nq));
+  CACHE_CHECK(check_apart("O", O, no, "Kn", Kn, 2 * nkv));
+  CACHE_CHECK(check_apart("O", O, no, "Vn", Vn, 2 * nkv));
+  const int64_t nl = 4 * rows * Hq;
+  CACHE_CHECK(check_apart("LSE", LSE, nl, "O", O, no));
+  CACHE_CHECK(check_apart("LSE", LSE, nl, "Qn", Qn, 2 * nq));
+  CACHE_CHECK(check_apart("LSE", LSE, nl, "Kn", Kn, 2 * nkv));
+  CACHE_CHECK(check_apart("LSE", LSE, nl, "Vn", Vn, 2 * nkv));
+  CACHE_CHECK(check_apart("O", O, no, "visible", visible, 4 * rows * words));
+  CACHE_CHECK(check_apart("LSE", LSE, nl, "visible", visible, 4 * rows * words));
+  const int64_t flat = max_rows * (Hq / p.c.Hkv);
+  CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(flat, p.c.d)));
+  int sms;
+  CACHE_CHECK(abi_device(&sms));
+  p.sp.group = Hq / p.c.Hkv;
+  p.sp.local = Kn != nullptr;
+  p.Q = Qn;
+  p.K = Kn;
+  p.V = Vn;
+  p.Hq = Hq;
+  p.sl2 = scale * 1.4426950408889634f;
+  p.vis = reinterpret_cast<const uint32_t*>(visible);
+  p.words = (int)words;
+  p.O = O;
+  p.o_f32 = o_dtype == BDLM_F32;
+  p.LSE = LSE;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
+  p.limit_ns = abi_wait_limit_ns();
+  p.sp.tile_rows = cached_tile_rows(flat);
+  const bool small = p.sp.tile_rows <= kSmallRows;
+  p.sp.extra = !small ? kTcExtra : Kn ? kSmallExtraOwn : kSmallExtra;
+  p.sp.keyed = 0;
+  p.whole = 0;
+  p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
+  p.fine = p.part + (int64_t)p.G * 2 * part_floats(p.sp.tile_rows, p.c.d);
+  const int64_t rt = (flat + p.sp.tile_rows - 1) / p.sp.tile_rows;
+  if (small && (int64_t)p.c.max_pages * p.c.page <= kWholeKeys && rt * p.c.Hkv * p.c.n_seqs <= 0x7fffffff) {
+    p.whole = (int)rt;
+    p.G = (int)(rt * p.c.Hkv * p.c.n_seqs);
+  }
+  CachedMaps maps;
+  EncodeTiledFn enc;
+  CACHE_CHECK(abi_encoder(&enc));
+  CACHE_CHECK(encode_codes(enc, &maps.k8, p.c, p.c.k8));
+  if (small) {
+    CACHE_CHECK(encode_codes(enc, &maps.v8, p.c, p.c.v8));
+  } else {
+    // without own keys these maps are not used: any valid tensor encodes
+    CACHE_CHECK(encode_rows(enc, &maps.k, Kn ? Kn : Qn, rows, Kn ? p.c.Hkv : Hq, p.c.d));
+    CACHE_CHECK(encode_rows(enc, &maps.v, Vn ? Vn : Qn, rows, Vn ? p.c.Hkv : Hq, p.c.d));
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int launches = 0;
+  void* tm = abi_timer_begin(ABI_T_ATTN_CACHED, st);
+  cudaError_t e = visible ? (small ? launch_tree_small(maps, p, st, &launches) : launch_tree_tc(maps, p, st, &launches))
+                  : small ? launch_cached_small(maps, p, st, &launches)
+                          : launch_cached_tc(maps, p, st, &launches);
+  abi_timer_end(tm);
+  if (e == cudaSuccess && !p.whole) {
+    tm = abi_timer_begin(ABI_T_CACHED_MERGE, st);
+    e = launch_cached_merge(p, st, &launches);
+    abi_timer_end(tm);
+  }
+  return abi_finish(e, launches, "cached attention launch");
+}
+
+// Row offsets of a call without a cache.
+bdlm_status check_tree_rows(int n_seqs, const int32_t* off, int64_t T, int64_t max_rows, RowsDesc* r) {
+  if (n_seqs <= 0 || n_seqs > 65535) return abi_fail(BDLM_ERR_SHAPE, "n_seqs=%d must be in [1, 65535]", n_seqs);
+  CacheDesc c{};
+  c.n_seqs = n_seqs;
+  CACHE_CHECK(check_rows(c, off, T, max_rows, r));
+  if (max_rows > kMaxTreeRows)
+    return abi_fail(BDLM_ERR_SHAPE, "max_rows=%lld: a tree has at most %d rows", (long long)max_rows, kMaxTreeRows);
+  return BDLM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -161,30 +300,20 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
                               int64_t rows, int64_t max_rows, int32_t* lens_out, void* workspace, size_t ws_bytes,
                               bdlm_stream stream) {
   return guarded([&]() -> bdlm_status {
-    AppendParams p;
-    CACHE_CHECK(check_cache(cache, &p.c));
-    CACHE_CHECK(check_rows(p.c, row_offsets, rows, max_rows, &p.r));
-    if (rows > 0) {
-      CACHE_CHECK(check_ptr("K", K, 16));
-      CACHE_CHECK(check_ptr("V", V, 16));
-    }
-    if (lens_out) CACHE_CHECK(check_ptr("lens_out", lens_out, 4));
-    CACHE_CHECK(check_lens_out(lens_out, cache));
-    CACHE_CHECK(check_apart("lens_out", lens_out, 4 * (int64_t)cache->n_seqs, "row_offsets", row_offsets,
-                            4 * ((int64_t)cache->n_seqs + 1)));
-    CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
-    int sms;
-    CACHE_CHECK(abi_device(&sms));
-    p.K = K;
-    p.V = V;
-    p.lens_out = lens_out;
-    p.status = static_cast<uint32_t*>(workspace);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int launches = 0;
-    void* tm = abi_timer_begin(ABI_T_APPEND, st);
-    cudaError_t e = launch_cache_append(p, st, &launches);
-    abi_timer_end(tm);
-    return abi_finish(e, launches, "cache append launch");
+    return append_call(K, V, cache, nullptr, 0, nullptr, row_offsets, rows, max_rows, lens_out, workspace, ws_bytes,
+                       stream);
+  });
+}
+
+bdlm_status bdlm_cache_commit(const void* K, const void* V, const bdlm_cache* cache, const int32_t* path,
+                              int64_t max_path, const int32_t* accepted, const int32_t* row_offsets, int64_t rows,
+                              int64_t max_rows, int32_t* lens_out, void* workspace, size_t ws_bytes,
+                              bdlm_stream stream) {
+  return guarded([&]() -> bdlm_status {
+    CACHE_CHECK(check_ptr("path", path, 4));
+    CACHE_CHECK(check_ptr("accepted", accepted, 4));
+    return append_call(K, V, cache, path, max_path, accepted, row_offsets, rows, max_rows, lens_out, workspace, ws_bytes,
+                       stream);
   });
 }
 
@@ -192,80 +321,24 @@ bdlm_status bdlm_attn_cached(const void* Qn, const void* Kn, const void* Vn, con
                              const int32_t* row_offsets, int64_t rows, int64_t max_rows, int Hq, float scale, void* O,
                              bdlm_dtype o_dtype, float* LSE, void* workspace, size_t ws_bytes, bdlm_stream stream) {
   return guarded([&]() -> bdlm_status {
-    CachedParams p;
-    CACHE_CHECK(check_cache(cache, &p.c));
-    CACHE_CHECK(check_rows(p.c, row_offsets, rows, max_rows, &p.r));
-    CACHE_CHECK(check_heads(p.c, p.r, Hq, scale));
-    if (o_dtype != BDLM_BF16 && o_dtype != BDLM_F32) return abi_fail(BDLM_ERR_INVALID_ARG, "bad o_dtype %d", (int)o_dtype);
-    if (!Kn != !Vn) return abi_fail(BDLM_ERR_INVALID_ARG, "Kn and Vn: give both or neither");
-    if (rows == 0) return BDLM_OK;
-    CACHE_CHECK(check_ptr("Qn", Qn, 16));
-    if (Kn) {
-      CACHE_CHECK(check_ptr("Kn", Kn, 16));
-      CACHE_CHECK(check_ptr("Vn", Vn, 16));
+    return attn_call(Qn, Kn, Vn, nullptr, 0, cache, row_offsets, rows, max_rows, Hq, scale, O, o_dtype, LSE, workspace,
+                     ws_bytes, stream);
+  });
+}
+
+bdlm_status bdlm_attn_tree(const void* Qn, const void* Kn, const void* Vn, const int32_t* visible, int64_t words,
+                           const bdlm_cache* cache, const int32_t* row_offsets, int64_t rows, int64_t max_rows, int Hq,
+                           float scale, void* O, bdlm_dtype o_dtype, float* LSE, void* workspace, size_t ws_bytes,
+                           bdlm_stream stream) {
+  return guarded([&]() -> bdlm_status {
+    if (words <= 0 || words > (int64_t)1 << 19)
+      return abi_fail(BDLM_ERR_SHAPE, "words=%lld must be in [1, 2^19]", (long long)words);
+    if (rows != 0) {
+      if (!Kn || !Vn) return abi_fail(BDLM_ERR_INVALID_ARG, "Kn and Vn: a tree's rows see themselves, give both");
+      CACHE_CHECK(check_ptr("visible", visible, 4));
     }
-    CACHE_CHECK(check_ptr("O", O, 16));
-    CACHE_CHECK(check_ptr("LSE", LSE, 4));
-    const int64_t nq = rows * Hq * p.c.d, nkv = rows * p.c.Hkv * p.c.d, no = nq * (o_dtype == BDLM_F32 ? 4 : 2);
-    CACHE_CHECK(check_apart("O", O, no, "Qn", Qn, 2 * nq));
-    CACHE_CHECK(check_apart("O", O, no, "Kn", Kn, 2 * nkv));
-    CACHE_CHECK(check_apart("O", O, no, "Vn", Vn, 2 * nkv));
-    const int64_t nl = 4 * rows * Hq;
-    CACHE_CHECK(check_apart("LSE", LSE, nl, "O", O, no));
-    CACHE_CHECK(check_apart("LSE", LSE, nl, "Qn", Qn, 2 * nq));
-    CACHE_CHECK(check_apart("LSE", LSE, nl, "Kn", Kn, 2 * nkv));
-    CACHE_CHECK(check_apart("LSE", LSE, nl, "Vn", Vn, 2 * nkv));
-    const int64_t flat = max_rows * (Hq / p.c.Hkv);
-    CACHE_CHECK(check_space(workspace, ws_bytes, kHeader + attn_space(flat, p.c.d)));
-    int sms;
-    CACHE_CHECK(abi_device(&sms));
-    p.sp.group = Hq / p.c.Hkv;
-    p.sp.local = Kn != nullptr;
-    p.Q = Qn;
-    p.K = Kn;
-    p.V = Vn;
-    p.Hq = Hq;
-    p.sl2 = scale * 1.4426950408889634f;
-    p.O = O;
-    p.o_f32 = o_dtype == BDLM_F32;
-    p.LSE = LSE;
-    p.status = static_cast<uint32_t*>(workspace);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
-    p.limit_ns = abi_wait_limit_ns();
-    p.sp.tile_rows = cached_tile_rows(flat);
-    const bool small = p.sp.tile_rows <= kSmallRows;
-    p.sp.extra = !small ? kTcExtra : Kn ? kSmallExtraOwn : kSmallExtra;
-    p.sp.keyed = 0;
-    p.whole = 0;
-    p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));
-    p.fine = p.part + (int64_t)p.G * 2 * part_floats(p.sp.tile_rows, p.c.d);
-    const int64_t rt = (flat + p.sp.tile_rows - 1) / p.sp.tile_rows;
-    if (small && (int64_t)p.c.max_pages * p.c.page <= kWholeKeys && rt * p.c.Hkv * p.c.n_seqs <= 0x7fffffff) {
-      p.whole = (int)rt;
-      p.G = (int)(rt * p.c.Hkv * p.c.n_seqs);
-    }
-    CachedMaps maps;
-    EncodeTiledFn enc;
-    CACHE_CHECK(abi_encoder(&enc));
-    CACHE_CHECK(encode_codes(enc, &maps.k8, p.c, p.c.k8));
-    if (small) {
-      CACHE_CHECK(encode_codes(enc, &maps.v8, p.c, p.c.v8));
-    } else {
-      // without own keys these maps are not used: any valid tensor encodes
-      CACHE_CHECK(encode_rows(enc, &maps.k, Kn ? Kn : Qn, rows, Kn ? p.c.Hkv : Hq, p.c.d));
-      CACHE_CHECK(encode_rows(enc, &maps.v, Vn ? Vn : Qn, rows, Vn ? p.c.Hkv : Hq, p.c.d));
-    }
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int launches = 0;
-    void* tm = abi_timer_begin(ABI_T_ATTN_CACHED, st);
-    cudaError_t e = small ? launch_cached_small(maps, p, st, &launches) : launch_cached_tc(maps, p, st, &launches);
-    abi_timer_end(tm);
-    if (e == cudaSuccess && !p.whole) {
-      tm = abi_timer_begin(ABI_T_CACHED_MERGE, st);
-      e = launch_cached_merge(p, st, &launches);
-      abi_timer_end(tm);
-    }
-    return abi_finish(e, launches, "cached attention launch");
+    return attn_call(Qn, Kn, Vn, visible, words, cache, row_offsets, rows, max_rows, Hq, scale, O, o_dtype, LSE,
+                     workspace, ws_bytes, stream);
   });
 }
 
@@ -355,6 +428,126 @@ bdlm_status bdlm_cache_evict(const bdlm_cache* cache, const float* weights, cons
     cudaError_t e = launch_cache_evict(p, st, &launches);
     abi_timer_end(tm);
     return abi_finish(e, launches, "cache evict launch");
+  });
+}
+
+bdlm_status bdlm_tree_mask(const int32_t* parents, const bdlm_cache* cache, const int32_t* row_offsets, int64_t rows,
+                           int64_t max_rows, int32_t* visible, int64_t words, int32_t* positions, void* workspace,
+                           size_t ws_bytes, bdlm_stream stream) {
+  return guarded([&]() -> bdlm_status {
+    TreeMaskParams p;
+    CACHE_CHECK(check_cache(cache, &p.c));
+    CACHE_CHECK(check_tree_rows(p.c.n_seqs, row_offsets, rows, max_rows, &p.r));
+    if (words <= 0 || words > (int64_t)1 << 19)
+      return abi_fail(BDLM_ERR_SHAPE, "words=%lld must be in [1, 2^19]", (long long)words);
+    if (max_rows > 32 * words)
+      return abi_fail(BDLM_ERR_SHAPE, "%lld words hold the bits of fewer rows than max_rows=%lld", (long long)words,
+                      (long long)max_rows);
+    if (rows == 0) return BDLM_OK;
+    CACHE_CHECK(check_ptr("parents", parents, 4));
+    CACHE_CHECK(check_ptr("visible", visible, 4));
+    CACHE_CHECK(check_ptr("positions", positions, 4));
+    const int64_t ns = 4 * (int64_t)cache->n_seqs, nr = 4 * rows;
+    const struct { const char* name; const void* at; int64_t bytes; } in[3] = {
+        {"parents", parents, nr}, {"row_offsets", row_offsets, ns + 4}, {"the cache's lens", cache->lens, ns}};
+    for (const auto& x : in) {
+      CACHE_CHECK(check_apart("visible", visible, nr * words, x.name, x.at, x.bytes));
+      CACHE_CHECK(check_apart("positions", positions, nr, x.name, x.at, x.bytes));
+    }
+    CACHE_CHECK(check_apart("positions", positions, nr, "visible", visible, nr * words));
+    CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
+    int sms;
+    CACHE_CHECK(abi_device(&sms));
+    p.parents = parents;
+    p.vis = reinterpret_cast<uint32_t*>(visible);
+    p.words = (int)words;
+    p.positions = positions;
+    p.status = static_cast<uint32_t*>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    void* tm = abi_timer_begin(ABI_T_TREE_MASK, st);
+    cudaError_t e = launch_tree_mask(p, st, &launches);
+    abi_timer_end(tm);
+    return abi_finish(e, launches, "tree mask launch");
+  });
+}
+
+size_t bdlm_workspace_size_verify(int n_seqs, int64_t max_rows, int64_t V) {
+  if (n_seqs <= 0 || n_seqs > 65535 || max_rows <= 0 || max_rows > kMaxTreeRows || V <= 0 || V > (int64_t)1 << 30) return 0;
+  return kHeader;
+}
+
+bdlm_status bdlm_tree_verify(const int32_t* parents, const int32_t* tokens, const void* target, const void* draft,
+                             bdlm_dtype p_dtype, int64_t V, int64_t target_stride, int64_t draft_stride,
+                             const float* uniforms, const float* sample, int n_seqs, const int32_t* row_offsets,
+                             int64_t rows, int64_t max_rows, int32_t* path, int64_t max_path, int32_t* accepted,
+                             int32_t* next_token, void* workspace, size_t ws_bytes, bdlm_stream stream) {
+  return guarded([&]() -> bdlm_status {
+    VerifyParams p;
+    CACHE_CHECK(check_tree_rows(n_seqs, row_offsets, rows, max_rows, &p.r));
+    if (p_dtype != BDLM_BF16 && p_dtype != BDLM_F32) return abi_fail(BDLM_ERR_INVALID_ARG, "bad p_dtype %d", (int)p_dtype);
+    if (V <= 0 || V > (int64_t)1 << 30) return abi_fail(BDLM_ERR_SHAPE, "V=%lld must be in [1, 2^30]", (long long)V);
+    if (max_path <= 0 || max_path > (int64_t)1 << 24)
+      return abi_fail(BDLM_ERR_SHAPE, "max_path=%lld must be in [1, 2^24]", (long long)max_path);
+    const int64_t e = p_dtype == BDLM_F32 ? 4 : 2, ns = 4 * (int64_t)n_seqs, nr = 4 * rows;
+    const struct { const char* name; const void* at; int64_t stride; } probs[2] = {{"target", target, target_stride},
+                                                                                 {"draft", draft, draft_stride}};
+    for (const auto& x : probs) {
+      if (&x == &probs[1] && !draft) break;
+      if (rows > 0) CACHE_CHECK(check_ptr(x.name, x.at, (unsigned)e));
+      if (x.stride < V || x.stride > (int64_t)1 << 40)
+        return abi_fail(BDLM_ERR_SHAPE, "%s's rows are %lld values apart, at least V=%lld are needed", x.name,
+                        (long long)x.stride, (long long)V);
+    }
+    if (rows > 0) {
+      CACHE_CHECK(check_ptr("parents", parents, 4));
+      CACHE_CHECK(check_ptr("tokens", tokens, 4));
+      CACHE_CHECK(check_ptr("uniforms", uniforms, 4));
+    }
+    CACHE_CHECK(check_ptr("sample", sample, 4));
+    CACHE_CHECK(check_ptr("path", path, 4));
+    CACHE_CHECK(check_ptr("accepted", accepted, 4));
+    CACHE_CHECK(check_ptr("next_token", next_token, 4));
+    const struct { const char* name; const void* at; int64_t bytes; } out[3] = {
+        {"path", path, ns * max_path}, {"accepted", accepted, ns}, {"next_token", next_token, ns}};
+    const struct { const char* name; const void* at; int64_t bytes; } in[7] = {
+        {"parents", parents, nr},
+        {"tokens", tokens, nr},
+        {"target", target, rows > 0 ? ((rows - 1) * target_stride + V) * e : 0},
+        {"draft", draft, rows > 0 ? ((rows - 1) * draft_stride + V) * e : 0},
+        {"uniforms", uniforms, nr},
+        {"sample", sample, ns},
+        {"row_offsets", row_offsets, ns + 4}};
+    for (int i = 0; i < 3; ++i) {
+      for (const auto& x : in) CACHE_CHECK(check_apart(out[i].name, out[i].at, out[i].bytes, x.name, x.at, x.bytes));
+      for (int j = 0; j < i; ++j)
+        CACHE_CHECK(check_apart(out[i].name, out[i].at, out[i].bytes, out[j].name, out[j].at, out[j].bytes));
+    }
+    CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
+    int sms;
+    CACHE_CHECK(abi_device(&sms));
+    p.n_seqs = n_seqs;
+    p.parents = parents;
+    p.tokens = tokens;
+    p.target = target;
+    p.draft = draft;
+    p.bf16 = p_dtype == BDLM_BF16;
+    p.V = V;
+    p.target_stride = target_stride;
+    p.draft_stride = draft_stride;
+    p.uniforms = uniforms;
+    p.sample = sample;
+    p.path = path;
+    p.max_path = (int)max_path;
+    p.accepted = accepted;
+    p.next_token = next_token;
+    p.status = static_cast<uint32_t*>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int launches = 0;
+    void* tm = abi_timer_begin(ABI_T_VERIFY, st);
+    cudaError_t err = launch_tree_verify(p, sms, st, &launches);
+    abi_timer_end(tm);
+    return abi_finish(err, launches, "tree verify launch");
   });
 }
 

@@ -57,8 +57,10 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, __half2 r) {
 // the measured copy rate; 16 sequences' blocks of 512 (43 MB) 14.3 us, half of it
 // before the first bytes arrive; 64 single tokens 7 us, a launch.  (A CTA per
 // block, one chunk per thread at a time: 203 us for the first.)
+// PATH (commit): the new tokens are the rows path[s, 0 .. accepted[s]) of the
+// sequence instead of all of them in order.
 constexpr int kAppendThreads = 256;
-template <int HD, int TT>
+template <int HD, int TT, bool PATH>
 __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_kernel(const AppendParams p) {
   constexpr int CH = HD / 16;                     // 16-value chunks of a token
   constexpr int kThreads = kAppendThreads * TT / 64;
@@ -72,6 +74,11 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
   const SeqView v = seq_view(c, p.r, s, bad);
   const int64_t cap = (int64_t)c.max_pages << c.lp;
   int rows = v.rows;
+  if (PATH) {
+    rows = p.accepted[s];
+    if (rows < 0 || rows > p.max_path) bad |= kStatusBadTree;
+    if (bad) rows = 0;
+  }
   if (v.len + (int64_t)rows > cap) {
     bad |= kStatusBadLen;
     rows = (int)(cap - v.len);
@@ -98,8 +105,14 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
   uint4 x[NT][2];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kThreads + tid, tok = first + k / CH;
-    const bool ok = tok >= 0 && tok < rows;
+    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kThreads + tid;
+    int tok = first + k / CH;
+    bool ok = tok >= 0 && tok < rows;
+    if (PATH && ok) {
+      tok = __ldg(p.path + (int64_t)s * p.max_path + tok);
+      ok = tok >= 0 && tok < v.rows;  // (a row that is not the sequence's: zeros)
+      if (!ok) atomicOr(p.status + kContentsWord, kStatusBadTree);
+    }
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv ? p.V : p.K) +
                                                       ((v.row0 + (ok ? tok : 0)) * c.Hkv + h) * HD) + 2 * (k % CH);
     x[i][0] = ok ? __ldg(src) : make_uint4(0, 0, 0, 0);
@@ -540,12 +553,17 @@ cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
   return e;
 }
 
+template <bool PATH>
+static auto append_kernel(int d, int TT) {
+  return d == 128 ? (TT == 128 ? bdlm_cache_append_kernel<128, 128, PATH> : bdlm_cache_append_kernel<128, 64, PATH>)
+                  : (TT == 128 ? bdlm_cache_append_kernel<64, 128, PATH> : bdlm_cache_append_kernel<64, 64, PATH>);
+}
+
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* launches) {
   const int TT = p.c.page > 64 ? 128 : 64;
-  // groups of TT slots that max_rows new tokens can touch
-  const dim3 grid((unsigned)((p.r.max_rows + TT - 2) / TT + 1), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
-  auto k = p.c.d == 128 ? (TT == 128 ? bdlm_cache_append_kernel<128, 128> : bdlm_cache_append_kernel<128, 64>)
-                        : (TT == 128 ? bdlm_cache_append_kernel<64, 128> : bdlm_cache_append_kernel<64, 64>);
+  // groups of TT slots that max_rows (commit: max_path) new tokens can touch
+  const dim3 grid((unsigned)(((p.path ? p.max_path : p.r.max_rows) + TT - 2) / TT + 1), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
+  auto k = p.path ? append_kernel<true>(p.c.d, TT) : append_kernel<false>(p.c.d, TT);
   k<<<grid, kAppendThreads * TT / 64, 0, st>>>(p);
   ++*launches;
   return cudaGetLastError();

@@ -13,6 +13,9 @@ struct AppendParams {
   CacheDesc c;
   RowsDesc r;
   const void *K, *V;  // bf16 [T, Hkv, d]
+  const int32_t* path;      // commit: [n_seqs, max_path] rows of their sequences, the first accepted[s] of them; else null
+  const int32_t* accepted;  // [n_seqs]
+  int max_path;
   int32_t* lens_out;
   uint32_t* status;
 };

@@ -15,6 +15,8 @@ struct CachedParams {
   const void *Q, *K, *V;  // bf16 [T, Hq, d], [T, Hkv, d]
   int Hq;
   float sl2;  // softmax scale * log2(e)
+  const uint32_t* vis;  // (trees) [T, words]: bit j % 32 of word j / 32: the row sees row j of its sequence
+  int words;
   void* O;
   int o_f32;
   float* LSE;
@@ -70,6 +72,7 @@ struct CachedMaps {
   CUtensorMap k8, v8, k, v;
 };
 cudaError_t launch_cached_tc(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
+cudaError_t launch_tree_tc(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 // Longest cache, in tokens, up to which the mma.sync kernel gives each segment
 // one CTA, without a list to walk and a merge.  1 / 32 sequences of 8 KV heads (in a
 // graph, warm): whole against split 8.0 / 8.9 and 10.1 / 13.3 us at 256 tokens, 14.1 /
@@ -78,7 +81,7 @@ constexpr int kWholeKeys = 1024;
 // AttnSplit::extra: what a segment costs beside its units, in units.  The
 // mma.sync kernel spends about 6000 cycles to begin and end a segment, 5000 more
 // on its own rows' keys and 2300 on a unit: with 1 / 3 / 5, the token batch of
-// cached_small.cu took 220 / 207 / 205 us with own keys and 205 / 204 / 206 without,
+// cached_small.cuh took 220 / 207 / 205 us with own keys and 205 / 204 / 206 without,
 // blocks of 8 over 16 short sequences 70 / 47 / 42 and 48 / 40 / 41.  The tcgen05
 // kernels spend 10 to 20 thousand cycles to end a segment and begin the next, and
 // 2000 (split) or 4000 (pairs) on a unit: with 0 / 6, when it was tried, blocks of 32 and 128 took 130 / 106 and 293 /
@@ -86,6 +89,7 @@ constexpr int kWholeKeys = 1024;
 constexpr int kSmallExtra = 3, kSmallExtraOwn = 5, kTcExtra = 6;
 
 cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
+cudaError_t launch_tree_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches);
 
 }  // namespace bdlm

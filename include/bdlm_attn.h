@@ -540,8 +540,9 @@ size_t bdlm_workspace_size_verify(int n_seqs, int64_t max_rows, int64_t V);
  * gets 0 and -1; one whose p is 0 everywhere the token -1 (reported).  Rows whose
  * parent or token is out of range, and those other than row 0 whose parent is -1, are not
  * accepted.
- * Probabilities below 0 (above 1) and NaN count as 0 (as 1 and 0), and are summed as
- * whole numbers of 2^-62; a row's sum must stay below 4.  Tests are made in 64 bits.
+ * Probabilities below 0 (above 1) and NaN count as 0 (as 1 and 0); a row's sum must stay
+ * below 4.  Tests are made in 64 bits, sums in twice fp32's width, joined as whole
+ * numbers of 2^-62.
  * Deterministic; outputs overlap neither inputs nor each other. */
 bdlm_status bdlm_tree_verify(const int32_t* parents, const int32_t* tokens, const void* target, const void* draft,
                              bdlm_dtype p_dtype, int64_t V, int64_t target_stride, int64_t draft_stride,

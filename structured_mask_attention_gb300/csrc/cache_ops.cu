@@ -91,17 +91,6 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
     bad = 0;
   }
   if (rows <= 0 || first >= rows) return;  // (without new rows a half-filled page, maybe another sequence's too, stays as it is)
-  if (tid < TT / 16) {
-    const int f = first + (tid << c.lp);  // new token of the block's first slot
-    int id = -1;
-    if (tid < (TT >> c.lp) && f < rows && f + c.page > 0) id = page_id(c, s, (base >> c.lp) + tid, bad);
-    s_page[tid] = id;
-    const int64_t b = (int64_t)max(id, 0) * c.Hkv + h;
-    s_was[0][tid] = id >= 0 && f < 0 ? c.ks[b] : 0.f;
-    s_was[1][tid] = id >= 0 && f < 0 ? c.vs[b] : 0.f;
-    s_amax[0][tid] = s_amax[1][tid] = 0;
-    if (bad) atomicOr(p.status + kContentsWord, bad);
-  }
   uint4 x[NT][2];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
@@ -117,6 +106,18 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
                                                       ((v.row0 + (ok ? tok : 0)) * c.Hkv + h) * HD) + 2 * (k % CH);
     x[i][0] = ok ? __ldg(src) : make_uint4(0, 0, 0, 0);
     x[i][1] = ok ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+  }
+  // (behind the loads: a page's id and its scale are two more round trips)
+  if (tid < TT / 16) {
+    const int f = first + (tid << c.lp);  // new token of the block's first slot
+    int id = -1;
+    if (tid < (TT >> c.lp) && f < rows && f + c.page > 0) id = page_id(c, s, (base >> c.lp) + tid, bad);
+    s_page[tid] = id;
+    const int64_t b = (int64_t)max(id, 0) * c.Hkv + h;
+    s_was[0][tid] = id >= 0 && f < 0 ? c.ks[b] : 0.f;
+    s_was[1][tid] = id >= 0 && f < 0 ? c.vs[b] : 0.f;
+    s_amax[0][tid] = s_amax[1][tid] = 0;
+    if (bad) atomicOr(p.status + kContentsWord, bad);
   }
   __syncthreads();
 #pragma unroll

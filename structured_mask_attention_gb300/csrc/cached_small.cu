@@ -95,8 +95,16 @@ __global__ void __launch_bounds__(kMergeThreads) bdlm_cached_merge_kernel(const 
 
 }  // namespace
 
+template <int HD, bool FINE>
+static cudaError_t launch_rows(const CachedMaps& m, const CachedParams& p, cudaStream_t st) {
+  return p.sp.tile_rows == 16 ? launch<HD, 1, 1, FINE, false>(m, p, st) : launch<HD, 1, 2, FINE, false>(m, p, st);
+}
+
 cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches) {
-  return launch_small<false>(m, p, st, launches);
+  const cudaError_t e = p.c.d == 128 ? (p.o_f32 ? launch_rows<128, true>(m, p, st) : launch_rows<128, false>(m, p, st))
+                                     : (p.o_f32 ? launch_rows<64, true>(m, p, st) : launch_rows<64, false>(m, p, st));
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t st, int* launches) {

@@ -28,8 +28,19 @@
 namespace bdlm {
 namespace {
 
-constexpr int kWarps = 4;                       // warps that compute; one more loads
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 4;  // warps that compute; one more loads
+// With two row tiles to a warp (RT = 2) its state takes 200 registers and more, and of ten
+// warps on the SM's four register files three share one: 168 each.  So the loader
+// gets a warpgroup of its own (three of its warps leave) and hands its registers over.
+template <int RT>
+struct Roles {
+  static constexpr bool kSplit = RT > 1;
+  static constexpr int kThreads = kSplit ? 256 : 32 * (kWarps + 1);
+  static constexpr int kFirst = kSplit ? 4 : 0;  // the first computing warp
+  static constexpr int kLoader = kSplit ? 0 : kWarps;
+  static constexpr int kRegs = 128, kRegsLoad = 24, kRegsCompute = 232;  // (split)
+  static_assert(128 * (kRegsLoad + kRegsCompute) <= 256 * kRegs, "register split exceeds the block");
+};
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -170,17 +181,19 @@ struct LayS {
   static constexpr int kAlloc = kBytes + 1024;    // (aligned to 1024)
 };
 
-template <int HD, int MT, bool FINE, bool TREE>
-__global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
+template <int HD, int RT, int RG, bool FINE, bool TREE>
+__global__ void __launch_bounds__(Roles<RT>::kThreads, kSmallCtasPerSm)
     bdlm_cached_small_kernel(const __grid_constant__ CUtensorMap tK8, const __grid_constant__ CUtensorMap tV8,
                              const CachedParams p) {
   using LY = LayS<HD>;
   constexpr int NS = LY::NS;
   constexpr int KH = HD / 64;   // 64-byte halves of a key's codes
   constexpr int VW = HD / 32;   // words of a thread's piece of a value row
-  constexpr int KG = kWarps / MT;         // key groups
+  constexpr int KG = kWarps / RG;         // key groups
   constexpr int kStep = 128 / KG / 32;    // 32-key steps of a warp per tile
-  constexpr int kRows = 16 * MT;
+  constexpr int kRows = 16 * RT * RG;
+  constexpr int kFrag = KH * 4 * 512;     // bytes of a row tile's query fragments
+  static_assert(RT * kFrag <= 16 * (HD + 4) * 4, "the fragments fit a warp's part of the reduction buffer");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -193,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
   auto KE = [&](uint32_t i) -> uint32_t { return base + LY::kBar + 8 * (NS + i); };
   auto VF = [&](uint32_t i) -> uint32_t { return base + LY::kBar + 8 * (2 * NS + i); };
   auto VE = [&](uint32_t i) -> uint32_t { return base + LY::kBar + 8 * (3 * NS + i); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  using R = Roles<RT>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < NS; ++i) {
       mbar_init(KF(i), 1);
@@ -228,7 +242,11 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
     seg = o.seg;
   }
 
-  if (warp == kWarps) {
+  if (R::kSplit ? threadIdx.x < 128 : (int)(threadIdx.x >> 5) == R::kLoader) {
+    if (R::kSplit) {
+      setmaxnreg_dec<R::kRegsLoad>();
+      if (threadIdx.x >= 32) return;
+    }
     // -------------------------------------------------- loader
     uint32_t slot = 0, ph = 1, tc = 0;
     const uint32_t page_bytes = (uint32_t)(c.page * HD), page_groups = first_groups(c.page);
@@ -310,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
   // ---------------------------------------------------- the computing warps
   // After a timeout (ok false) they go on without waiting, so that all of them
   // meet at the same barriers; the call reports the timeout.
-  const int mt = warp / KG, kg = warp % KG;
+  if (R::kSplit) setmaxnreg_inc<R::kRegsCompute>();
+  const int warp = (int)(threadIdx.x >> 5) - R::kFirst;
+  const int rg = warp / KG, kg = warp % KG;
   auto perm = [](int x) { return HD == 128 ? (x >> 1) | ((x & 1) << 2) : x; };
   uint32_t slot = 0, ph = 0, tc = 0;
   bool ok = true;
@@ -324,53 +344,61 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
     // (their fragments stay in the warp's part of the reduction buffer: registers
     // go to the keys in flight)
     const uint32_t qs = base + LY::kRed + warp * (16 * (HD + 4) * 4) + lane * 16;
-    float cq[2];
-    int64_t qoff[2];
-    bool live[2];
-    uint32_t q[KH * 4][4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int fr = pos.rt * kRows + 16 * mt + g + 8 * r, tok = fr / p.sp.group;
-      live[r] = tok < seg.v.rows;
+    // row r (of two: g, g + 8) of the warp's row tile x, as a token of the sequence and a query head
+    auto token = [&](int x, int r) { return (pos.rt * kRows + 16 * (RT * rg + x) + g + 8 * r) / p.sp.group; };
+    auto query = [&](int x, int r) -> const __nv_bfloat16* {  // null: no such row
+      const int fr = pos.rt * kRows + 16 * (RT * rg + x) + g + 8 * r, tok = fr / p.sp.group;
+      if (tok >= seg.v.rows) return nullptr;
       const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
-      qoff[r] = ((seg.v.row0 + (live[r] ? tok : 0)) * p.Hq + head) * HD;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.Q) + qoff[r];
-      uint32_t w[KH][8];
-      uint32_t amax = 0;
+      return static_cast<const __nv_bfloat16*>(p.Q) + ((seg.v.row0 + tok) * p.Hq + head) * HD;
+    };
+    float cq[RT][2];
 #pragma unroll
-      for (int h = 0; h < KH; ++h) {
-        const uint4 x = live[r] ? ldg16(src + 64 * h + 16 * t) : make_uint4(0, 0, 0, 0);
-        const uint4 y = live[r] ? ldg16(src + 64 * h + 16 * t + 8) : make_uint4(0, 0, 0, 0);
-        w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
-        w[h][4] = y.x; w[h][5] = y.y; w[h][6] = y.z; w[h][7] = y.w;
+    for (int x = 0; x < RT; ++x) {
+      uint32_t q[KH * 4][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, max(w[h][i] & 0x7fffu, (w[h][i] >> 16) & 0x7fffu));
-      }
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      int e = 14 + 127 - (int)(amax >> 7);  // bf16 exponent field
-      if (amax >= 0x7f80u || amax == 0) e = 0;
-      e = min(e, 126);
-      const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-      cq[r] = p.sl2 * __uint_as_float((uint32_t)(127 - e) << 23);
+      for (int r = 0; r < 2; ++r) {
+        const __nv_bfloat16* src = query(x, r);
+        uint32_t w[KH][8];
+        uint32_t amax = 0;
 #pragma unroll
-      for (int h = 0; h < KH; ++h)
+        for (int h = 0; h < KH; ++h) {
+          const uint4 y = src ? ldg16(src + 64 * h + 16 * t) : make_uint4(0, 0, 0, 0);
+          const uint4 z = src ? ldg16(src + 64 * h + 16 * t + 8) : make_uint4(0, 0, 0, 0);
+          w[h][0] = y.x; w[h][1] = y.y; w[h][2] = y.z; w[h][3] = y.w;
+          w[h][4] = z.x; w[h][5] = z.y; w[h][6] = z.z; w[h][7] = z.w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          q[4 * h + i][r] = pack_half2(bf_lo(w[h][2 * i]) * f, bf_hi(w[h][2 * i]) * f);
-          q[4 * h + i][2 + r] = pack_half2(bf_lo(w[h][2 * i + 1]) * f, bf_hi(w[h][2 * i + 1]) * f);
+          for (int i = 0; i < 8; ++i) amax = max(amax, max(w[h][i] & 0x7fffu, (w[h][i] >> 16) & 0x7fffu));
         }
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        int e = 14 + 127 - (int)(amax >> 7);  // bf16 exponent field
+        if (amax >= 0x7f80u || amax == 0) e = 0;
+        e = min(e, 126);
+        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+        cq[x][r] = p.sl2 * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int h = 0; h < KH; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            q[4 * h + i][r] = pack_half2(bf_lo(w[h][2 * i]) * f, bf_hi(w[h][2 * i]) * f);
+            q[4 * h + i][2 + r] = pack_half2(bf_lo(w[h][2 * i + 1]) * f, bf_hi(w[h][2 * i + 1]) * f);
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < KH * 4; ++k) st_shared_v4(qs + x * kFrag + k * 512, q[k][0], q[k][1], q[k][2], q[k][3]);
     }
-#pragma unroll
-    for (int k = 0; k < KH * 4; ++k) st_shared_v4(qs + k * 512, q[k][0], q[k][1], q[k][2], q[k][3]);
     __syncwarp();
-    State<HD> st;
+    State<HD> st[RT];
 #pragma unroll
-    for (int j = 0; j < HD / 8; ++j)
+    for (int x = 0; x < RT; ++x) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st.o[j][i] = 0.f;
-    st.m[0] = st.m[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.f;
+      for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st[x].o[j][i] = 0.f;
+      st[x].m[0] = st[x].m[1] = -INFINITY;
+      st[x].l[0] = st[x].l[1] = 0.f;
+    }
 
     // ---- cached keys
     const int kc = min(je, seg.ktiles);
@@ -383,10 +411,12 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
 #pragma unroll 1
       for (int step = 0; step < kStep; ++step) {
         const int kb = (kg * kStep + step) * 32;  // first key of the step in the tile
-        float s[4][4];
+        float s[RT][4][4];
         const uint32_t sk = base + LY::kK + slot * LY::kTile;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int y = 0; y < RT; ++y)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[y][i][0] = s[y][i][1] = s[y][i][2] = s[y][i][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < KH; ++h) {
           uint32_t w[4][4];  // four columns' halves; their sums advance side by side
@@ -399,10 +429,15 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 a = lds16(qs + (4 * h + k) * 512);
+            uint4 a[RT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_f16(s[i], a.x, a.y, a.z, a.w, e4m3x2_to_half2(w[i][k]), e4m3x2_to_half2(w[i][k] >> 16));
+            for (int y = 0; y < RT; ++y) a[y] = lds16(qs + y * kFrag + (4 * h + k) * 512);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t b0 = e4m3x2_to_half2(w[i][k]), b1 = e4m3x2_to_half2(w[i][k] >> 16);
+#pragma unroll
+              for (int y = 0; y < RT; ++y) mma_f16(s[y][i], a[y].x, a[y].y, a[y].z, a[y].w, b0, b1);
+            }
           }
         }
         float iv[2];
@@ -412,30 +447,37 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
           const float ks = si.s[b], lv = si.lv[b];
           iv[x] = si.iv[b];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int y = 0; y < RT; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[2 * x + i][e] = fmaf(s[2 * x + i][e], cq[e >> 1] * ks, lv);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[y][2 * x + i][e] = fmaf(s[y][2 * x + i][e], cq[y][e >> 1] * ks, lv);
           if (!full)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (kb + 16 * x + 8 * i + perm(2 * t + (e & 1)) >= left || ((gone >> b) & 1)) s[2 * x + i][e] = -INFINITY;
+                if (kb + 16 * x + 8 * i + perm(2 * t + (e & 1)) >= left || ((gone >> b) & 1))
+#pragma unroll
+                  for (int y = 0; y < RT; ++y) s[y][2 * x + i][e] = -INFINITY;
         }
         if (step == kStep - 1) {  // K's slot and its info are read
           __syncwarp();
           if (lane == 0) mbar_arrive(KE(slot));
         }
-        softmax_step<HD, 4>(st, s, iv);
-        uint32_t pa[2][4], pr[2][4];
+        uint32_t pa[RT][2][4], pr[RT][2][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int y = 0; y < RT; ++y) {
+          softmax_step<HD, 4>(st[y], s[y], iv);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = s[2 * x + (i >> 1)][2 * (i & 1)], b = s[2 * x + (i >> 1)][2 * (i & 1) + 1];
-            pa[x][i] = pack_half2(a, b);
-            if (FINE) pr[x][i] = rest_half2(pa[x][i], a, b);
-          }
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = s[y][2 * x + (i >> 1)][2 * (i & 1)], b = s[y][2 * x + (i >> 1)][2 * (i & 1) + 1];
+              pa[y][x][i] = pack_half2(a, b);
+              if (FINE) pr[y][x][i] = rest_half2(pa[y][x][i], a, b);
+            }
+        }
         if (step == 0 && ok) ok = mbar_wait(VF(slot), ph, wd, 73);
         const uint32_t sv = base + LY::kV + slot * LY::kTile;
 #pragma unroll
@@ -465,15 +507,20 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const uint32_t b0 = e4m3x2_to_half2(lo >> (16 * y)), b1 = e4m3x2_to_half2(hi >> (16 * y));
-                float (&o)[4] = st.o[4 * w + 2 * hf + y];
-                if (FINE) {
-                  float z[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma_f16(z, pa[x][0], pa[x][1], pa[x][2], pa[x][3], b0, b1);
-                  mma_f16(z, pr[x][0], pr[x][1], pr[x][2], pr[x][3], b0, b1);
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) o[e] += z[e];
-                } else {
-                  mma_f16(o, pa[x][0], pa[x][1], pa[x][2], pa[x][3], b0, b1);
+                for (int z = 0; z < RT; ++z) {
+                  float (&o)[4] = st[z].o[4 * w + 2 * hf + y];
+                  const uint32_t(&a)[4] = pa[z][x];
+                  if (FINE) {
+                    const uint32_t(&r)[4] = pr[z][x];
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(sum, a[0], a[1], a[2], a[3], b0, b1);
+                    mma_f16(sum, r[0], r[1], r[2], r[3], b0, b1);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] += sum[e];
+                  } else {
+                    mma_f16(o, a[0], a[1], a[2], a[3], b0, b1);
+                  }
                 }
               }
             }
@@ -485,26 +532,17 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
     }
 
     // ---- the rows' own block (bf16), in groups of 16 keys
-    static_assert(kSmallRows <= kFoldRows, "the own block follows the last cached unit");
     if (p.sp.local && je == seg.units) {
-      uint32_t sees[2] = {0, 0};  // (at most 32 rows: one word)
-      if (TREE) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (live[r])
-            sees[r] = __ldg(p.vis + (seg.v.row0 + (pos.rt * kRows + 16 * mt + g + 8 * r) / p.sp.group) * p.words);
-      }
+#pragma unroll 1
       for (int key0 = 16 * kg; key0 < seg.v.rows; key0 += 16 * KG) {
-        float s[2][4];
+        float s[RT][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int y = 0; y < RT; ++y)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) s[y][i][0] = s[y][i][1] = s[y][i][2] = s[y][i][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < HD / 32; ++h) {
-          uint4 a[2], b[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            a[r] = live[r] ? ldg16(static_cast<const __nv_bfloat16*>(p.Q) + qoff[r] + 32 * h + 8 * t)
-                           : make_uint4(0, 0, 0, 0);
+          uint4 b[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int key = key0 + 8 * i + g;
@@ -512,29 +550,51 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
                        ? ldg16(static_cast<const __nv_bfloat16*>(p.K) +
                                ((seg.v.row0 + key) * c.Hkv + pos.h) * HD + 32 * h + 8 * t)
                        : make_uint4(0, 0, 0, 0);
-            mma_bf16(s[i], a[0].x, a[1].x, a[0].y, a[1].y, b[i].x, b[i].y);
-            mma_bf16(s[i], a[0].z, a[1].z, a[0].w, a[1].w, b[i].z, b[i].w);
+          }
+#pragma unroll
+          for (int y = 0; y < RT; ++y) {
+            uint4 a[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const __nv_bfloat16* src = query(y, r);
+              a[r] = src ? ldg16(src + 32 * h + 8 * t) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              mma_bf16(s[y][i], a[0].x, a[1].x, a[0].y, a[1].y, b[i].x, b[i].y);
+              mma_bf16(s[y][i], a[0].z, a[1].z, a[0].w, a[1].w, b[i].z, b[i].w);
+            }
           }
         }
+        uint32_t sees[RT][2];  // (TREE) the bits of these 16 keys
+        uint32_t pa[RT][4], pr[RT][4], pq[RT][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int y = 0; y < RT; ++y) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[i][e] = key0 + 8 * i + 2 * t + (e & 1) < seg.v.rows &&
-                              (!TREE || (sees[e >> 1] >> (key0 + 8 * i + 2 * t + (e & 1))) & 1)
-                          ? s[i][e] * p.sl2
-                          : -INFINITY;
-        const float one[1] = {kSmallUnshift};
-        softmax_step<HD, 2>(st, s, one);
-        uint32_t pa[4], pr[4], pq[4];
+          for (int r = 0; r < 2; ++r) {
+            const int tok = TREE ? token(y, r) : 0;
+            sees[y][r] = TREE && tok < seg.v.rows
+                             ? __ldg(p.vis + (seg.v.row0 + tok) * p.words + (key0 >> 5)) >> (key0 & 31)
+                             : 0;
+          }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = s[i >> 1][2 * (i & 1)], b = s[i >> 1][2 * (i & 1) + 1];
-          pa[i] = pack_bf16x2(a, b);
-          pr[i] = rest_bf16x2(pa[i], a, b);
-          if (FINE) pq[i] = rest_bf16x2(pr[i], a - bf_lo(pa[i]), b - bf_hi(pa[i]));
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = 8 * i + 2 * t + (e & 1);
+              s[y][i][e] = key0 + k < seg.v.rows && (!TREE || (sees[y][e >> 1] >> k) & 1) ? s[y][i][e] * p.sl2 : -INFINITY;
+            }
+          const float one[1] = {kSmallUnshift};
+          softmax_step<HD, 2>(st[y], s[y], one);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = s[y][i >> 1][2 * (i & 1)], b = s[y][i >> 1][2 * (i & 1) + 1];
+            pa[y][i] = pack_bf16x2(a, b);
+            pr[y][i] = rest_bf16x2(pa[y][i], a, b);
+            if (FINE) pq[y][i] = rest_bf16x2(pr[y][i], a - bf_lo(pa[y][i]), b - bf_hi(pa[y][i]));
+          }
         }
-        bool odd = false;  // (trees) a value that is not finite
+        bool odd = false;  // (TREE) a value that is not finite
 #pragma unroll
         for (int w = 0; w < HD / 64; ++w) {  // 8 columns of the thread's HD / 8 (16 bytes) at a time
           uint4 v[4];
@@ -554,37 +614,44 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
             for (int y = 0; y < 2; ++y) {
               const uint32_t sel = y ? 0x7632 : 0x5410;
               const uint32_t b0 = __byte_perm(x0[k], x1[k], sel), b1 = __byte_perm(y0[k], y1[k], sel);
-              // (the weights' rests may be 0 or negative: infinite values meet the first part alone)
-              // (TREE: rows that do not see them must not meet them either)
+              // (the weights' rests may be 0 or negative: infinite values meet the first part alone;
+              // TREE: rows that do not see them must not meet them either)
               const uint32_t c0 = finite2(b0), c1 = finite2(b1), d0 = TREE ? c0 : b0, d1 = TREE ? c1 : b1;
               if (TREE) odd |= c0 != b0 || c1 != b1;
-              float (&o)[4] = st.o[8 * w + 2 * k + y];
-              if (FINE) {
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_bf16(z, pa[0], pa[1], pa[2], pa[3], d0, d1);
-                mma_bf16(z, pr[0], pr[1], pr[2], pr[3], c0, c1);
-                mma_bf16(z, pq[0], pq[1], pq[2], pq[3], c0, c1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] += z[e];
-              } else {
-                mma_bf16(o, pa[0], pa[1], pa[2], pa[3], d0, d1);
-                mma_bf16(o, pr[0], pr[1], pr[2], pr[3], c0, c1);
+              for (int z = 0; z < RT; ++z) {
+                float (&o)[4] = st[z].o[8 * w + 2 * k + y];
+                if (FINE) {
+                  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_bf16(sum, pa[z][0], pa[z][1], pa[z][2], pa[z][3], d0, d1);
+                  mma_bf16(sum, pr[z][0], pr[z][1], pr[z][2], pr[z][3], c0, c1);
+                  mma_bf16(sum, pq[z][0], pq[z][1], pq[z][2], pq[z][3], c0, c1);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[e] += sum[e];
+                } else {
+                  mma_bf16(o, pa[z][0], pa[z][1], pa[z][2], pa[z][3], d0, d1);
+                  mma_bf16(o, pr[z][0], pr[z][1], pr[z][2], pr[z][3], c0, c1);
+                }
               }
             }
           }
         }
         if (TREE && __any_sync(0xffffffffu, odd)) {  // values that are not finite, to the rows that see them
 #pragma unroll 1
-          for (int key = key0; key < min(key0 + 16, seg.v.rows); ++key) {
-            const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(p.V) + ((seg.v.row0 + key) * c.Hkv + pos.h) * HD;
+          for (int k = 0; k < min(16, seg.v.rows - key0); ++k) {
+            const __nv_bfloat16* V =
+                static_cast<const __nv_bfloat16*>(p.V) + ((seg.v.row0 + key0 + k) * c.Hkv + pos.h) * HD;
 #pragma unroll
             for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float x = __bfloat162float(V[(HD / 8) * perm(2 * t + e) + j]);
                 if (isfinite(x)) continue;
-                if ((sees[0] >> key) & 1) st.o[j][e] += x;
-                if ((sees[1] >> key) & 1) st.o[j][2 + e] += x;
+#pragma unroll
+                for (int z = 0; z < RT; ++z) {
+                  if ((sees[z][0] >> k) & 1) st[z].o[j][e] += x;
+                  if ((sees[z][1] >> k) & 1) st[z].o[j][2 + e] += x;
+                }
               }
           }
         }
@@ -592,95 +659,97 @@ __global__ void __launch_bounds__(kThreads, kSmallCtasPerSm)
     }
 
     // ---- the warps' states through shared memory, a row tile's key groups joined
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float l = st.l[r];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (t == 0) {
-        red_ml[warp][g + 8 * r][0] = st.m[r];
-        red_ml[warp][g + 8 * r][1] = l;
-      }
-      // tile j, element e: column HD / 8 perm(2 t + e) + j
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float* o = &red_o[warp][g + 8 * r][(HD / 8) * perm(2 * t + e)];
-#pragma unroll
-        for (int j = 0; j < HD / 8; j += 4)
-          *reinterpret_cast<float4*>(o + j) =
-              make_float4(st.o[j][2 * r + e], st.o[j + 1][2 * r + e], st.o[j + 2][2 * r + e], st.o[j + 3][2 * r + e]);
-      }
-    }
-    compute_sync();
     const bool whole = jb == 0 && je == seg.units;
     float* part = p.part + (2 * (int64_t)cta + (jb == 0 ? 1 : 0)) * part_floats(kRows, HD);
-#pragma unroll 1
-    for (int item = threadIdx.x; item < kRows * 8; item += 32 * kWarps) {
-      const int row = item >> 3, c0 = (item & 7) * 4, w0 = (row >> 4) * KG, r = row & 15;
-      float M = -INFINITY, w[KG], L = 0.f;
 #pragma unroll
-      for (int x = 0; x < KG; ++x) M = fmaxf(M, red_ml[w0 + x][r][0]);
+    for (int y = 0; y < RT; ++y) {  // (the warps' tiles y of their row groups)
 #pragma unroll
-      for (int x = 0; x < KG; ++x) {
-        w[x] = M == -INFINITY ? 0.f : ex2_approx(red_ml[w0 + x][r][0] - M);
-        L = fmaf(w[x], red_ml[w0 + x][r][1], L);
+      for (int r = 0; r < 2; ++r) {
+        float l = st[y].l[r];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (t == 0) {
+          red_ml[warp][g + 8 * r][0] = st[y].m[r];
+          red_ml[warp][g + 8 * r][1] = l;
+        }
+        // tile j, element e: column HD / 8 perm(2 t + e) + j
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* o = &red_o[warp][g + 8 * r][(HD / 8) * perm(2 * t + e)];
+#pragma unroll
+          for (int j = 0; j < HD / 8; j += 4)
+            *reinterpret_cast<float4*>(o + j) = make_float4(st[y].o[j][2 * r + e], st[y].o[j + 1][2 * r + e],
+                                                            st[y].o[j + 2][2 * r + e], st[y].o[j + 3][2 * r + e]);
+        }
       }
-      const int fr = pos.rt * kRows + row, tok = fr / p.sp.group;
-      if (tok >= seg.v.rows) continue;
-      const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
-      const int64_t o0 = ((seg.v.row0 + tok) * p.Hq + head) * HD;
-      const float inv = whole ? (L != 0.f ? kSmallUnshift / L : 0.f) : kSmallUnshift;
+      compute_sync();
+#pragma unroll 1
+      for (int item = 32 * warp + lane; item < RG * 16 * 8; item += 32 * kWarps) {
+        const int r = (item >> 3) & 15, c0 = (item & 7) * 4, w0 = (item >> 7) * KG;
+        const int row = 16 * (RT * (item >> 7) + y) + r;  // of the CTA's rows
+        float M = -INFINITY, w[KG], L = 0.f;
 #pragma unroll
-      for (int k = 0; k < HD / 32; ++k) {
-        const int col = c0 + 32 * k;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < KG; ++x) M = fmaxf(M, red_ml[w0 + x][r][0]);
 #pragma unroll
         for (int x = 0; x < KG; ++x) {
-          const float4 b = *reinterpret_cast<const float4*>(&red_o[w0 + x][r][col]);
-          a.x = fmaf(w[x], b.x, a.x); a.y = fmaf(w[x], b.y, a.y);
-          a.z = fmaf(w[x], b.z, a.z); a.w = fmaf(w[x], b.w, a.w);
+          w[x] = M == -INFINITY ? 0.f : ex2_approx(red_ml[w0 + x][r][0] - M);
+          L = fmaf(w[x], red_ml[w0 + x][r][1], L);
         }
-        a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
-        if (!whole) reinterpret_cast<float4*>(part)[(col >> 2) * kRows + row] = a;
-        else if (p.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o0 + col) = a;
-        else
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + o0 + col) =
-              make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-      }
-      if ((item & 7) == 0) {
-        if (whole) p.LSE[(int64_t)head * p.r.T + seg.v.row0 + tok] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-        else {
-          part[kRows * HD + row] = M;
-          part[kRows * HD + kRows + row] = L;
+        const int fr = pos.rt * kRows + row, tok = fr / p.sp.group;
+        if (tok >= seg.v.rows) continue;
+        const int head = pos.h * p.sp.group + fr - tok * p.sp.group;
+        const int64_t o0 = ((seg.v.row0 + tok) * p.Hq + head) * HD;
+        const float inv = whole ? (L != 0.f ? kSmallUnshift / L : 0.f) : kSmallUnshift;
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k) {
+          const int col = c0 + 32 * k;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < KG; ++x) {
+            const float4 b = *reinterpret_cast<const float4*>(&red_o[w0 + x][r][col]);
+            a.x = fmaf(w[x], b.x, a.x); a.y = fmaf(w[x], b.y, a.y);
+            a.z = fmaf(w[x], b.z, a.z); a.w = fmaf(w[x], b.w, a.w);
+          }
+          a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
+          if (!whole) reinterpret_cast<float4*>(part)[(col >> 2) * kRows + row] = a;
+          else if (p.o_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + o0 + col) = a;
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + o0 + col) =
+                make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        }
+        if ((item & 7) == 0) {
+          if (whole)
+            p.LSE[(int64_t)head * p.r.T + seg.v.row0 + tok] = L != 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+          else {
+            part[kRows * HD + row] = M;
+            part[kRows * HD + kRows + row] = L;
+          }
         }
       }
+      compute_sync();
     }
-    compute_sync();
     if (u < u1) next_segment(c, p.r, p.sp, pos, seg, bad);
   }
 }
 
-template <int HD, int MT, bool FINE, bool TREE>
+template <int HD, int RT, int RG, bool FINE, bool TREE>
 cudaError_t launch(const CachedMaps& m, const CachedParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> raised{0};
-  const cudaError_t e = raise_smem(reinterpret_cast<const void*>(bdlm_cached_small_kernel<HD, MT, FINE, TREE>),
-                                   LayS<HD>::kAlloc, raised);
+  auto k = bdlm_cached_small_kernel<HD, RT, RG, FINE, TREE>;
+  if (Roles<RT>::kSplit) {
+    // the register split needs the block's full allotment: refuse to launch otherwise
+    static const cudaError_t ready = [&] {
+      cudaFuncAttributes fa;
+      const cudaError_t e = cudaFuncGetAttributes(&fa, k);
+      if (e != cudaSuccess) return e;
+      return fa.numRegs == Roles<RT>::kRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+    }();
+    if (ready != cudaSuccess) return ready;
+  }
+  const cudaError_t e = raise_smem(reinterpret_cast<const void*>(k), LayS<HD>::kAlloc, raised);
   if (e != cudaSuccess) return e;
-  bdlm_cached_small_kernel<HD, MT, FINE, TREE><<<p.G, kThreads, LayS<HD>::kAlloc, st>>>(m.k8, m.v8, p);
+  k<<<p.G, Roles<RT>::kThreads, LayS<HD>::kAlloc, st>>>(m.k8, m.v8, p);
   return cudaGetLastError();
-}
-template <int HD, bool FINE, bool TREE>
-cudaError_t launch_mt(const CachedMaps& m, const CachedParams& p, cudaStream_t st) {
-  return p.sp.tile_rows == 16 ? launch<HD, 1, FINE, TREE>(m, p, st) : launch<HD, 2, FINE, TREE>(m, p, st);
-}
-
-template <bool TREE>
-cudaError_t launch_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches) {
-  const cudaError_t e =
-      p.c.d == 128 ? (p.o_f32 ? launch_mt<128, true, TREE>(m, p, st) : launch_mt<128, false, TREE>(m, p, st))
-                   : (p.o_f32 ? launch_mt<64, true, TREE>(m, p, st) : launch_mt<64, false, TREE>(m, p, st));
-  if (e == cudaSuccess) ++*launches;
-  return e;
 }
 
 }  // namespace

@@ -84,17 +84,38 @@ __global__ void __launch_bounds__(kMaskThreads) bdlm_tree_mask_kernel(const Tree
 // token each; Z_k, and the token behind the path, pass over the vocabulary, which the
 // cluster's CTAs and their warps take in consecutive runs.
 //
-// Probabilities are summed as whole numbers of 2^-62 (exact from 2^-38 on, cut off
-// below): sums do not depend on their order, so results do not on the number of
-// CTAs, and the token is the first whose running sum passes u total to the bit.
-// Bound by HBM, and for few sequences by its chain of latencies.
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32;
+// Sums carry the rounding of every addition beside them, about twice fp32's
+// width: a running sum that is off by d picks another token for a share d of all random
+// numbers, for each token of the vocabulary, 1e-4 of all calls with fp32 sums.  Lanes'
+// sums join as whole numbers of 2^-62, whose order does not matter.  (Whole numbers from
+// the start: 98 us for the drawn trees below with the conversion instruction, 64 with
+// shifts, 39 this way; fp64 has two additions a clock and SM.)
+// Bound by a chain of latencies: row offsets, parents, the rows' p and q (2 thousand
+// cycles), the walk (2, and 0.4 for each accepted row), 5 for a pass and its join by
+// the cluster, 1 to find the token; and by HBM for its passes where sequences are many.
+// 64 trees of 16 rows drawn with up to 3 children, V = 131072 in fp32 (66 MB, more for
+// 2nd and 3rd passes): 39 us, the last sequences 3 passes; 16 trees of 64 chosen rows, V
+// = 100003 in bf16: 16 us; one chain of 8, V = 32000: 10 us.  CTAs of 512 / 256 / 128
+// threads: 48 / 39 / 41 us; up to 2 / 4 CTAs for each SM: 41 / 39.
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;
-constexpr double kOne = 4611686018427387904.0;  // 2^62
+constexpr double kOne = 4611686018427387904.0;  // 2^62: the whole numbers' unit
 
-// A probability in units of 2^-62 (outside [0, 1]: the nearer end; NaN: 0).
-__device__ __forceinline__ uint64_t fixed(float x) {
-  return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 4611686018427387904.f);
+// A number of fp32's width twice over: s + e.
+struct Wide {
+  float s, e;
+};
+// In units of 2^-62, what is below cut off.
+__device__ __forceinline__ uint64_t fixed(Wide x) {
+  constexpr float k = 4611686018427387904.f;
+  return (uint64_t)(__float2ll_rz(x.s * k) + __float2ll_rz(x.e * k));
+}
+// sum += x, both parts of every rounding kept.
+__device__ __forceinline__ void add(Wide& sum, Wide x) {
+  const float t = __fadd_rn(sum.s, x.s), b = __fsub_rn(t, sum.s);
+  const float r = __fadd_rn(__fsub_rn(x.s, b), __fsub_rn(sum.s, __fsub_rn(t, b)));
+  sum.e = __fadd_rn(sum.e, __fadd_rn(r, x.e));
+  sum.s = t;
 }
 
 template <typename T>
@@ -103,66 +124,69 @@ template <>
 struct Probs<float> {
   static constexpr int N = 4;  // values of 16 bytes
   static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
-  static __device__ __forceinline__ void vec(const float* p, float (&x)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  static __device__ __forceinline__ float value(const uint4& v, int i) {
+    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  }
+  static __device__ __forceinline__ void put(uint4& v, int i, float x) {
+    (i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w) = __float_as_uint(x);
   }
 };
 template <>
 struct Probs<__nv_bfloat16> {
   static constexpr int N = 8;
   static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  static __device__ __forceinline__ void vec(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  static __device__ __forceinline__ float value(const uint4& v, int i) {
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  static __device__ __forceinline__ void put(uint4& v, int i, float x) {
+    const uint32_t b = __float_as_uint(x) >> 16;  // (x is a bf16 value)
+    (i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w) |= i & 1 ? b << 16 : b;
   }
 };
 
-// One pass over max(p - c q, 0) of a vocabulary row.
+// What a pass adds up over a vocabulary row: p, or max(p - c q, 0) with c = 1 (the first
+// rejected child) or any c = ch + cl.
+enum PassKind { kPlain, kFirst, kAny };
 struct PassRow {
-  const void *p, *q;  // q null: p alone
-  uint64_t ci, cf;    // c = ci + cf 2^-64
-  int sh;             // elements between the 16-byte boundary below the row's start and its start
-  bool same;          // q has the same shift
-  int64_t V;
+  const void *p, *q;
+  float ch, cl;
+  int kind;
+  int sh;     // elements between the 16-byte boundary below the row's start and its start
+  int aside;  // q has another shift: its vectors are put together from single values
+  int V;
 };
 
-__device__ __forceinline__ uint64_t residual(uint64_t P, uint64_t Q, const PassRow& w) {
-  if (w.ci == 1 && w.cf == 0) return P > Q ? P - Q : 0;  // (the first rejected child)
-  if (__umul64hi(Q, w.ci) != 0) return 0;
-  const uint64_t x = Q * w.ci, y = x + __umul64hi(Q, w.cf);
-  return y >= x && P > y ? P - y : 0;
+// The 16 bytes of vector k (elements k N - sh on); outside the row: 0.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const void* row, int x0, int V, bool aside) {
+  constexpr int N = Probs<T>::N;
+  const T* p = static_cast<const T*>(row) + x0;
+  if (x0 >= 0 && x0 + N <= V && !aside) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint4 v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (x0 + i >= 0 && x0 + i < V) Probs<T>::put(v, i, Probs<T>::one(p + i));
+  return v;
 }
 
-// The N values of vector k (elements k N - sh on); outside the row: 0.
-template <typename T>
-__device__ __forceinline__ void load_vec(const PassRow& w, int64_t k, uint64_t (&r)[Probs<T>::N]) {
-  constexpr int N = Probs<T>::N;
-  const int64_t x0 = k * N - w.sh;
-  const T *p = static_cast<const T*>(w.p) + x0, *q = static_cast<const T*>(w.q) + x0;
-  float a[N], b[N];
-  const bool in = x0 >= 0 && x0 + N <= w.V;
-  if (in) {
-    Probs<T>::vec(p, a);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = x0 + i >= 0 && x0 + i < w.V ? Probs<T>::one(p + i) : 0.f;
+// Exact for c = 1 (the difference of two fp32 numbers and its rounding); any c: to about 2^-46 of p and c q.
+template <int KIND>
+__device__ __forceinline__ Wide residual(float p, float q, const PassRow& w) {
+  p = __saturatef(p);  // (NaN: 0)
+  if (KIND == kPlain) return Wide{p, 0.f};
+  q = __saturatef(q);
+  Wide r;
+  if (KIND == kFirst) {
+    r.s = __fsub_rn(p, q);
+    r.e = __fsub_rn(__fsub_rn(p, r.s), q);
+    return r.s > 0.f ? r : Wide{0.f, 0.f};
   }
-  if (w.q) {
-    if (in && w.same) {
-      Probs<T>::vec(q, b);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) b[i] = x0 + i >= 0 && x0 + i < w.V ? Probs<T>::one(q + i) : 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) r[i] = w.q ? residual(fixed(a[i]), fixed(b[i]), w) : fixed(a[i]);
+  const float h = __fmul_rn(w.ch, q), l = __fmaf_rn(w.cl, q, __fmaf_rn(w.ch, q, -h));  // c q = h + l
+  r.s = __fsub_rn(p, h);
+  const float b = __fsub_rn(r.s, p);
+  r.e = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(r.s, b)), __fadd_rn(h, b)), l);
+  return __fadd_rn(r.s, r.e) > 0.f ? r : Wide{0.f, 0.f};
 }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -171,10 +195,40 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
+// A warp's run of vectors [v0, v1) is cut into four quarters of whole 32-vector tiles.
+__device__ __forceinline__ int quarter(int v0, int v1, int i) {
+  return min(v1, v0 + ((v1 - v0 + 127) >> 7) * 32 * i);
+}
+
+// A lane's sums of the quarters: a tile of each at a time, all loads in flight.
+template <typename T, int KIND>
+__device__ __forceinline__ void sum_run(const PassRow& w, int v0, int v1, uint64_t (&sum)[4]) {
+  constexpr int N = Probs<T>::N;
+  const int lane = threadIdx.x & 31, len = ((v1 - v0 + 127) >> 7) * 32;
+  Wide x[4] = {};
+#pragma unroll 1
+  for (int k = lane; k < len; k += 32) {
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int at = v0 + u * len + k, x0 = at < v1 ? at * N - w.sh : w.V;
+      a[u] = load_vec<T>(w.p, x0, w.V, false);
+      if (KIND != kPlain) b[u] = load_vec<T>(w.q, x0, w.V, w.aside);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int y = 0; y < N; ++y)
+        add(x[u], residual<KIND>(Probs<T>::value(a[u], y), KIND == kPlain ? 0.f : Probs<T>::value(b[u], y), w));
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) sum[u] = fixed(x[u]);
+}
+
 // What the walk holds of a sequence's rows, and where it stands.
 struct TreeRows {
   int *par, *tok, *gone;  // gone: the rejected tokens of the current row (chosen drafts)
-  float *u, *p, *q;
+  float *u, *p, *q;       // (u negative: the row is accepted as a first child)
 };
 struct Walk {
   int cur, last, took, gone;
@@ -206,15 +260,23 @@ __device__ __forceinline__ void advance(Walk& w, const TreeRows& t, int rows, bo
       return;
     }
     const int x = t.tok[j];
-    const double p = t.p[j], q = t.q[j];
-    double left = drawn ? __dsub_rn(p, __dmul_rn(w.c, q)) : p, weight = drawn ? __dmul_rn((double)t.u[j], q) : (double)t.u[j];
-    if (left < 0.0) left = 0.0;
-    if (!drawn) {
-      bool was = false;
-      for (int k = lane; k < w.gone; k += 32) was |= t.gone[k] == x;
-      if (__any_sync(0xffffffffu, was)) left = 0.0;
+    const float u = t.u[j];
+    bool ok;
+    double left = t.p[j];
+    if (w.last < 0) {
+      ok = u < 0.f;
+    } else {
+      const double q = t.q[j], ua = fabsf(u);
+      if (drawn) {
+        left = __dsub_rn(left, __dmul_rn(w.c, q));
+      } else {
+        bool was = false;
+        for (int k = lane; k < w.gone; k += 32) was |= t.gone[k] == x;
+        if (__any_sync(0xffffffffu, was)) left = 0.0;
+      }
+      ok = __dmul_rn(drawn ? __dmul_rn(ua, q) : ua, w.z) < (left > 0.0 ? left : 0.0);
     }
-    if (__dmul_rn(weight, w.z) < left) {
+    if (ok) {
       if (lane == 0 && path) path[w.took] = j;
       ++w.took;
       w.cur = j;
@@ -238,7 +300,7 @@ __device__ __forceinline__ void advance(Walk& w, const TreeRows& t, int rows, bo
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) bdlm_tree_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, 3) bdlm_tree_verify_kernel(const VerifyParams p) {
   constexpr int N = Probs<T>::N;
   extern __shared__ int verify_smem[];
   __shared__ uint64_t s_cta[2][kVerifyCluster], s_warp[kVerifyWarps];
@@ -271,9 +333,12 @@ __global__ void __launch_bounds__(kVerifyThreads) bdlm_tree_verify_kernel(const 
     const float qq = par < 0 || !drawn ? 0.f : Probs<T>::one(static_cast<const T*>(p.draft) + row * p.draft_stride + x);
     t.par[i] = par < 0 ? -1 : par;
     t.tok[i] = x;
-    t.u[i] = fmaxf(u, 0.f);
-    t.p[i] = fminf(fmaxf(pp, 0.f), 1.f);
-    t.q[i] = fminf(fmaxf(qq, 0.f), 1.f);
+    const float pc = fminf(fmaxf(pp, 0.f), 1.f), qc = fminf(fmaxf(qq, 0.f), 1.f), uc = fmaxf(u, 0.f);
+    // the test against p itself, for all rows side by side (u q is exact in 64 bits); its answer is u's sign
+    const bool first = drawn ? (double)uc * (double)qc < (double)pc : uc < pc;
+    t.u[i] = first ? -fmaxf(uc, 1e-38f) : uc;
+    t.p[i] = pc;
+    t.q[i] = qc;
   }
   if (bad && rank == 0) atomicOr(p.status + kContentsWord, bad);
   __syncthreads();
@@ -298,37 +363,37 @@ __global__ void __launch_bounds__(kVerifyThreads) bdlm_tree_verify_kernel(const 
         const int64_t row = v.row0 + w.cur;
         s_want = w.want;
         s_gone = drawn || fallback ? 0 : w.gone;
+        const bool rest = drawn && w.c > 0.0 && !fallback;
         s_row.p = static_cast<const T*>(p.target) + row * p.target_stride;
-        s_row.q = drawn && w.c > 0.0 && !fallback ? static_cast<const T*>(p.draft) + row * p.draft_stride : nullptr;
-        const double ci = floor(w.c);
-        s_row.ci = (uint64_t)ci;
-        s_row.cf = __double2ull_rz((w.c - ci) * 18446744073709551616.0);
+        s_row.q = rest ? static_cast<const T*>(p.draft) + row * p.draft_stride : nullptr;
+        s_row.kind = !rest ? kPlain : w.c == 1.0 ? kFirst : kAny;
+        s_row.ch = (float)w.c;
+        s_row.cl = (float)(w.c - (double)s_row.ch);
         s_row.sh = (int)((reinterpret_cast<uintptr_t>(s_row.p) & 15) / sizeof(T));
-        s_row.same = s_row.sh == (int)((reinterpret_cast<uintptr_t>(s_row.q) & 15) / sizeof(T));
-        s_row.V = p.V;
+        s_row.aside = s_row.sh != (int)((reinterpret_cast<uintptr_t>(s_row.q) & 15) / sizeof(T));
+        s_row.V = (int)p.V;
       }
     }
     __syncthreads();
     const PassRow row = s_row;
     const int want = s_want, gone = s_gone;
     // this warp's run of vectors
-    const int64_t nv = (p.V + row.sh + N - 1) / N;
-    const int64_t c0 = nv * rank / C, c1 = nv * (rank + 1) / C;
-    const int64_t v0 = c0 + (c1 - c0) * warp / kVerifyWarps, v1 = c0 + (c1 - c0) * (warp + 1) / kVerifyWarps;
-    uint64_t sum = 0;
-#pragma unroll 4
-    for (int64_t k = v0 + lane; k < v1; k += 32) {
-      uint64_t r[N];
-      load_vec<T>(row, k, r);
-#pragma unroll
-      for (int i = 0; i < N; ++i) sum += r[i];
-    }
+    const int nv = (row.V + row.sh + N - 1) / N, per = (nv + C * kVerifyWarps - 1) / (C * kVerifyWarps);
+    const int v0 = min(nv, (rank * kVerifyWarps + warp) * per), v1 = min(nv, v0 + per);
+    uint64_t part[4];
+    if (row.kind == kPlain) sum_run<T, kPlain>(row, v0, v1, part);
+    else if (row.kind == kFirst) sum_run<T, kFirst>(row, v0, v1, part);
+    else sum_run<T, kAny>(row, v0, v1, part);
     // (rejected tokens are left out: each is in the list once)
     for (int i = lane; i < gone; i += 32) {
-      const int64_t k = (t.gone[i] + row.sh) / N;
-      if (k >= v0 && k < v1) sum -= fixed(Probs<T>::one(static_cast<const T*>(row.p) + t.gone[i]));
+      const int k = (t.gone[i] + row.sh) / N;
+      if (k < v0 || k >= v1) continue;
+      const uint64_t x = fixed(Wide{__saturatef(Probs<T>::one(static_cast<const T*>(row.p) + t.gone[i])), 0.f});
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (k >= quarter(v0, v1, y) && k < quarter(v0, v1, y + 1)) part[y] -= x;
     }
-    sum = warp_sum(sum);
+    const uint64_t sum = warp_sum(part[0] + part[1] + part[2] + part[3]);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
     uint64_t mine = 0;
@@ -356,40 +421,55 @@ __global__ void __launch_bounds__(kVerifyThreads) bdlm_tree_verify_kernel(const 
     for (int i = 0; i < warp; ++i) before += s_warp[i];
     if (goal >= before && goal - before < sum) {
       uint64_t run = before;
-      int found = -1;
-      for (int64_t k0 = v0; k0 < v1 && found < 0; k0 += 32) {
-        uint64_t r[N], part = 0;
+      int y = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = 0;
-        if (k0 + lane < v1) load_vec<T>(row, k0 + lane, r);
-        const int64_t x0 = (k0 + lane) * N - row.sh;
-        for (int g = 0; g < gone; ++g)
+      for (int i = 0; i < 3; ++i) {  // the quarter
+        const uint64_t z = warp_sum(part[i]);
+        if (y == i && goal - run >= z) run += z, y = i + 1;
+      }
+      const int e = quarter(v0, v1, y + 1);
+      // the token, a tile after the other (its sums may differ from the run's in the last unit: then the last token
+      // that has any)
+      int token = -1, last = -1;
+#pragma unroll 1
+      for (int k0 = quarter(v0, v1, y); k0 < e && token < 0; k0 += 32) {
+        const int x0 = k0 + lane < e ? (k0 + lane) * N - row.sh : row.V;
+        const uint4 a = load_vec<T>(row.p, x0, row.V, false);
+        const uint4 b = row.kind == kPlain ? make_uint4(0, 0, 0, 0) : load_vec<T>(row.q, x0, row.V, row.aside);
+        uint64_t r[N], mine = 0;
 #pragma unroll
-          for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+          const float pv = Probs<T>::value(a, i), qv = Probs<T>::value(b, i);
+          r[i] = fixed(row.kind == kPlain   ? residual<kPlain>(pv, qv, row)
+                       : row.kind == kFirst ? residual<kFirst>(pv, qv, row)
+                                            : residual<kAny>(pv, qv, row));
+          for (int g = 0; g < gone; ++g)
             if (x0 + i == t.gone[g]) r[i] = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) part += r[i];
-        uint64_t upto = part;
+          mine += r[i];
+          if (r[i] != 0) last = x0 + i;
+        }
+        uint64_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
+          const uint64_t z = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += z;
         }
         const unsigned hit = __ballot_sync(0xffffffffu, run + upto > goal);
         if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            uint64_t at = run + upto - part;
+          uint64_t at = run + upto - mine;
+          int x = -1;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              at += r[i];
-              if (found < 0 && at > goal) found = (int)(x0 + i);
-            }
-            p.next_token[s] = found;
+          for (int i = 0; i < N; ++i) {
+            at += r[i];
+            if (x < 0 && at > goal) x = x0 + i;
           }
-          break;
+          token = __shfl_sync(0xffffffffu, x, __ffs(hit) - 1);
+        } else {
+          run += __shfl_sync(0xffffffffu, upto, 31);
         }
-        run += __shfl_sync(0xffffffffu, upto, 31);
       }
+      if (token < 0) token = __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0) p.next_token[s] = token;
     }
     if (rank == 0 && tid == 0) {
       p.accepted[s] = w.took;
@@ -416,7 +496,7 @@ static cudaError_t launch_verify(const VerifyParams& p, int sms, cudaStream_t st
   const cudaError_t e = raise_smem(reinterpret_cast<const void*>(k), 24 * kMaxTreeRows, raised);
   if (e != cudaSuccess) return e;
   int C = 1;
-  while (C < kVerifyCluster && p.n_seqs * C < 4 * sms) C *= 2;
+  while (C < kVerifyCluster && p.n_seqs * C * 2 <= 4 * sms) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C, (unsigned)p.n_seqs);
   cfg.blockDim = dim3(kVerifyThreads);

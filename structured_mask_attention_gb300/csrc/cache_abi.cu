@@ -150,9 +150,10 @@ size_t kept_space(int n_seqs, int Hkv, int64_t keep) { return (size_t)n_seqs * H
 bdlm_status append_call(const void* K, const void* V, const bdlm_cache* cache, const int32_t* path, int64_t max_path,
                         const int32_t* accepted, const int32_t* row_offsets, int64_t rows, int64_t max_rows,
                         int32_t* lens_out, void* workspace, size_t ws_bytes, bdlm_stream stream) {
-  AppendParams p;
-  CACHE_CHECK(check_cache(cache, &p.c));
-  CACHE_CHECK(check_rows(p.c, row_offsets, rows, max_rows, &p.r));
+  CacheDesc c;
+  RowsDesc r;
+  CACHE_CHECK(check_cache(cache, &c));
+  CACHE_CHECK(check_rows(c, row_offsets, rows, max_rows, &r));
   const int64_t ns = 4 * (int64_t)cache->n_seqs;
   if (path && (max_path <= 0 || max_path > (int64_t)1 << 24))
     return abi_fail(BDLM_ERR_SHAPE, "max_path=%lld must be in [1, 2^24]", (long long)max_path);
@@ -168,17 +169,13 @@ bdlm_status append_call(const void* K, const void* V, const bdlm_cache* cache, c
   CACHE_CHECK(check_space(workspace, ws_bytes, kHeader));
   int sms;
   CACHE_CHECK(abi_device(&sms));
-  p.K = K;
-  p.V = V;
-  p.path = path;
-  p.accepted = accepted;
-  p.max_path = (int)max_path;
-  p.lens_out = lens_out;
-  p.status = static_cast<uint32_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int launches = 0;
   void* tm = abi_timer_begin(path ? ABI_T_COMMIT : ABI_T_APPEND, st);
-  cudaError_t e = launch_cache_append(p, st, &launches);
+  uint32_t* status = static_cast<uint32_t*>(workspace);
+  cudaError_t e = path ? launch_cache_commit(CommitParams{c, r, K, V, path, accepted, (int)max_path, lens_out, status}, st,
+                                             &launches)
+                       : launch_cache_append(AppendParams{c, r, K, V, lens_out, status}, st, &launches);
   abi_timer_end(tm);
   return abi_finish(e, launches, path ? "cache commit launch" : "cache append launch");
 }

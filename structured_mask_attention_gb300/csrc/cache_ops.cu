@@ -57,10 +57,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, __half2 r) {
 // the measured copy rate; 16 sequences' blocks of 512 (43 MB) 14.3 us, half of it
 // before the first bytes arrive; 64 single tokens 7 us, a launch.  (A CTA per
 // block, one chunk per thread at a time: 203 us for the first.)
-// PATH (commit): the new tokens are the rows path[s, 0 .. accepted[s]) of the
-// sequence instead of all of them in order.
 constexpr int kAppendThreads = 256;
-template <int HD, int TT, bool PATH>
+template <int HD, int TT>
 __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_kernel(const AppendParams p) {
   constexpr int CH = HD / 16;                     // 16-value chunks of a token
   constexpr int kThreads = kAppendThreads * TT / 64;
@@ -74,11 +72,6 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
   const SeqView v = seq_view(c, p.r, s, bad);
   const int64_t cap = (int64_t)c.max_pages << c.lp;
   int rows = v.rows;
-  if (PATH) {
-    rows = p.accepted[s];
-    if (rows < 0 || rows > p.max_path) bad |= kStatusBadTree;
-    if (bad) rows = 0;
-  }
   if (v.len + (int64_t)rows > cap) {
     bad |= kStatusBadLen;
     rows = (int)(cap - v.len);
@@ -91,23 +84,6 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
     bad = 0;
   }
   if (rows <= 0 || first >= rows) return;  // (without new rows a half-filled page, maybe another sequence's too, stays as it is)
-  uint4 x[NT][2];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kThreads + tid;
-    int tok = first + k / CH;
-    bool ok = tok >= 0 && tok < rows;
-    if (PATH && ok) {
-      tok = __ldg(p.path + (int64_t)s * p.max_path + tok);
-      ok = tok >= 0 && tok < v.rows;  // (a row that is not the sequence's: zeros)
-      if (!ok) atomicOr(p.status + kContentsWord, kStatusBadTree);
-    }
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv ? p.V : p.K) +
-                                                      ((v.row0 + (ok ? tok : 0)) * c.Hkv + h) * HD) + 2 * (k % CH);
-    x[i][0] = ok ? __ldg(src) : make_uint4(0, 0, 0, 0);
-    x[i][1] = ok ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
-  }
-  // (behind the loads: a page's id and its scale are two more round trips)
   if (tid < TT / 16) {
     const int f = first + (tid << c.lp);  // new token of the block's first slot
     int id = -1;
@@ -118,6 +94,16 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
     s_was[1][tid] = id >= 0 && f < 0 ? c.vs[b] : 0.f;
     s_amax[0][tid] = s_amax[1][tid] = 0;
     if (bad) atomicOr(p.status + kContentsWord, bad);
+  }
+  uint4 x[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int kv = i >= NT / 2, k = (i % (NT / 2)) * kThreads + tid, tok = first + k / CH;
+    const bool ok = tok >= 0 && tok < rows;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv ? p.V : p.K) +
+                                                      ((v.row0 + (ok ? tok : 0)) * c.Hkv + h) * HD) + 2 * (k % CH);
+    x[i][0] = ok ? __ldg(src) : make_uint4(0, 0, 0, 0);
+    x[i][1] = ok ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
 #pragma unroll
@@ -175,6 +161,168 @@ __global__ void __launch_bounds__(kAppendThreads* TT / 64) bdlm_cache_append_ker
       const uint2 lo = quantise8(*reinterpret_cast<const float(*)[8]>(f), sc, inv, pow2);
       const uint2 hi = quantise8(*reinterpret_cast<const float(*)[8]>(f + 8), sc, inv, pow2);
       *code = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ commit
+// The append of the accepted rows of drafted trees: new token i of sequence s is row
+// path[s, i] of it.  A call has few tokens for each of many sequences, so what counts is
+// how many CTAs are under way and how little each does: it takes TT slots of one
+// (sequence, KV head) as the append does, but its warps share out the slots that take in
+// new tokens alone, 32 / (HD / 16) of them and K or V at a time, and hold four such
+// pieces; where there are more they read the rest again.  Four round trips follow each
+// other: lengths and offsets, path and pages, the rows, and (beside them) the scales.
+// 256 sequences' chains of up to 128 accepted rows, 8 heads of 128 (84 MB): 25.6 us, 3.3
+// TB/s (the append's kernel with rows looked up, all slots of a tile: 45; 256 threads
+// and more instructions to a piece: 36; 10 CTAs per SM instead of 8: 32; heads one
+// after the other in a CTA: 58).  32 sequences' trees of 16: 6.2 us, a launch.
+constexpr int kCommitThreads = 128, kCommitPieces = 4;
+template <int HD, int TT>
+__global__ void __launch_bounds__(kCommitThreads, 8) bdlm_cache_commit_kernel(const CommitParams p) {
+  constexpr int CH = HD / 16, WT = 32 / CH, kTeam = kCommitThreads / 64;  // warps of K's and of V's pieces
+  __shared__ uint32_t s_amax[2][TT / 16];
+  __shared__ float s_was[2][TT / 16], s_scale[2][TT / 16], s_inv[2][TT / 16];  // s_inv: 0 where it is not exact
+  __shared__ int64_t s_code[TT / 16];                                          // the blocks' codes, -1: no page
+  const CacheDesc& c = p.c;
+  const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t bad = 0;
+  int rows = __ldg(p.accepted + s);
+  const SeqView v = seq_view(c, p.r, s, bad);
+  if (rows < 0 || rows > p.max_path) bad |= kStatusBadTree;
+  if (bad) rows = 0;
+  const int64_t cap = (int64_t)c.max_pages << c.lp;
+  if (v.len + (int64_t)rows > cap) {
+    bad |= kStatusBadLen;
+    rows = (int)(cap - v.len);
+  }
+  const int base = (v.len & ~(TT - 1)) + (int)blockIdx.x * TT;  // first position
+  const int first = base - v.len;                               // as a new token (negative: old tokens)
+  if (blockIdx.x == 0 && h == 0 && tid == 0) {
+    if (p.lens_out) p.lens_out[s] = v.len + rows;
+    if (bad) atomicOr(p.status + kContentsWord, bad);
+  }
+  if (rows <= 0 || first >= rows) return;
+  bad = 0;
+  // block `tid` of the tile: its page, asked for now and looked at behind the rows' loads
+  const int f = first + (tid << c.lp);  // new token of the block's first slot
+  const bool mine = tid < (TT >> c.lp) && f < rows && f + c.page > 0;
+  int id = mine ? __ldg(c.table + (int64_t)s * c.max_pages + (base >> c.lp) + tid) : -1;
+  // a warp's pieces: WT slots of K or of V, from slot s0 on
+  const int kv = warp & 1, s0 = (first < 0 ? -first & ~(WT - 1) : 0) + lane / CH, s1 = min(TT, rows - first);
+  const int stride = c.Hkv * HD * 2;  // bytes between tokens
+  const char* src = static_cast<const char*>(kv ? p.V : p.K) + ((v.row0 * c.Hkv + h) * HD + 16 * (lane % CH)) * 2;
+  const int32_t* path = p.path + (int64_t)s * p.max_path + first;
+  auto slot = [&](int n, int i) { return s0 + ((n * kCommitPieces + i) * kTeam + (warp >> 1)) * WT; };
+  auto idle = [&](int t) { return t - lane / CH >= s1; };  // (the piece lies behind the last new token)
+  auto isnew = [&](int t) { return t < s1 && first + t >= 0; };
+  uint4 x[kCommitPieces][2];
+  auto load = [&](int n) {
+    int from[kCommitPieces];
+#pragma unroll
+    for (int i = 0; i < kCommitPieces; ++i) from[i] = isnew(slot(n, i)) ? __ldg(path + slot(n, i)) : -1;
+#pragma unroll
+    for (int i = 0; i < kCommitPieces; ++i) {
+      const bool ok = (unsigned)from[i] < (unsigned)v.rows;
+      if (!ok && isnew(slot(n, i))) bad |= kStatusBadTree;  // (a row that is not the sequence's: zeros)
+      const uint4* at = reinterpret_cast<const uint4*>(src + (int64_t)(ok ? from[i] : 0) * stride);
+      x[i][0] = ok ? __ldg(at) : make_uint4(0, 0, 0, 0);
+      x[i][1] = ok ? __ldg(at + 1) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  const int batches = (s1 - (s0 - lane / CH) + WT * kTeam * kCommitPieces - 1) / (WT * kTeam * kCommitPieces);
+  load(batches - 1);
+  if (tid < TT / 16) {
+    if (id < 0 || id >= c.n_pages) {
+      if (mine) bad |= kStatusBadPage;
+      id = -1;
+    }
+    const int64_t b = (int64_t)max(id, 0) * c.Hkv + h;
+    s_code[tid] = id >= 0 ? b * c.page * HD : -1;
+    s_was[0][tid] = id >= 0 && f < 0 ? c.ks[b] : 0.f;
+    s_was[1][tid] = id >= 0 && f < 0 ? c.vs[b] : 0.f;
+    s_amax[0][tid] = s_amax[1][tid] = 0;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int n = batches - 1;; --n) {  // (the first batch comes last and stays)
+#pragma unroll
+    for (int i = 0; i < kCommitPieces; ++i) {
+      if (idle(slot(n, i))) continue;
+      // bf16 magnitudes compare like integers
+      uint32_t m = 0;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i][y].x & 0x7fff7fffu, x[i][y].y & 0x7fff7fffu),
+                                 __vmaxu2(x[i][y].z & 0x7fff7fffu, x[i][y].w & 0x7fff7fffu)));
+      m = umax2(m & 0xffffu, m >> 16);
+      // a piece's slots belong to one block
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) atomicMax(&s_amax[kv][slot(n, i) >> c.lp], m << 16);
+    }
+    if (n == 0) break;
+    load(n - 1);
+  }
+  __syncthreads();
+  // a block's scale: it never shrinks while the block holds tokens, NaN stays
+  if (tid < TT / 16) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const float was = s_was[y][tid];
+      float sc = block_scale(s_amax[y][tid]);
+      if (f < 0) sc = (was != was || sc != sc) ? __uint_as_float(0x7fc00000u) : fmaxf(was, sc);
+      s_scale[y][tid] = sc;
+      s_inv[y][tid] = is_pow2(sc) ? __uint_as_float(0x7f000000u - __float_as_uint(sc)) : 0.f;
+      if (id >= 0) (y ? c.vs : c.ks)[(int64_t)id * c.Hkv + h] = sc;
+    }
+  }
+  __syncthreads();
+  uint8_t* codes = (kv ? c.v8 : c.k8) + 16 * (lane % CH);
+#pragma unroll 1
+  for (int n = 0; n < batches; ++n) {
+    if (n > 0) load(n);
+#pragma unroll
+    for (int i = 0; i < kCommitPieces; ++i) {
+      const int t = slot(n, i), j = t >> c.lp;
+      if (!isnew(t) || s_code[j] < 0) continue;
+      const float sc = s_scale[kv][j], inv = s_inv[kv][j];
+      uint2 o[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t w[4] = {x[i][y].x, x[i][y].y, x[i][y].z, x[i][y].w};
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[2 * e] = __uint_as_float(w[e] << 16);
+          z[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+        o[y] = quantise8(z, sc, inv, inv != 0.f);
+      }
+      *reinterpret_cast<uint4*>(codes + s_code[j] + (t & (c.page - 1)) * HD) = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
+    }
+  }
+  if (bad) atomicOr(p.status + kContentsWord, bad);
+  // old codes of the block that takes in new tokens behind them, where its scale grew
+  const int j = first < 0 ? -first >> c.lp : 0, old = first < 0 ? -first - (j << c.lp) : 0;
+  if (old == 0 || s_code[j] < 0) return;
+#pragma unroll 1
+  for (int y = 0; y < 2; ++y) {
+    const float was = s_was[y][j], sc = s_scale[y][j], inv = s_inv[y][j];
+    if (sc == was) continue;  // (false for NaN as well)
+    uint4* code = reinterpret_cast<uint4*>((y ? c.v8 : c.k8) + s_code[j]);
+#pragma unroll 1
+    for (int k = tid; k < old * CH; k += kCommitThreads) {
+      const uint4 u = code[k];
+      float z[16];
+      e4m3x4_to_float(u.x, z);
+      e4m3x4_to_float(u.y, z + 4);
+      e4m3x4_to_float(u.z, z + 8);
+      e4m3x4_to_float(u.w, z + 12);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i] *= was;
+      const uint2 lo = quantise8(*reinterpret_cast<const float(*)[8]>(z), sc, inv, inv != 0.f);
+      const uint2 hi = quantise8(*reinterpret_cast<const float(*)[8]>(z + 8), sc, inv, inv != 0.f);
+      code[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
   }
 }
@@ -554,18 +702,23 @@ cudaError_t raise_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
   return e;
 }
 
-template <bool PATH>
-static auto append_kernel(int d, int TT) {
-  return d == 128 ? (TT == 128 ? bdlm_cache_append_kernel<128, 128, PATH> : bdlm_cache_append_kernel<128, 64, PATH>)
-                  : (TT == 128 ? bdlm_cache_append_kernel<64, 128, PATH> : bdlm_cache_append_kernel<64, 64, PATH>);
-}
-
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* launches) {
   const int TT = p.c.page > 64 ? 128 : 64;
-  // groups of TT slots that max_rows (commit: max_path) new tokens can touch
-  const dim3 grid((unsigned)(((p.path ? p.max_path : p.r.max_rows) + TT - 2) / TT + 1), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
-  auto k = p.path ? append_kernel<true>(p.c.d, TT) : append_kernel<false>(p.c.d, TT);
+  // groups of TT slots that max_rows new tokens can touch
+  const dim3 grid((unsigned)((p.r.max_rows + TT - 2) / TT + 1), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
+  auto k = p.c.d == 128 ? (TT == 128 ? bdlm_cache_append_kernel<128, 128> : bdlm_cache_append_kernel<128, 64>)
+                        : (TT == 128 ? bdlm_cache_append_kernel<64, 128> : bdlm_cache_append_kernel<64, 64>);
   k<<<grid, kAppendThreads * TT / 64, 0, st>>>(p);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t st, int* launches) {
+  const int TT = p.c.page > 64 ? 128 : 64;
+  const dim3 grid((unsigned)((p.max_path + TT - 2) / TT + 1), (unsigned)p.c.Hkv, (unsigned)p.c.n_seqs);
+  auto k = p.c.d == 128 ? (TT == 128 ? bdlm_cache_commit_kernel<128, 128> : bdlm_cache_commit_kernel<128, 64>)
+                        : (TT == 128 ? bdlm_cache_commit_kernel<64, 128> : bdlm_cache_commit_kernel<64, 64>);
+  k<<<grid, kCommitThreads, 0, st>>>(p);
   ++*launches;
   return cudaGetLastError();
 }

@@ -13,13 +13,22 @@ struct AppendParams {
   CacheDesc c;
   RowsDesc r;
   const void *K, *V;  // bf16 [T, Hkv, d]
-  const int32_t* path;      // commit: [n_seqs, max_path] rows of their sequences, the first accepted[s] of them; else null
-  const int32_t* accepted;  // [n_seqs]
-  int max_path;
   int32_t* lens_out;
   uint32_t* status;
 };
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t st, int* launches);
+
+struct CommitParams {
+  CacheDesc c;
+  RowsDesc r;
+  const void *K, *V;        // bf16 [T, Hkv, d]
+  const int32_t* path;      // [n_seqs, max_path]: rows of their sequences
+  const int32_t* accepted;  // [n_seqs]: how many of them
+  int max_path;
+  int32_t* lens_out;
+  uint32_t* status;
+};
+cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t st, int* launches);
 
 struct WeightsParams {
   CacheDesc c;

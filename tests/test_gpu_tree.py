@@ -200,6 +200,71 @@ def test_attn_long_prefix_spans_many_parts(lib):
         run_tree(lib, [5000, 1], trees_of([rows, 2], 3), 4, 1, 64, 128, seed=9)
 
 
+@pytest.mark.parametrize("rows", [[53, 20, 52, 0, 3], [64, 64, 64, 52, 7], [110, 60, 103, 52, 20]])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+def test_attn_several_row_tiles(lib, rows, d, o_dtype):
+    """5 heads to a KV head: one to three tiles of 256 rows, the last ones part empty."""
+    run_tree(lib, [4200, 0, 130, 77, 600], trees_of(rows, 3), 5, 1, d, 32, o_dtype=o_dtype, seed=rows[0])
+
+
+@pytest.mark.parametrize("rows", [1, 12, 20, 70])
+@pytest.mark.parametrize("size", [2.0 ** 16, 2.0 ** 22, 2.0 ** 26])
+def test_attn_scores_beyond_fp32s_fractions(lib, rows, size):
+    """Scores of 2^20 and more: a row's LSE is its largest score, its output inside its values' range."""
+    m = lib
+    c, cache = small_cache(m, [700], seed=23)
+    Q, K, V = (make_rows(rows, H, 64, 1 + i) for i, H in enumerate((2, 1, 1)))
+    Q = (Q * np.float32(size)).astype(np.float32)
+    sees = to.ancestors(make_tree(rows, 2, 1))
+    ref = to.attn(c, Q, K, V, [sees], offsets_of([rows]), 0.125)
+    for o_dtype in (torch.bfloat16, torch.float32):
+        O, LSE = m.bdlm_attn_tree(*(to_dev(x, torch) for x in (Q, K, V)), DEV(to.words(sees, -(-rows // 32))), cache,
+                                  o_dtype=o_dtype)
+        assert torch.isfinite(O).all() and torch.isfinite(LSE).all()
+        assert (np.abs(LSE.double().cpu().numpy() - ref[1])
+                <= (64 + 8) * 2.0 ** -24 * ref[3] + 2.0 ** -21 + 2.0 ** -22 * np.abs(ref[1])).all()
+        v = np.concatenate([co.tokens(c, "v", 0, 0), V[:, 0]])
+        assert (O.double().cpu().numpy() <= v.max(0) * (1 + 2.0 ** -8) + 1e-3).all()
+        assert (O.double().cpu().numpy() >= v.min(0) * (1 + 2.0 ** -8) - 1e-3).all()
+
+
+@pytest.mark.parametrize("rows", [1, 12, 40, 200])
+def test_attn_of_a_pool_past_32_bit_offsets(lib, rows):
+    """Pages whose codes lie past 2^31 bytes (a pool of 2.4 GB for each of K and V, as good as empty)."""
+    m = lib
+    d, Hkv, page, n_pages = 128, 2, 128, 74000
+    cc, _ = make_cache([300, 140], 384, Hkv, d, page, seed=4)
+    far = np.asarray([[73999, 70001, 0], [65600, 1, 73111]], np.int32)  # the same pages, elsewhere
+    c8 = {w: torch.zeros((n_pages, Hkv, page, d), dtype=torch.uint8, device="cuda") for w in "kv"}
+    sc = {w: torch.ones((n_pages, Hkv), device="cuda") for w in "kv"}
+    for s in range(2):
+        for j in range(3):
+            for w in "kv":
+                c8[w][int(far[s, j])] = DEV(cc[w + "8"][cc["table"][s, j]])
+                sc[w][int(far[s, j])] = DEV(cc[w + "s"][cc["table"][s, j]])
+    cache = m.BdlmCache(c8["k"].view(torch.float8_e4m3fn), c8["v"].view(torch.float8_e4m3fn), sc["k"], sc["v"], DEV(far),
+                        DEV(cc["lens"]))
+    sees = trees_of([rows, rows], 2)
+    Q, K, V = (make_rows(2 * rows, H, d, 1 + i) for i, H in enumerate((4, Hkv, Hkv)))
+    vis = DEV(np.concatenate([to.words(x, -(-rows // 32)) for x in sees]))
+    O, LSE = m.bdlm_attn_tree(*(to_dev(x, torch) for x in (Q, K, V)), vis, cache)
+    off = offsets_of([rows, rows])
+    check_attn(O, LSE, to.attn(cc, Q, K, V, sees, off, 1 / math.sqrt(d)), d, True)
+    path = np.tile(np.arange(rows, dtype=np.int32), (2, 1))
+    acc = np.asarray([rows, 1], np.int32)
+    want = to.commit(cc, K, V, path, np.minimum(acc, [84, 84]) if rows > 84 else acc, off)
+    ws = m.bdlm_cache_workspace(cache)
+    got = m.bdlm_cache_commit(cache, to_dev(K, torch), to_dev(V, torch), DEV(path), DEV(acc), workspace=ws)
+    if rows <= 84:  # (room for 84 more tokens)
+        m.bdlm_sync_status(ws)
+        assert got.tolist() == want.tolist()
+        for s in range(2):
+            for j in range(3):
+                for w in "kv":
+                    assert (c8[w][int(far[s, j])].cpu().numpy() == cc[w + "8"][cc["table"][s, j]]).all()
+
+
 def test_attn_many_sequences(lib):
     run_tree(lib, [(37 * i) % 200 for i in range(70)], trees_of([1 + i % 4 for i in range(70)], 2), 4, 2, 64, 16, seed=11)
 

@@ -5,8 +5,8 @@
 // One token of a sequence, or a short block, gives Hq / Hkv rows per token and
 // KV head, a handful against thousands of keys: the stream of codes bounds the
 // call, and a tcgen05 tile of 128 rows would be mostly padding.  A CTA of four
-// warps takes 16 or 32 rows (MT 16-row tiles); its warps are MT row tiles by
-// 4 / MT groups of keys.  A fifth warp keeps a ring of K and V tiles of 128 keys
+// warps takes 16 or 32 rows (RT 16-row tiles to a warp, RG groups of them); its warps
+// are RG row groups by 4 / RG groups of keys.  A fifth warp keeps a ring of K and V tiles of 128 keys
 // filled by TMA, codes as they lie, so that 128 KB per SM (two CTAs) are in flight
 // whatever the warps do; they turn codes into fp16 on the way from shared
 // memory to the MMA.

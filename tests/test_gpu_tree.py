@@ -200,6 +200,34 @@ def test_attn_long_prefix_spans_many_parts(lib):
         run_tree(lib, [5000, 1], trees_of([rows, 2], 3), 4, 1, 64, 128, seed=9)
 
 
+@pytest.mark.parametrize("rows", [[12, 9, 16], [16, 0, 13]])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("spoiled", [False, True])
+def test_attn_32_rows_over_long_caches(lib, rows, d, o_dtype, spoiled):
+    """17 to 32 rows and room for 65536 tokens (lengths up to 1500): both row tiles in each warp."""
+    m = lib
+    c, _ = make_cache([1500, 70, 0], 1500, 16, d, 128, seed=d)
+    cap = np.zeros((3, 512), np.int32)
+    cap[:, : c["table"].shape[1]] = c["table"]
+    c["table"] = cap
+    off, T = offsets_of(rows), sum(rows)
+    Q, K, V = (make_rows(T, H, d, 2 + i) for i, H in enumerate((32, 16, 16)))
+    sees = trees_of(rows, 3)
+    if spoiled:  # the last row is seen by none but itself: its neighbours' results do not know of it
+        for x in sees:
+            if len(x):
+                x[:, -1] = False
+    ref = to.attn(c, Q, K, V, sees, off, 1 / math.sqrt(d))
+    if spoiled:
+        last = [int(off[s + 1]) - 1 for s, r in enumerate(rows) if r]
+        K[last], V[last] = math.nan, math.inf
+    vis = np.concatenate([to.words(x, 1) for x in sees])
+    cache = device_cache(m, torch, c)
+    O, LSE = m.bdlm_attn_tree(*(to_dev(x, torch) for x in (Q, K, V)), DEV(vis), cache, DEV(off), max(rows), o_dtype=o_dtype)
+    check_attn(O, LSE, ref, d, o_dtype == torch.bfloat16)
+
+
 @pytest.mark.parametrize("rows", [[53, 20, 52, 0, 3], [64, 64, 64, 52, 7], [110, 60, 103, 52, 20]])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])

@@ -115,7 +115,7 @@ bdlm_status check_space(void* ws, size_t bytes, size_t need) {
 }
 
 size_t attn_space(int64_t flat, int d) {
-  const int tile = cached_tile_rows(flat);
+  const int tile = cached_tile_rows(flat);  // (a tree's may be 128 where this is 256: less)
   return (size_t)cached_ctas(tile, kSmsMax) * (2 * part_floats(tile, d) + fine_floats(tile, d)) * sizeof(float);
 }
 
@@ -232,7 +232,7 @@ bdlm_status attn_call(const void* Qn, const void* Kn, const void* Vn, const int3
   p.status = static_cast<uint32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kHeader);
   p.limit_ns = abi_wait_limit_ns();
-  p.sp.tile_rows = cached_tile_rows(flat);
+  p.sp.tile_rows = visible ? tree_tile_rows(flat) : cached_tile_rows(flat);
   const bool small = p.sp.tile_rows <= kSmallRows;
   p.sp.extra = !small ? kTcExtra : Kn ? kSmallExtraOwn : kSmallExtra;
   p.sp.keyed = 0;

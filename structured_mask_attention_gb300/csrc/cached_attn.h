@@ -63,6 +63,12 @@ constexpr float kSmallUnshift = 1.0f / (1 << (int)kSmallShift), kTcUnshift = 1.0
 inline int cached_tile_rows(int64_t flat) {
   return flat <= 16 ? 16 : flat <= kSmallRows ? 32 : flat <= 128 ? 128 : 256;
 }
+// Trees: 257 to 384 rows go in three tiles of 128; of pairs' two tiles the second would be at
+// most half full (8 sequences of 16384, 5 heads to a KV head, 260 / 320 / 380 rows: 249 / 253 /
+// 258 us in three tiles, 278 / 281 / 286 in two of 256; one of 131072, 300 rows: 220 / 267; 16 of
+// 500: 70 / 73.  160 to 250 rows in tiles of 128: 174 to 181, in one of 256 165 to 169; 450 rows
+// 342 / 297).
+inline int tree_tile_rows(int64_t flat) { return flat > 256 && flat <= 384 ? 128 : cached_tile_rows(flat); }
 inline int64_t fine_floats(int tile_rows, int d) { return tile_rows > kSmallRows ? (int64_t)2 * 128 * d : 0; }
 inline int cached_ctas(int tile_rows, int sms) { return tile_rows <= kSmallRows ? sms * kSmallCtasPerSm : sms; }
 

@@ -53,6 +53,11 @@
 // (instructions that no CTA has run yet), 2 for each of 33 units, and 10 to 16 for
 // the end of a segment and the beginning of the next (1 to 2 of them): 102 to 156 in
 // all, 132 in the mean, 69 us.
+// Trees (in a graph, warm; 16 / 8 heads but for the second): 32 rows behind each of 16
+// sequences of 8192 at most 86 us, 64 behind each of 8 of 32768, 40 / 8 heads, 284 (three
+// tiles of 128), 256 behind one of 131072 274 us, 1.0 PFLOP/s.  By the issuing thread's clock a
+// unit of 128 keys and 128 rows (split) takes it 1400 cycles for 16 products and their
+// commits, 200 for its waits and 700 in which the softmax is not through.
 // Registers: ptxas reports 60 to 176 bytes of spills in the bf16 instances and 208
 // to 420 in the fp32 ones.
 #pragma once
@@ -666,8 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t kt = desc_lo(base + LY::kK + ks * kSlot, 16), q = desc_lo(base + LY::kQ, 16);
                 constexpr uint32_t HV = desc_hi(2, 1024), HQ = desc_hi(SWQ, SBO8);
                 constexpr int n8 = HD / 32;
-                if (!(mbar_wait(BAR(B_WF + vs), (wc >> 1) & 1, wd, 33) && mbar_wait(BAR(B_KF + ks), kph, wd, 30) &&
-                      mbar_wait(BAR(B_PF + t), bit(pph, t), wd, 31)))
+                if (!mbar_wait3(BAR(B_WF + vs), (wc >> 1) & 1, BAR(B_KF + ks), kph, BAR(B_PF + t), bit(pph, t), wd, 33, 30, 31))
                   return false;
                 tc_fence_after();
 #pragma unroll
@@ -719,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t acc = j > 0, vt = desc_lo(base + LY::kW + (wc & 1) * LY::kWBytes, kSlot);
                 const uint32_t kt = desc_lo(base + LY::kK + ks * kSlot, 16), q = desc_lo(base + LY::kQ, 16);
                 constexpr uint32_t HV = desc_hi(2, 1024), HQ = desc_hi(SWQ, SBO8);
-                ok = mbar_wait(BAR(B_WF + (wc & 1)), (wc >> 1) & 1, wd, 33) && mbar_wait(BAR(B_KF + ks), kph, wd, 30) &&
-                     mbar_wait(BAR(B_PF + 0), pph & 1, wd, 31);
+                ok = mbar_wait3(BAR(B_WF + (wc & 1)), (wc >> 1) & 1, BAR(B_KF + ks), kph, BAR(B_PF + 0), pph & 1, wd, 33, 30,
+                                31);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll

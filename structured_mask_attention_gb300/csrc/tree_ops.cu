@@ -228,7 +228,7 @@ __device__ __forceinline__ void sum_run(const PassRow& w, int v0, int v1, uint64
 // What the walk holds of a sequence's rows, and where it stands.
 struct TreeRows {
   int *par, *tok, *gone;  // gone: the rejected tokens of the current row (chosen drafts)
-  float *u, *p, *q;       // (u negative: the row is accepted as a first child)
+  float *u, *p, *q;       // (u with a sign, -0 too: the row is accepted as a first child)
 };
 struct Walk {
   int cur, last, took, gone;
@@ -255,7 +255,7 @@ __device__ __forceinline__ void advance(Walk& w, const TreeRows& t, int rows, bo
     if (w.took >= max_path) return;
     const int j = next_child(t.par, rows, w.cur, w.last);
     if (j < 0) return;
-    if (w.z < 0.0) {  // (drawn) a child was rejected, and another one is left
+    if (drawn && w.z < 0.0) {  // a child was rejected, and another one is left
       w.want = 1;
       return;
     }
@@ -264,7 +264,7 @@ __device__ __forceinline__ void advance(Walk& w, const TreeRows& t, int rows, bo
     bool ok;
     double left = t.p[j];
     if (w.last < 0) {
-      ok = u < 0.f;
+      ok = __float_as_int(u) < 0;
     } else {
       const double q = t.q[j], ua = fabsf(u);
       if (drawn) {
@@ -333,10 +333,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) bdlm_tree_verify_kernel(con
     const float qq = par < 0 || !drawn ? 0.f : Probs<T>::one(static_cast<const T*>(p.draft) + row * p.draft_stride + x);
     t.par[i] = par < 0 ? -1 : par;
     t.tok[i] = x;
-    const float pc = fminf(fmaxf(pp, 0.f), 1.f), qc = fminf(fmaxf(qq, 0.f), 1.f), uc = fmaxf(u, 0.f);
+    const float pc = fminf(fmaxf(pp, 0.f), 1.f), qc = fminf(fmaxf(qq, 0.f), 1.f), uc = fabsf(fmaxf(u, 0.f));
     // the test against p itself, for all rows side by side (u q is exact in 64 bits); its answer is u's sign
     const bool first = drawn ? (double)uc * (double)qc < (double)pc : uc < pc;
-    t.u[i] = first ? -fmaxf(uc, 1e-38f) : uc;
+    t.u[i] = first ? -uc : uc;
     t.p[i] = pc;
     t.q[i] = qc;
   }

@@ -450,6 +450,18 @@ def test_verify_the_same_token_twice(lib):
             run_verify(lib, [9] * 20, 8, 6, drawn, seed=seed, spoil=spoil)
 
 
+@pytest.mark.parametrize("total", [0.9, 1.1, 1.6])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_verify_rows_that_do_not_sum_to_one(lib, total, drawn):
+    """Chosen drafts may then use up more than 1: what is left falls below 0, and the next one is accepted."""
+    def spoil(parents, tokens, target, draft, us, s):
+        target *= np.float32(total)
+        us[:] = 0.5 + us / 2
+        tokens[:] = np.arange(len(tokens)) % 4
+    for seed in range(5):
+        run_verify(lib, [14] * 16, 6, 4, drawn, seed=seed, spoil=spoil, spread=0.3)
+
+
 def test_verify_values_outside_their_range(lib):
     """NaN and below 0: 0; above 1: 1."""
     def spoil(parents, tokens, target, draft, us, s):

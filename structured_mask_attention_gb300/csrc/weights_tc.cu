@@ -4,7 +4,7 @@
 //   W[j] += sum over rows i of exp(s_ij - LSE_i)
 // needs the sum of each *key* over all rows, so the scores are computed
 // transposed: K's tile of 128 keys is the first operand (its e4m3 codes as TMA
-// left them), the rows' queries the second (two 8-bit parts, cached_tc.cu), and
+// left them), the rows' queries the second (two 8-bit parts, cached_tc.cuh), and
 // S^T has a key per TMEM lane.  A thread then owns a key: its block's scale is
 // a constant, the rows' factors and LSEs are read from shared memory by all
 // threads together, the sum stays in two registers, and no two threads ever

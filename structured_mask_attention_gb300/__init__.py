@@ -875,12 +875,14 @@ def bdlm_verify_workspace(n_seqs: int, max_rows: int, V: int, device="cuda"):
     return _torch().zeros(n, dtype=_torch().uint8, device=device)
 
 
-def _check_probs(name, t, dtype, T, device):
-    if t.dim() != 2 or t.shape[0] != T or t.dtype is not dtype or t.device != device or not t.is_cuda or \
-            (t.shape[1] > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must be [{T}, V] {dtype} on {device} (a CUDA device) with rows that lie apart and values "
-                         f"side by side, not {t.dtype} {list(t.shape)} of strides {list(t.stride())} on {t.device}")
-    return t.stride(0) if T > 1 else t.shape[1]
+def _check_probs(name, t, dtype, shape, device):
+    """The row stride of a [rows, V] tensor whose rows lie apart, each side by side."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_cuda:
+        row, one = t.stride()
+        if (one == 1 or shape[1] == 1) and (row >= shape[1] or shape[0] < 2):
+            return row if shape[0] > 1 else shape[1]
+    raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on {device} (a CUDA device) with rows that lie "
+                     f"apart and values side by side, not {t.dtype} {list(t.shape)} of strides {list(t.stride())} on {t.device}")
 
 
 def bdlm_tree_verify(parents, tokens, target, draft, uniforms, sample, row_offsets=None, max_rows: int | None = None,
@@ -899,15 +901,15 @@ def bdlm_tree_verify(parents, tokens, target, draft, uniforms, sample, row_offse
     that the tokens follow the target's distribution).  ``row_offsets``, ``max_rows``,
     ``workspace`` (from ``bdlm_verify_workspace``) and ``stream`` as in the calls on a cache."""
     torch = _torch()
-    T, n, device = parents.shape[0], sample.shape[0], target.device
-    if target.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"target must be float32 or bfloat16, not {target.dtype}")
-    strides = [_check_probs("target", target, target.dtype, T, device)]
-    V = target.shape[1]
+    T, n, device, dtype = parents.shape[0], sample.shape[0], target.device, target.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise ValueError(f"target must be float32 or bfloat16, not {dtype}")
+    if target.dim() != 2:
+        raise ValueError(f"target must be [rows, V], not {list(target.shape)}")
+    shape = (T, target.shape[1])
+    row_t = row_d = _check_probs("target", target, dtype, shape, device)
     if draft is not None:
-        strides.append(_check_probs("draft", draft, target.dtype, T, device))
-        if draft.shape != target.shape:
-            raise ValueError(f"draft is {list(draft.shape)}, target {list(target.shape)}")
+        row_d = _check_probs("draft", draft, dtype, shape, device)
     _check_tensor("parents", parents, torch.int32, (T,), device)
     _check_tensor("tokens", tokens, torch.int32, (T,), device)
     _check_tensor("uniforms", uniforms, torch.float32, (T,), device)
@@ -930,7 +932,7 @@ def bdlm_tree_verify(parents, tokens, target, draft, uniforms, sample, row_offse
     ws = _cache_workspace(like, workspace, made, 256)
     _cache_call(load_library().bdlm_tree_verify, like, stream,
                 (parents.data_ptr(), tokens.data_ptr(), target.data_ptr(), None if draft is None else draft.data_ptr(),
-                 F32 if target.dtype is torch.float32 else BF16, V, strides[0], strides[-1], uniforms.data_ptr(),
+                 F32 if dtype is torch.float32 else BF16, shape[1], row_t, row_d, uniforms.data_ptr(),
                  sample.data_ptr(), n, off, T, max_rows, path.data_ptr(), path.shape[1], accepted.data_ptr(),
                  token.data_ptr(), ws.data_ptr(), ws.nbytes), made)
     return path, accepted, token

@@ -693,6 +693,80 @@ def test_calls_on_another_stream(lib):
     assert all(torch.equal(i, j) for i, j in zip((*want, *a), (*got, *b)))
 
 
+def test_a_padded_batch_is_the_ragged_one(lib):
+    """Trees of equal size, the rest of each filled with rows without a parent and any tokens, keys and values: the same
+    paths, tokens, outputs and cache as packed trees with offsets."""
+    m = lib
+    rows, R, V, d = [5, 9, 1, 12], 12, 60, 64
+    trees = [make_tree(n, 2, 3 + i) for i, n in enumerate(rows)]
+    parents, tokens, target, draft, u, s = make_drafts(trees, V, 4)
+    off = offsets_of(rows)
+    at = np.concatenate([np.arange(R * i, R * i + n) for i, n in enumerate(rows)])
+    rng = np.random.default_rng(1)
+
+    def pad(x, fill):
+        y = np.empty((4 * R,) + x.shape[1:], x.dtype)
+        y[:] = fill
+        y[at] = x
+        return y
+    P = dict(parents=pad(parents, -1), tokens=pad(tokens, 3), target=pad(target, np.nan), draft=pad(draft, np.nan),
+             u=pad(u, 0.0))
+    got = m.bdlm_tree_verify(*(DEV(P[k]) for k in ("parents", "tokens", "target", "draft", "u")), DEV(s))
+    want = m.bdlm_tree_verify(DEV(parents), DEV(tokens), DEV(target), DEV(draft), DEV(u), DEV(s), DEV(off), R)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    Q, K, Vv = (make_rows(sum(rows), H, d, 1 + i) for i, H in enumerate((4, 2, 2)))
+    make = lambda: device_cache(m, torch, make_cache([50, 0, 17, 33], 80, 2, d, 16, seed=2)[0])
+    a, b = make(), make()
+    va, vb = m.bdlm_tree_mask(a, DEV(P["parents"])), m.bdlm_tree_mask(b, DEV(parents), DEV(off), R)
+    assert torch.equal(va[0][DEV(at)], vb[0]) and torch.equal(va[1][DEV(at)], vb[1])
+    wide = [to_dev(pad(x, np.float32(np.inf)), torch) for x in (Q, K, Vv)]
+    Oa, La = m.bdlm_attn_tree(*wide, va[0], a, scale=0.1)
+    Ob, Lb = m.bdlm_attn_tree(*(to_dev(x, torch) for x in (Q, K, Vv)), vb[0], b, DEV(off), R, scale=0.1)
+    assert torch.equal(Oa[DEV(at)], Ob) and torch.equal(La[:, DEV(at)], Lb)
+    la = m.bdlm_cache_commit(a, wide[1], wide[2], got[0], got[1])
+    lb = m.bdlm_cache_commit(b, *(to_dev(x, torch) for x in (K, Vv)), want[0], want[1], DEV(off), R)
+    assert torch.equal(la, lb) and torch.equal(a.k8.view(torch.uint8), b.k8.view(torch.uint8))
+
+
+def test_calls_side_by_side(lib):
+    """Two streams, a workspace for each, the same inputs: all calls at once, many times."""
+    m = lib
+    rows = [12, 7, 3, 20]
+    x, _ = step_inputs(4, rows)
+    make = lambda: device_cache(m, torch, make_cache([200, 0, 150, 77], 240, 2, 64, 16, seed=1)[0])  # (256 places)
+    a, b, c = make(), make(), make()
+    wa, wb, wc = (m.bdlm_cache_workspace(y, 4, 20) for y in (a, b, c))
+    va, vb, vc = (m.bdlm_verify_workspace(4, 20, 211) for _ in range(3))
+    for _ in range(10):  # (a commit may round the old codes of its first block to a larger scale: once)
+        want = verify_step(m, c, x, wc, vc)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(sa):
+            ya = verify_step(m, a, x, wa, va)
+        with torch.cuda.stream(sb):
+            yb = verify_step(m, b, x, wb, vb)
+    torch.cuda.synchronize()
+    for k in ("path", "acc", "tok", "lens", "O"):
+        assert torch.equal(ya[k], want[k]) and torch.equal(yb[k], want[k]), k
+    for w in (wa, wb, va, vb):
+        m.bdlm_sync_status(w)
+
+
+def test_verify_repeats_bitwise_in_any_company(lib):
+    """A sequence's result does not depend on how many others there are (other clusters, other runs of the
+    vocabulary)."""
+    m = lib
+    trees = [make_tree(16, 3, 1)]
+    parents, tokens, target, draft, u, s = make_drafts(trees, 5003, 2)
+    one = m.bdlm_tree_verify(DEV(parents), DEV(tokens), DEV(target), DEV(draft), DEV(u), DEV(s))
+    for n in (2, 90, 200, 700):
+        t = lambda x: DEV(np.concatenate([x] * n))
+        many = m.bdlm_tree_verify(t(parents), t(tokens), t(target), t(draft), t(u), t(s))
+        for a, b in zip(one, many):
+            assert (b == a).all()
+
+
 def test_no_rows_at_all(lib):
     m = lib
     c, cache = small_cache(m, [20, 3], capacity=32)

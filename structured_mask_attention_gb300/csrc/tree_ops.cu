@@ -3,6 +3,8 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <utility>
+
 #include "kernels.h"
 #include "tree_ops.h"
 
@@ -307,6 +309,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) bdlm_tree_verify_kernel(con
   __shared__ PassRow s_row;
   __shared__ int s_want, s_gone;
   cg::cluster_group cl = cg::this_cluster();
+  auto begun = cl.barrier_arrive();  // (waited for before the first write into another CTA's shared memory)
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank(), s = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t bad = 0;
@@ -341,6 +344,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 3) bdlm_tree_verify_kernel(con
     t.q[i] = qc;
   }
   if (bad && rank == 0) atomicOr(p.status + kContentsWord, bad);
+  cl.barrier_wait(std::move(begun));
   __syncthreads();
   if (v.rows == 0) {  // (all CTAs of the cluster alike)
     if (rank == 0) {

@@ -33,16 +33,16 @@ struct CachedParams {
 // side by side), then the rows' reference maxima (log2 units) and sums.
 __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (int64_t)tile_rows * (d + 2); }
 
-// Rows up to which the mma.sync kernel takes a call.  16 sequences of up to 16384
+// Rows up to which the mma.sync kernels take a call.  16 sequences of up to 16384
 // tokens with 20 / 32 rows: 108 / 108 us here, 128 / 127 in the tcgen05 kernel (in a
 // graph, warm); 64 rows (16 sequences of up to 8192): 118 us with tiles of 64 rows
-// here, when it was tried, 83 there.
+// here, when it was tried, 83 there (trees in two tiles of 32 of tree_small.cu 92).
 constexpr int kSmallRows = 32;
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
 // Weights are kept in fp16, 2^shift larger than exp2(s - reference): the largest
-// come near 2^16, its end, and its range lies below them.  The mma.sync kernel has
+// come near 2^16, its end, and its range lies below them.  cached_small.cu has
 // the exact running maximum for a reference: a weight keeps 11 bits down to 2^-29
-// of the row's largest and counts down to 2^-40.  The tcgen05 kernels' reference
+// of the row's largest and counts down to 2^-40 (tree_small.cu: one bit less).  The tcgen05 kernels' reference
 // may lie kRescale behind the maximum (and a tenth of a bit for rounding): 11
 // bits down to 2^-23 of the reference, something down to 2^-34.  Such weights make up O
 // where one key dominates a row and has a small value, an attention sink.  The

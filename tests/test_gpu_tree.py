@@ -302,14 +302,53 @@ def test_attn_equal_trees_without_offsets(lib):
 
 
 def test_attn_of_all_bits_is_cached_attention(lib):
-    """Bit for bit: the same kernels, nothing hidden."""
+    """Above 32 rows times heads of a group bit for bit: the same kernels, nothing hidden.  Up to 32 (4 rows here) the
+    kernels are two, each off from the formula by check_attn's bound at most."""
     m = lib
     for rows in (4, 30, 64, 200):
         c, cache = small_cache(m, [700, 60], page=32, Hkv=2, d=128)
         Q, K, V = (to_dev(make_rows(2 * rows, H, 128, i + 1), torch) for i, H in enumerate((4, 2, 2)))
         vis = torch.full((2 * rows, -(-rows // 32)), -1, dtype=torch.int32, device="cuda")
         a, b = m.bdlm_attn_tree(Q, K, V, vis, cache), m.bdlm_attn_cached(Q, K, V, cache)
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        if 2 * rows > 32:
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            continue
+        ref = to.attn(c, *(make_rows(2 * rows, H, 128, i + 1) for i, H in enumerate((4, 2, 2))),
+                      [np.ones((rows, rows), bool)] * 2, offsets_of([rows] * 2), 1 / math.sqrt(128))
+        for x in (a, b):
+            check_attn(x[0], x[1], ref, 128, True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [1, 8, 9, 16, 17, 24, 25, 32])
+def test_attn_every_count_of_row_tiles(lib, rows, o_dtype, d):
+    """Of 8 rows each, full and one over; caches split between CTAs and whole ones."""
+    for lens in ([1500, 130], [900, 33]):
+        run_tree(lib, lens, trees_of([rows, max(rows - 3, 1)], 3), 1, 1, d, 32, o_dtype=o_dtype, seed=rows)
+
+
+@pytest.mark.parametrize("rows", [3, 13, 23, 31])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_scores_that_climb(lib, rows, d):
+    """Keys whose scores rise from tile to tile by less, about and more than a reference's step, and one row's by
+    hundreds: references move often, and for one row of a warp's alone."""
+    m = lib
+    lens = [1400]
+    c, _ = make_cache(lens, 1400, 1, d, 16, 7)
+    Q, K, V = (make_rows(rows, 1, d, i + 1) for i in range(3))
+    Q = Q / 8 + 1.0
+    Q[rows // 2] *= 16
+    Q = torch.from_numpy(Q.astype(np.float32)).to(torch.bfloat16).float().numpy()
+    for b in range(-(-1400 // 16)):
+        c["ks"][c["table"][0, b]] = 2.0 ** -12 * (1 + b / 4)
+    sees = trees_of([rows], 2)
+    off = offsets_of([rows])
+    ref = to.attn(c, Q, K, V, sees, off, 1 / math.sqrt(d))
+    cache = device_cache(m, torch, c)
+    out = m.bdlm_attn_tree(*(to_dev(x, torch) for x in (Q, K, V)), DEV(np.concatenate([to.words(x, 1) for x in sees])),
+                           cache, max_rows=rows)
+    check_attn(out[0], out[1], ref, d, True)
 
 
 @pytest.mark.parametrize("rows", [1, 40, 150])

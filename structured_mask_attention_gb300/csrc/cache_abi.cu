@@ -234,7 +234,7 @@ bdlm_status attn_call(const void* Qn, const void* Kn, const void* Vn, const int3
   p.limit_ns = abi_wait_limit_ns();
   p.sp.tile_rows = visible ? tree_tile_rows(flat) : cached_tile_rows(flat);
   const bool small = p.sp.tile_rows <= kSmallRows;
-  p.sp.extra = !small ? kTcExtra : Kn ? kSmallExtraOwn : kSmallExtra;
+  p.sp.extra = !small ? kTcExtra : visible ? kTreeExtra : Kn ? kSmallExtraOwn : kSmallExtra;
   p.sp.keyed = 0;
   p.whole = 0;
   p.G = cached_ctas(p.sp.tile_rows, std::min(sms, kSmsMax));

@@ -92,7 +92,10 @@ constexpr int kWholeKeys = 1024;
 // kernels spend 10 to 20 thousand cycles to end a segment and begin the next, and
 // 2000 (split) or 4000 (pairs) on a unit: with 0 / 6, when it was tried, blocks of 32 and 128 took 130 / 106 and 293 /
 // 248 us; 4 to 12 are level.
-constexpr int kSmallExtra = 3, kSmallExtraOwn = 5, kTcExtra = 6;
+// tree_small.cu spends some 20 thousand cycles on a segment with own rows and 3000 on a unit: with 3 / 5 / 7 / 9 /
+// 12, chains of 5 over 32 sequences of up to 32768 tokens took 249 / 236 / 223 / 222 / 222 us, of 8192 107 / 90 / 82 / 82 /
+// 82, with d = 64, 4096 tokens 36 / 35 / 36 / 37 / 39, with fp32 outputs, 32768 tokens, 342 / 329 / 328 / 331 / 335.
+constexpr int kSmallExtra = 3, kSmallExtraOwn = 5, kTreeExtra = 7, kTcExtra = 6;
 
 cudaError_t launch_cached_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);
 cudaError_t launch_tree_small(const CachedMaps& m, const CachedParams& p, cudaStream_t st, int* launches);

@@ -16,16 +16,16 @@
 // warpgroup of its own (three of its warps leave) and hands its registers over.
 //
 // In a graph, warm, 32 sequences, 32 / 8 heads of 128: chains of 5 (24 columns) behind at most
-// 2048 / 8192 / 32768 tokens 43 / 88 / 233 us, where tiles of 16 rows, one to each of two warps,
+// 2048 / 8192 / 32768 tokens 43 / 82 / 223 us, where tiles of 16 rows, one to each of two warps,
 // took 50 / 114 / 363 and both to each warp 53 / 108 / 299; chains of 8 behind 32768 285 (both
 // tiles to each warp: 311); one token 198 (cached_small.cu's tiles: 202); fp32 outputs, chains of
 // 5, 329 (470); d = 64, chains of 5 behind 16384, 86 (both: 115).
-// What bounds chains of 5, 1.30 GB at 5.5 TB/s or 82 % of the measured copy rate: HBM beside the
-// instructions' latencies, which two computing warps per scheduler see; with all codes from L2
-// it is 204 us.  Tried: the next tile's scores beside this one's weights, 259 against 249 without
-// (293 with the loop written out twice: instructions no longer fit); three slots of K and V,
-// those 249 against 234 (they take the first-level cache); 24 / 40 / 64 registers for the
-// loader instead of 56, 245 / 236 / 237.
+// What bounds chains of 5, 1.28 GB at 5.7 TB/s or 85 % of the measured copy rate: HBM beside the
+// instructions' latencies, which two computing warps per scheduler see.  Tried where segments
+// were split less evenly (234 us; with all codes from L2 204): the next tile's scores beside
+// this one's weights and three slots of K and V, 259; the three slots alone 249 (they take the
+// first-level cache); the loop written out twice 293 (instructions no longer fit); 24 / 40 / 64
+// registers for the loader instead of 56, 245 / 236 / 237.
 #include "cached_small.cuh"
 
 namespace bdlm {

@@ -110,7 +110,7 @@ struct Lay {
   static constexpr int kW = kV + 2 * kSlot;       // fp16 V, 2 slots of HD / 64 panels
   static constexpr int kWBytes = kSlot * (HD / 64);
   static constexpr int kBar = kW + 2 * kWBytes;
-  static constexpr int kKI = kBar + ((8 * B_COUNT + 12 + 15) & ~15);
+  static constexpr int kKI = kBar + ((8 * B_COUNT + 16 + 15) & ~15);
   static constexpr int kML = kKI + NI * (int)sizeof(KInfo);
   static constexpr int kCQ = kML + 2 * 128 * 8;
   static constexpr int kPC = kCQ + 256 * 4;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the rows' score factors
   float* row_cq = reinterpret_cast<float*>(bp + LY::kCQ);
   Piece* pieces = reinterpret_cast<Piece*>(bp + LY::kPC);
-  // (TREE, split) the piece's own tile holds values that are not finite
+  // (TREE, split) an own tile that sub-tile t took in this piece holds values that are not finite, [2]
   volatile int* own_odd = reinterpret_cast<volatile int*>(bp + LY::kBar + 8 * B_COUNT + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -1005,14 +1005,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
         }
         ml[t * 128 + row] = make_float2(m_ref, l);
-        // (the own tile, the last one, is of one sub-tile)
-        if (TREE && nl > 0 && t == ((n - 1) & 1) && row == 0) *own_odd = odd;
+        // (own tiles alternate between the sub-tiles too: with one or two heads to a KV head a piece has up to three)
+        if (TREE && row == 0) own_odd[t] = odd;
         mbar_arrive(BAR(B_ML));
         ok = mbar_wait(BAR(B_ML), mlc & 1, wd, 46);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++mlc;
-        if (TREE) odd = nl > 0 && *own_odd != 0;
+        if (TREE) odd = (own_odd[0] | own_odd[1]) != 0;
         const float2 x0 = ml[row], x1 = ml[128 + row];
         M = fmaxf(x0.x, x1.x);
         const float b = M == -INFINITY ? 0.f : M;

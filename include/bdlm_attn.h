@@ -506,7 +506,10 @@ bdlm_status bdlm_tree_mask(const int32_t* parents, const bdlm_cache* cache, cons
  * A row that sees no key gets O = 0, LSE = -inf.  Keys and values that a row does not
  * see may hold anything, NaN and infinities too; where a value that it sees is not
  * finite, its output is not.  Everything else, bounds on O and LSE among it, as in
- * bdlm_attn_cached; the outputs must not overlap visible either. */
+ * bdlm_attn_cached, but that for more than 32 rows times heads of a group own values whose
+ * rows' sizes in a tile of 128 differ by more than 2^5 count as codes of up to 2^15 with a scale
+ * that the smallest of them decide (2^-48 to 2^100; for a row of zeros 2^-8 at most), larger
+ * ones taking part in fp32.  The outputs must not overlap visible either. */
 bdlm_status bdlm_attn_tree(const void* Qn, const void* Kn, const void* Vn, const int32_t* visible, int64_t words,
                            const bdlm_cache* cache, const int32_t* row_offsets, int64_t rows, int64_t max_rows, int Hq,
                            float scale, void* O, bdlm_dtype o_dtype, float* LSE, void* workspace, size_t ws_bytes,

@@ -54,8 +54,8 @@
 // the end of a segment and the beginning of the next (1 to 2 of them): 102 to 156 in
 // all, 132 in the mean, 69 us.
 // Trees (in a graph, warm; 16 / 8 heads but for the second): 32 rows behind each of 16
-// sequences of 8192 at most 86 us, 64 behind each of 8 of 32768, 40 / 8 heads, 284 (three
-// tiles of 128), 256 behind one of 131072 274 us, 1.0 PFLOP/s.  By the issuing thread's clock a
+// sequences of 8192 at most 80 us, 64 behind each of 8 of 32768, 40 / 8 heads, 270 (three
+// tiles of 128), 256 behind one of 131072 278 us, 1.0 PFLOP/s.  By the issuing thread's clock a
 // unit of 128 keys and 128 rows (split) takes it 1400 cycles for 16 products and their
 // commits, 200 for its waits and 700 in which the softmax is not through.
 // Registers: ptxas reports 60 to 176 bytes of spills in the bf16 instances and 208
@@ -98,10 +98,12 @@ enum { B_QF = 0, B_KF = 2, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + 2, 
 struct alignas(16) KInfo {
   float s[2][4], lv[2][4], iv[2][4];
   int fine;  // scales differ inside 32 keys, or some keys' page is missing
-  int gone;  // bit x: the page of keys 16 x .. 16 x + 15 is missing
+  int gone;  // bit x: the page of keys 16 x .. 16 x + 15 is missing (own tiles: values that the products do not take)
 };
 
-template <int HD>
+constexpr int kLimits = 4;  // (split) own tiles of a piece, at most: 384 rows
+
+template <int HD, bool TREE>
 struct Lay {
   static constexpr int kQ = 0;                    // two regions of 128 rows x HD bf16 (or its two 8-bit parts)
   static constexpr int kQBytes = 128 * HD * 2;
@@ -114,11 +116,12 @@ struct Lay {
   static constexpr int kML = kKI + NI * (int)sizeof(KInfo);
   static constexpr int kCQ = kML + 2 * 128 * 8;
   static constexpr int kPC = kCQ + 256 * 4;
-  static constexpr int kBytes = kPC + 4 * 64;
+  static constexpr int kLim = kPC + 4 * 64;       // (TREE) limits of the pieces' own tiles
+  static constexpr int kBytes = kLim + (TREE ? 4 * kLimits * 4 : 0);
   // 1024 bytes to align; at least 120 KB so that no second CTA shares the SM (each holds all of TMEM)
   static constexpr int kAlloc = kBytes + 1024 > 120 * 1024 ? kBytes + 1024 : 120 * 1024;
 };
-static_assert(Lay<128>::kAlloc <= 232448, "shared memory");
+static_assert(Lay<128, true>::kAlloc <= 232448, "shared memory");
 
 // One CTA's share of a segment, as the roles read it from a ring in shared
 // memory (warp 3 fills it, so that no other role carries the walk over the
@@ -190,6 +193,9 @@ __device__ __noinline__ void put_rows_call(const CachedParams& p, const Piece* p
   put_rows<HD, TEAM, E4M3>(p, pp, tid, first, dst, factor);
 }
 
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
 // 2^x of a whole x in fp32's normal range.
 __device__ __forceinline__ float exp2_int(float x) { return __uint_as_float((uint32_t)((int)x + 127) << 23); }
 
@@ -199,40 +205,111 @@ __device__ __forceinline__ float exp2_int(float x) { return __uint_as_float((uin
 // them finite values (others stay what they are in fp16).  By the K loader's warp,
 // which would come late to the next tile's keys if each round of loads took its way
 // to L2: the lines are asked for first (block of 512: 501 -> 487 us).
-// odd: whether it holds values that are not finite.
-template <int HD>
-__device__ __forceinline__ float own_scale(const CachedParams& p, const Piece* pp, int l, int lane, bool* odd = nullptr) {
+//
+// TREE: a row sees some of the tile's rows alone, and what the others hold must not
+// show.  One huge value among them would push all others out of fp16, and with its scale
+// in the scores the cached keys' weights too.  So that scale is taken where every row's largest
+// value lies within 2^(kOwnSpread + 1) of the tile's (told by the lanes' chunks of four columns: one
+// chunk that is large enough in all rows will do, nothing is joined over a row).  Else the
+// scale goes by the smallest chunk that is not zero, which comes to [1, 2) (the scale is 2^-48 to
+// 2^100, and 2^-8 at most where there are rows of zeros, which a row may see beside cached values alone;
+// fp16's smallest step is then 2^-72, as e4m3's of the cache's smallest scale), and values of 2^15 and more of
+// it stay outside the products, as those that are not finite do: add_outside gives them to the rows that
+// see them at the piece's end.  limit: the magnitude (bf16 bits) from which on they do; outside: whether
+// there are any.  U and U2 loads are in flight: the loader's 72 registers hold few (a scale for each key, which the
+// softmax adds to its scores, cost every tile 5 to 25 %).  Trees of 32 / 64 / 256 (as in the head) 80 / 270 / 278 us;
+// with a 16th of their rows zeros, or 2^8 times the others, 84 / 306 / 315; a 16th NaN or 1e30, half of
+// the rows seeing each, 133 / 461 / 467.
+constexpr int kOwnSpread = 4, kOutsideStep = 48;
+template <int HD, bool TREE, int U = TREE ? 4 : 8, int U2 = U>
+__device__ __forceinline__ float own_scale(const CachedParams& p, int64_t row0, int rows, int h, int l, int lane,
+                                           uint32_t* limit = nullptr, bool* outside = nullptr) {
   constexpr int PER = HD / 8, STEP = 32 / PER;  // lanes to a row, rows at a time
-  const int first = (pp->l0 + l) * kUnit, n = min(pp->rows - first, kUnit);
+  const int first = l * kUnit, n = min(rows - first, kUnit);
   const __nv_bfloat16* V =
-      static_cast<const __nv_bfloat16*>(p.V) + ((pp->row0 + first) * p.c.Hkv + pp->h) * HD + (lane % PER) * 8;
-  if (n > 16 * STEP)
+      static_cast<const __nv_bfloat16*>(p.V) + ((row0 + first) * p.c.Hkv + h) * HD + (lane % PER) * 8;
+  if (TREE || n > 16 * STEP)
     for (int r = lane; r < n; r += 32)
 #pragma unroll
       for (int x = 0; x < HD / 64; ++x)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(V - (lane % PER) * 8 + (int64_t)r * p.c.Hkv * HD + x * 64));
-  uint32_t m = 0, top = 0;
+  // (pairs: of even and of odd columns) the largest, and the smallest of the rows' chunks.  TREE: of all, at first
+  uint32_t m = 0, least = 0x7fff7fffu;
 #pragma unroll 1
-  for (int r0 = lane / PER; r0 < n; r0 += 8 * STEP) {  // (eight loads in flight)
-    uint4 w[8];
+  for (int r0 = lane / PER; r0 < n; r0 += U * STEP) {  // (U loads in flight)
+    uint4 w[U];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
+    for (int x = 0; x < U; ++x) {
       const int r = r0 + x * STEP;
       w[x] = r < n ? __ldg(reinterpret_cast<const uint4*>(V + (int64_t)r * p.c.Hkv * HD)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
+    for (int x = 0; x < U; ++x) {
       const uint32_t v[4] = {w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu, w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu};
+      if (TREE) {
+        const uint32_t z = __vmaxu2(__vmaxu2(v[0], v[1]), __vmaxu2(v[2], v[3]));
+        m = __vmaxu2(m, z);
+        if (r0 + x * STEP < n) least = __vminu2(least, z);
+      } else {
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        m = __vmaxu2(m, v[y] & __vcmpltu2(v[y], 0x7f807f80u));
-        if (odd) top = __vmaxu2(top, v[y]);
+        for (int y = 0; y < 4; ++y) m = __vmaxu2(m, v[y] & __vcmpltu2(v[y], 0x7f807f80u));
       }
     }
   }
-  if (odd) *odd = __any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= 0x7f80u);
   m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-  return (float)max((int)(m >> 7) - 127 - 8, -96);
+  if (TREE) {
+    auto together = [&]() {  // every row has a chunk that is not far below m
+      const unsigned large =
+          __ballot_sync(0xffffffffu, (max(least & 0xffffu, least >> 16) >> 7) + kOwnSpread >= (m >> 7));
+      bool all = true;
+#pragma unroll
+      for (int x = 0; x < STEP; ++x) all &= ((large >> (x * PER)) & ((1u << PER) - 1u)) != 0;
+      return all;
+    };
+    *limit = 0x7f80u;
+    *outside = m >= 0x7f80u;
+    if (*outside || !together()) {  // once more, finite values alone
+      const uint32_t top = m;
+      uint32_t some = 0x7fff7fffu;  // the smallest chunk that is not zero
+      bool zeros = false;           // a row of zeros
+      m = 0;
+      least = 0x7fff7fffu;
+#pragma unroll 1
+      for (int r0 = 0; r0 < n; r0 += U2 * STEP) {
+        uint4 w[U2];
+#pragma unroll
+        for (int x = 0; x < U2; ++x) {
+          const int r = r0 + x * STEP + lane / PER;
+          w[x] = r < n ? __ldg(reinterpret_cast<const uint4*>(V + (int64_t)r * p.c.Hkv * HD)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int x = 0; x < U2; ++x) {
+          const uint32_t v[4] = {w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu, w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu};
+          uint32_t z = 0;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) z = __vmaxu2(z, v[y] & __vcmpltu2(v[y], 0x7f807f80u));
+          m = __vmaxu2(m, z);
+          const unsigned any = __ballot_sync(0xffffffffu, z != 0) >> (lane / PER * PER) & ((1u << PER) - 1u);
+          if (r0 + x * STEP + lane / PER < n) {
+            least = __vminu2(least, z);
+            zeros |= any == 0;
+          }
+          some = __vminu2(some, z | (__vcmpeq2(z, 0u) & 0x7fff7fffu));
+        }
+      }
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      if (!together()) {
+        some = __reduce_min_sync(0xffffffffu, min(some & 0xffffu, some >> 16));
+        const int most = __any_sync(0xffffffffu, zeros) ? -8 : 100;
+        const int lv = min(max((int)(some >> 7) - 127, -kOutsideStep), most);
+        *limit = (uint32_t)(lv + 15 + 127) << 7;
+        *outside = top >= *limit;
+        return (float)lv;
+      }
+    }
+  }
+  // (TREE: references of parts that are joined stay within 2^100 of each other, kOutsideStep among it)
+  return (float)max((int)(m >> 7) - 127 - 8, TREE ? -kOutsideStep : -96);
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
@@ -319,11 +396,66 @@ __device__ __forceinline__ void store_p(uint32_t (&a)[32], uint32_t taddr) {
   tmem_st16(taddr, pk);
 }
 
+// (TREE) Adds 32 columns, from col on, of the own values that the products did not take, keys key0 to end,
+// to the rows that see them: those that are not finite as they are, others times their weight, exp2(s - M) f.
+// (L holds that weight too: where scores are so large that their rounding shows, it is L at most.)  By a warp, a
+// lane to a key first; rows that none of its rows sees cost no more than that look.
+template <int HD>
+__device__ __forceinline__ void add_outside(const CachedParams& p, int64_t row0, int key0, int end, int h, int64_t at, int head,
+                                            bool live, int col, uint32_t limit, float M, float L, float f, uint32_t (&o)[32]) {
+  const int lane = threadIdx.x & 31;
+  auto values = [&](int key) {
+    return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.V) + ((row0 + key) * p.c.Hkv + h) * HD + col);
+  };
+#pragma unroll 1
+  for (; key0 < end; key0 += 32) {
+    uint32_t top = 0;
+    if (key0 + lane < end) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint4 v = __ldg(values(key0 + lane) + x);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      }
+    }
+    unsigned out = __ballot_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= limit);
+    if (!out) continue;
+    const uint32_t sees = live && (key0 >> 5) < p.words ? __ldg(p.vis + at * p.words + (key0 >> 5)) : 0u;
+    for (out &= __reduce_or_sync(0xffffffffu, sees); out; out &= out - 1) {
+      const int key = key0 + __ffs(out) - 1;
+      if (!((sees >> (key - key0)) & 1)) continue;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.Q) + (at * p.Hq + head) * HD);
+      const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.K) + ((row0 + key) * p.c.Hkv + h) * HD);
+      float s = 0.f;
+#pragma unroll 4
+      for (int x = 0; x < HD / 8; ++x) {
+        const uint4 a = __ldg(q + x), b = __ldg(k + x);
+        s = fmaf(bf_lo(a.x), bf_lo(b.x), s); s = fmaf(bf_hi(a.x), bf_hi(b.x), s);
+        s = fmaf(bf_lo(a.y), bf_lo(b.y), s); s = fmaf(bf_hi(a.y), bf_hi(b.y), s);
+        s = fmaf(bf_lo(a.z), bf_lo(b.z), s); s = fmaf(bf_hi(a.z), bf_hi(b.z), s);
+        s = fmaf(bf_lo(a.w), bf_lo(b.w), s); s = fmaf(bf_hi(a.w), bf_hi(b.w), s);
+      }
+      const float weight = M == -INFINITY ? 0.f : fminf(ex2_approx(fmaf(s, p.sl2, -M)), L) * f;
+      auto add = [&](int c, uint32_t bits) {
+        const float v = __uint_as_float(bits << 16), y = __uint_as_float(o[c]);
+        if ((bits & 0x7fffu) >= limit) o[c] = __float_as_uint(isfinite(v) ? fmaf(weight, v, y) : y + v);
+      };
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint4 v = __ldg(values(key) + x);
+        add(8 * x, v.x & 0xffffu); add(8 * x + 1, v.x >> 16);
+        add(8 * x + 2, v.y & 0xffffu); add(8 * x + 3, v.y >> 16);
+        add(8 * x + 4, v.z & 0xffffu); add(8 * x + 5, v.z >> 16);
+        add(8 * x + 6, v.w & 0xffffu); add(8 * x + 7, v.w >> 16);
+      }
+    }
+  }
+}
+
 template <int HD, bool KS, bool FINE, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     bdlm_cached_tc_kernel(const __grid_constant__ CUtensorMap tK8, const __grid_constant__ CUtensorMap tK,
                           const __grid_constant__ CUtensorMap tV, const CachedParams p) {
-  using LY = Lay<HD>;
+  using LY = Lay<HD, TREE>;
   constexpr int KP = HD / 64;        // 64-column panels of a bf16 tile
   constexpr int SWQ = HD == 128 ? 2 : 4;
   constexpr uint32_t SBO8 = 8 * HD;  // bytes between 8-row groups of an e4m3 tile
@@ -340,8 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the rows' score factors
   float* row_cq = reinterpret_cast<float*>(bp + LY::kCQ);
   Piece* pieces = reinterpret_cast<Piece*>(bp + LY::kPC);
-  // (TREE, split) an own tile that sub-tile t took in this piece holds values that are not finite, [2]
+  // (TREE, split) an own tile that sub-tile t took in this piece holds values outside the products, [2]
   volatile int* own_odd = reinterpret_cast<volatile int*>(bp + LY::kBar + 8 * B_COUNT + 8);
+  uint32_t* own_limit = reinterpret_cast<uint32_t*>(bp + LY::kLim);  // (TREE) [NP][kLimits], 0: nothing outside
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -477,9 +610,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!isV) {
             KInfo& ki = kinfo[tc % NI];
             bool odd = false;
-            const float lv = own_scale<HD>(p, pp, l, lane, TREE ? &odd : nullptr);
+            uint32_t limit = 0;
+            const float lv = own_scale<HD, TREE, TREE ? 4 : 8, KS ? 4 : 1>(p, pp->row0, pp->rows, h, pp->l0 + l, lane, &limit, &odd);
             if (lane < 4) ki.s[0][lane] = 1.f, ki.iv[0][lane] = exp2_int(-lv) * kTcUnshift, ki.lv[0][lane] = lv;
-            if (lane == 0) ki.fine = 0, ki.gone = odd;  // (own tiles, TREE: values that are not finite)
+            if (lane == 0) ki.fine = 0, ki.gone = odd;
+            if (TREE && lane == 0) {
+              ki.s[1][0] = __uint_as_float(limit | limit << 16);                // (for the conversion)
+              if (KS) own_limit[np % NP * kLimits + l] = odd ? limit : 0u;      // (for the piece's end)
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(B_KI + tc % NI));
           }
@@ -883,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_sum = m_ref;
         summed = true;
       };
-      bool odd = false;  // (TREE) an own tile of this sub-tile holds values that are not finite
+      bool odd = false;  // (TREE) an own tile of this sub-tile holds values outside the products
       // keys left from the piece's first cached (own) tile on
       const int left_k = pp->len - pp->k0 * kUnit, left_l = pp->rows - pp->l0 * kUnit;
       for (int j = KS ? t : 0; j < n; j += KS ? 2 : 1, ++sc) {
@@ -1033,6 +1171,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const bool whole = pp->whole;
+      if (TREE && odd && !whole && L > 1.f) {  // (a partial result's largest value times its weight stays below 2^128)
+        M += kOutsideStep;
+        L *= exp2_int(-kOutsideStep);
+        w0 *= exp2_int(-kOutsideStep);
+        w1 *= exp2_int(-kOutsideStep);
+      }
       const float inv = whole ? (L != 0.f ? kTcUnshift / L : 0.f) : kTcUnshift;
       const Row r = my_row();
       const bool live = r.live;
@@ -1040,11 +1184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* slot = p.part + (2 * (int64_t)blockIdx.x + (pp->first ? 1 : 0)) * part_floats(kTileRows, HD);
       const int prow = (KS ? 0 : t * 128) + row;
       const int64_t oofs = (r.at * p.Hq + r.head) * HD;
-      // (TREE) the own rows of the piece, its sequence's first row and KV head
-      const int own0 = TREE ? pp->l0 * kUnit : 0, own1 = TREE ? min(pp->rows, (pp->l0 + nl) * kUnit) : 0;
-      const int64_t row0 = TREE ? pp->row0 : 0;
-      const int kvh = TREE ? pp->h : 0;
-      done(np);  // (the rest is in registers)
+      if (!TREE) done(np);  // (the rest is in registers)
       // split: sub-tile t's threads write columns HD / 2 t ..; both read both accumulators
       constexpr int kCols = KS ? HD / 2 : HD;
       const int col0 = KS ? t * (HD / 2) : 0;
@@ -1062,23 +1202,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 32; ++x)
             o[x] = __float_as_uint(fmaf(__uint_as_float(o1[x]), s1, __uint_as_float(o[x])));
         }
-        if (!live) continue;  // (nobody reads a partial result's rows without a token)
-        if (TREE && odd) {  // values that are not finite, to the rows that see them (the products took zeros)
+        if (TREE && odd) {  // what the products did not take, to the rows that see it
 #pragma unroll 1
-          for (int key = own0; key < own1; ++key) {
-            const int w = key >> 5;
-            if (w >= p.words || !((__ldg(p.vis + r.at * p.words + w) >> (key & 31)) & 1)) continue;
-            const uint32_t* V = reinterpret_cast<const uint32_t*>(
-                static_cast<const __nv_bfloat16*>(p.V) + ((row0 + key) * p.c.Hkv + kvh) * HD + col);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const uint32_t v = __ldg(V + x);
-              const float lo = __uint_as_float(v << 16), hi = __uint_as_float(v & 0xffff0000u);
-              if (!isfinite(lo)) o[2 * x] = __float_as_uint(__uint_as_float(o[2 * x]) + lo);
-              if (!isfinite(hi)) o[2 * x + 1] = __float_as_uint(__uint_as_float(o[2 * x + 1]) + hi);
+          for (int l = 0; l < nl; ++l) {
+            const int l1 = pp->l0 + l;
+            uint32_t limit;
+            if (KS) {
+              limit = own_limit[np % NP * kLimits + l];
+            } else {  // (as the loader found it: any number of tiles)
+              bool any;
+              own_scale<HD, true, 4>(p, pp->row0, pp->rows, pp->h, l1, lane, &limit, &any);
+              if (!any) limit = 0;
             }
+            if (limit != 0)
+              add_outside<HD>(p, pp->row0, l1 * kUnit, min((l1 + 1) * kUnit, pp->rows), pp->h, r.at, r.head, live, col, limit, M,
+                              L, whole ? 1.f / L : 1.f, o);
           }
         }
+        if (!live) continue;  // (nobody reads a partial result's rows without a token)
         if (!whole) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
@@ -1103,6 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (TREE) done(np);
       tc_fence_before();
       if (n > 0) {
         if (KS) {
@@ -1174,14 +1316,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // belong to others: zero)
           const bool mine = i < left_l - (j - nk) * kUnit;
           const float f = exp2_int(-kinfo[w % NI].lv[0][0]);
+          const uint32_t limit = TREE ? __float_as_uint(kinfo[w % NI].s[1][0]) : 0u;
 #pragma unroll 2
           for (int x = 0; x < HD / 8; ++x) {
             const uint32_t at = dst + (x >> 3) * kSlot + i * 128 + (((x ^ i) & 7) << 4);
             const uint4 v = ld_shared_v4(at);
             uint32_t b[4] = {v.x, v.y, v.z, v.w};
-            if (TREE)  // (what is not finite reaches its rows at the piece's end)
+            if (TREE)  // (what does not enter the products reaches its rows at the piece's end)
 #pragma unroll
-              for (int y = 0; y < 4; ++y) b[y] &= __vcmpltu2(b[y] & 0x7fff7fffu, 0x7f807f80u);
+              for (int y = 0; y < 4; ++y) b[y] &= __vcmpltu2(b[y] & 0x7fff7fffu, limit);
             uint32_t h[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
@@ -1216,9 +1359,9 @@ cudaError_t launch(const CachedMaps& m, const CachedParams& p, cudaStream_t st) 
   }();
   if (ready != cudaSuccess) return ready;
   static std::atomic<uint64_t> raised{0};
-  const cudaError_t e = raise_smem(reinterpret_cast<const void*>(k), Lay<HD>::kAlloc, raised);
+  const cudaError_t e = raise_smem(reinterpret_cast<const void*>(k), Lay<HD, TREE>::kAlloc, raised);
   if (e != cudaSuccess) return e;
-  k<<<p.G, kThreads, Lay<HD>::kAlloc, st>>>(m.k8, m.k, m.v, p);
+  k<<<p.G, kThreads, Lay<HD, TREE>::kAlloc, st>>>(m.k8, m.k, m.v, p);
   return cudaGetLastError();
 }
 

@@ -107,10 +107,16 @@ constexpr double kOne = 4611686018427387904.0;  // 2^62: the whole numbers' unit
 struct Wide {
   float s, e;
 };
-// In units of 2^-62, what is below cut off.
+// In units of 2^-62, what is below cut off.  A single value, at most 1:
 __device__ __forceinline__ uint64_t fixed(Wide x) {
   constexpr float k = 4611686018427387904.f;
   return (uint64_t)(__float2ll_rz(x.s * k) + __float2ll_rz(x.e * k));
+}
+// A lane's sum, below 4, where a signed number ends at 2: 2 of it are set as a bit.
+__device__ __forceinline__ uint64_t fixed_sum(Wide x) {
+  const bool top = x.s >= 2.f;
+  if (top) x.s -= 2.f;
+  return fixed(x) + (top ? 1ull << 63 : 0ull);
 }
 // sum += x, both parts of every rounding kept.
 __device__ __forceinline__ void add(Wide& sum, Wide x) {
@@ -224,7 +230,7 @@ __device__ __forceinline__ void sum_run(const PassRow& w, int v0, int v1, uint64
         add(x[u], residual<KIND>(Probs<T>::value(a[u], y), KIND == kPlain ? 0.f : Probs<T>::value(b[u], y), w));
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) sum[u] = fixed(x[u]);
+  for (int u = 0; u < 4; ++u) sum[u] = fixed_sum(x[u]);
 }
 
 // What the walk holds of a sequence's rows, and where it stands.

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kCommitThreads, 8) bdlm_cache_commit_kernel(co
   int rows = __ldg(p.accepted + s);
   const SeqView v = seq_view(c, p.r, s, bad);
   if (rows < 0 || rows > p.max_path) bad |= kStatusBadTree;
-  if (bad) rows = 0;
+  if (bad & 0xff & (kStatusBadTree | kStatusBadRows)) rows = 0;  // (a length out of range is cut, as in the append)
   const int64_t cap = (int64_t)c.max_pages << c.lp;
   if (v.len + (int64_t)rows > cap) {
     bad |= kStatusBadLen;

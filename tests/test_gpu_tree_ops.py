@@ -1,12 +1,14 @@
-"""Verification of drafted trees whose probabilities add up to more than a distribution's, on the GPU against
-the fp64 oracle.  Everything compared is whole numbers: equal."""
+"""Verification of drafted trees whose probabilities add up to more than a distribution's, and commits on
+lengths out of range, on the GPU against the fp64 oracle.  Everything compared is whole numbers: equal."""
 from __future__ import annotations
 
 import numpy as np
 import pytest
 
+from tests.cache_util import device_cache, host_codes, make_cache, make_rows
+from tests.parity_util import to_dev
 from tests.test_gpu_cache import lib  # noqa: F401
-from tests.test_gpu_tree import run_verify
+from tests.test_gpu_tree import DEV, run_verify
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -43,3 +45,29 @@ def test_verify_every_token_of_large_sums_can_be_drawn(lib, drawn):
     s = (torch.arange(7, device="cuda") + 0.5) / 7
     path, acc, tok = lib.bdlm_tree_verify(i - 1, i, p, q, s, s)
     assert acc.tolist() == [1] * 7 and tok.tolist() == [0, 0, 1, 1, 2, 2, 3]
+
+
+@pytest.mark.parametrize("lens", [[-1, 9], [9, -2 ** 31], [9, 49], [2 ** 31 - 1, 0]])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 128)])
+def test_commit_treats_lengths_out_of_range_as_the_append_does(lib, lens, d, page):
+    """A negative length counts as 0, one behind the page table as the table's end; the call reports it."""
+    m = lib
+    c, _ = make_cache([9, 9], 40, 2, d, page, seed=5)
+    K, V = (to_dev(make_rows(10, 2, d, s), torch) for s in (1, 2))
+    made = []
+    for commit in (False, True):
+        cache = device_cache(m, torch, c)
+        cache.lens.copy_(torch.tensor([min(x, 2 ** 31 - 1) if x != 49 else -(-40 // page) * page + 1 for x in lens],
+                                      dtype=torch.int32))
+        ws = m.bdlm_cache_workspace(cache)
+        if commit:
+            path = DEV(np.tile(np.arange(5, dtype=np.int32), (2, 1)))
+            out = m.bdlm_cache_commit(cache, K, V, path, DEV(np.asarray([5, 5], np.int32)), workspace=ws)
+        else:
+            out = m.bdlm_cache_append(cache, K, V, workspace=ws)
+        with pytest.raises(m.BdlmError, match="length"):
+            m.bdlm_sync_status(ws)
+        made.append([out.cpu().numpy()] + [host_codes(getattr(cache, w + "8")) for w in "kv"]
+                    + [getattr(cache, w + "_scale").cpu().numpy() for w in "kv"])
+    for a, b in zip(*made):
+        np.testing.assert_array_equal(a, b)

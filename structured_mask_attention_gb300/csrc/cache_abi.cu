@@ -495,6 +495,8 @@ bdlm_status bdlm_tree_verify(const int32_t* parents, const int32_t* tokens, cons
       if (x.stride < V || x.stride > (int64_t)1 << 40)
         return abi_fail(BDLM_ERR_SHAPE, "%s's rows are %lld values apart, at least V=%lld are needed", x.name,
                         (long long)x.stride, (long long)V);
+      if (rows > 1 && x.stride > ((int64_t)1 << 58) / rows)  // (their bytes are counted in 64 bits below)
+        return abi_fail(BDLM_ERR_SHAPE, "%s's rows end past 2^58 values", x.name);
     }
     if (rows > 0) {
       CACHE_CHECK(check_ptr("parents", parents, 4));

@@ -434,7 +434,9 @@ bdlm_status bdlm_cache_append(const void* K, const void* V, const bdlm_cache* ca
  * key's weight times value scale meets its codes off by at most 2^-11 of itself
  * and 2^-34 of the row's largest (an fp32 output: 2^-22 and 2^-34), own values
  * counting as codes of up to 448 with a scale for each 128 rows; the row sum and
- * LSE take the weights in fp32.  (Value scales that a row sees may differ by 2^100.)
+ * LSE take the weights in fp32.  (Value scales that a row sees may differ by 2^100.  With
+ * up to 32 rows times heads of a group, own values that a row sees stay below 2^107: sums of
+ * larger ones may pass fp32's end.)
  * Scores are fp32 sums of products with the queries as they are, or, for more
  * than 32 rows times heads of a group and in bdlm_cache_weights, with queries
  * whose elements below 2^-13 of the row's largest are off by up to 2^-21 of it.

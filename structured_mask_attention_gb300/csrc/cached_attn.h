@@ -36,7 +36,7 @@ __host__ __device__ inline int64_t part_floats(int tile_rows, int d) { return (i
 // Rows up to which the mma.sync kernels take a call.  16 sequences of up to 16384
 // tokens with 20 / 32 rows: 108 / 108 us here, 128 / 127 in the tcgen05 kernel (in a
 // graph, warm); 64 rows (16 sequences of up to 8192): 118 us with tiles of 64 rows
-// here, when it was tried, 83 there (trees in two tiles of 32 of tree_small.cu 92).
+// here, when it was tried, 83 there (trees: 92 in two tiles of 32 of tree_small.cu, 80 there).
 constexpr int kSmallRows = 32;
 constexpr int kSmallCtasPerSm = 2;  // its resident CTAs
 // Weights are kept in fp16, 2^shift larger than exp2(s - reference): the largest
@@ -64,10 +64,10 @@ inline int cached_tile_rows(int64_t flat) {
   return flat <= 16 ? 16 : flat <= kSmallRows ? 32 : flat <= 128 ? 128 : 256;
 }
 // Trees: 257 to 384 rows go in three tiles of 128; of pairs' two tiles the second would be at
-// most half full (8 sequences of 16384, 5 heads to a KV head, 260 / 320 / 380 rows: 249 / 253 /
-// 258 us in three tiles, 278 / 281 / 286 in two of 256; one of 131072, 300 rows: 220 / 267; 16 of
-// 500: 70 / 73.  160 to 250 rows in tiles of 128: 174 to 181, in one of 256 165 to 169; 450 rows
-// 342 / 297).
+// most half full (8 sequences of up to 16384, one without rows, 5 heads to a KV head, 260 / 320 / 380
+// rows: 137 / 139 / 155 us in three tiles, 157 / 160 / 171 in two of 256; one of 131072, 300 rows: 223 / 275; 16 of
+// up to 500: 50 / 56.  450 rows: 176 in four, 173 in two.  160 / 250 rows: 97 / 105 in two, 108 / 112 in one of
+// 256, which these still take).
 inline int tree_tile_rows(int64_t flat) { return flat > 256 && flat <= 384 ? 128 : cached_tile_rows(flat); }
 inline int64_t fine_floats(int tile_rows, int d) { return tile_rows > kSmallRows ? (int64_t)2 * 128 * d : 0; }
 inline int cached_ctas(int tile_rows, int sms) { return tile_rows <= kSmallRows ? sms * kSmallCtasPerSm : sms; }
@@ -87,7 +87,7 @@ constexpr int kWholeKeys = 1024;
 // AttnSplit::extra: what a segment costs beside its units, in units.  The
 // mma.sync kernel spends about 6000 cycles to begin and end a segment, 5000 more
 // on its own rows' keys and 2300 on a unit: with 1 / 3 / 5, the token batch of
-// cached_small.cuh took 220 / 207 / 205 us with own keys and 205 / 204 / 206 without,
+// cached_small.cu took 220 / 207 / 205 us with own keys and 205 / 204 / 206 without,
 // blocks of 8 over 16 short sequences 70 / 47 / 42 and 48 / 40 / 41.  The tcgen05
 // kernels spend 10 to 20 thousand cycles to end a segment and begin the next, and
 // 2000 (split) or 4000 (pairs) on a unit: with 0 / 6, when it was tried, blocks of 32 and 128 took 130 / 106 and 293 /

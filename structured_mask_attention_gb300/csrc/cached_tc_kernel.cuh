@@ -56,10 +56,12 @@
 // Trees (in a graph, warm; 16 / 8 heads but for the second): 32 rows behind each of 16
 // sequences of 8192 at most 80 us, 64 behind each of 8 of 32768, 40 / 8 heads, 270 (three
 // tiles of 128), 256 behind one of 131072 278 us, 1.0 PFLOP/s.  By the issuing thread's clock a
-// unit of 128 keys and 128 rows (split) takes it 1400 cycles for 16 products and their
-// commits, 200 for its waits and 700 in which the softmax is not through.
-// Registers: ptxas reports 60 to 176 bytes of spills in the bf16 instances and 208
-// to 420 in the fp32 ones.
+// unit of 128 keys and 128 rows (split; when that tree of 64 took 284) takes 2300 cycles: 1400 go by while 16 products
+// and their commits are issued, 1300 of which the tensor cores need for them at the measured rate,
+// 200 in its waits, and in 700 neither sub-tile's softmax is through (S of a sub-tile's next tile goes where
+// P of this one lies, so its scores, softmax and P V follow each other).
+// Registers: ptxas reports 60 to 188 bytes of spills in the bf16 instances and 208
+// to 428 in the fp32 ones.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

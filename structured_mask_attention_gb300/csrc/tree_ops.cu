@@ -98,7 +98,9 @@ __global__ void __launch_bounds__(kMaskThreads) bdlm_tree_mask_kernel(const Tree
 // 64 trees of 16 rows drawn with up to 3 children, V = 131072 in fp32 (66 MB, more for
 // 2nd and 3rd passes): 39 us, the last sequences 3 passes; 16 trees of 64 chosen rows, V
 // = 100003 in bf16: 16 us; one chain of 8, V = 32000: 10 us.  CTAs of 512 / 256 / 128
-// threads: 48 / 39 / 41 us; up to 2 / 4 CTAs for each SM: 41 / 39.
+// threads: 48 / 39 / 41 us; up to 2 / 4 CTAs for each SM: 41 / 39 (80 registers leave room for three:
+// of 512 CTAs 456 are resident, at least 7 of 64 clusters begin when others have ended; a sequence that ends
+// early leaves its place).
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;
 constexpr double kOne = 4611686018427387904.0;  // 2^62: the whole numbers' unit

@@ -222,7 +222,7 @@ __device__ __forceinline__ float exp2_int(float x) { return __uint_as_float((uin
 // softmax adds to its scores, cost every tile 5 to 25 %).  Trees of 32 / 64 / 256 (as in the head) 80 / 270 / 278 us;
 // with a 16th of their rows zeros, or 2^8 times the others, 84 / 306 / 315; a 16th NaN or 1e30, half of
 // the rows seeing each, 133 / 461 / 467.
-constexpr int kOwnSpread = 4, kOutsideStep = 48;
+constexpr int kOwnSpread = 4, kOwnLeast = -48;
 template <int HD, bool TREE, int U = TREE ? 4 : 8, int U2 = U>
 __device__ __forceinline__ float own_scale(const CachedParams& p, int64_t row0, int rows, int h, int l, int lane,
                                            uint32_t* limit = nullptr, bool* outside = nullptr) {
@@ -303,15 +303,15 @@ __device__ __forceinline__ float own_scale(const CachedParams& p, int64_t row0, 
       if (!together()) {
         some = __reduce_min_sync(0xffffffffu, min(some & 0xffffu, some >> 16));
         const int most = __any_sync(0xffffffffu, zeros) ? -8 : 100;
-        const int lv = min(max((int)(some >> 7) - 127, -kOutsideStep), most);
+        const int lv = min(max((int)(some >> 7) - 127, kOwnLeast), most);
         *limit = (uint32_t)(lv + 15 + 127) << 7;
         *outside = top >= *limit;
         return (float)lv;
       }
     }
   }
-  // (TREE: references of parts that are joined stay within 2^100 of each other, kOutsideStep among it)
-  return (float)max((int)(m >> 7) - 127 - 8, TREE ? -kOutsideStep : -96);
+  // (TREE: not below the other scale's least, so that the references of own tiles lie near each other)
+  return (float)max((int)(m >> 7) - 127 - 8, TREE ? kOwnLeast : -96);
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
@@ -1173,11 +1173,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const bool whole = pp->whole;
-      if (TREE && odd && !whole && L > 1.f) {  // (a partial result's largest value times its weight stays below 2^128)
-        M += kOutsideStep;
-        L *= exp2_int(-kOutsideStep);
-        w0 *= exp2_int(-kOutsideStep);
-        w1 *= exp2_int(-kOutsideStep);
+      if (TREE && odd && !whole && L > 1.f) {
+        // a partial result's largest value times its weight, which is L at most, has to stay below 2^128: the
+        // reference rises by log2 L, to the row's own, whatever the scales
+        const float up = (float)min((int)(__float_as_uint(L) >> 23) - 126, 120), down = exp2_int(-up);
+        M += up;
+        L *= down;
+        w0 *= down;
+        w1 *= down;
       }
       const float inv = whole ? (L != 0.f ? kTcUnshift / L : 0.f) : kTcUnshift;
       const Row r = my_row();

@@ -108,3 +108,21 @@ def test_values_of_zero_count_in_the_row_sum(lib, g, rows, Hkv, size, d, o_dtype
     sees = random_bits(rows, 3)
     ref = plain_attn(torch, *(x[i] for i in (0, 2, 3, 4)), sees, x[1], 1 / math.sqrt(d))
     check(lib, x, sees, ref, d, o_dtype)
+
+
+@pytest.mark.parametrize("g,rows,Hkv", SHAPES)
+@pytest.mark.parametrize("d,o_dtype", TYPES)
+@pytest.mark.parametrize("value", [math.nan, 1e30])
+def test_cached_values_far_below_own_ones_keep_their_weights(lib, g, rows, Hkv, d, o_dtype, value):
+    """Cached values of 2^-70, own ones of 2^10, beside hidden rows of NaN or 1e30: the scales that a row sees differ by
+    less than 2^100, and the cached keys' weights, most of the sum, count in it."""
+    x = batch([1700, 300], rows, g, Hkv, d, 64, 8)
+    x[0]["vs"] *= np.float32(2.0 ** -70)
+    x[4][:] *= np.float32(2.0 ** 10)
+    sees = [see | np.eye(len(see), dtype=bool) for see in random_bits(rows, 7)]
+    for see in sees:
+        see[:, 1::3] = False
+    ref = plain_attn(torch, *(x[i] for i in (0, 2, 3, 4)), sees, x[1], 1 / math.sqrt(d))
+    for s in range(2):
+        x[4][x[1][s]:x[1][s + 1]][1::3] = value
+    check(lib, x, sees, ref, d, o_dtype)
